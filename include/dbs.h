@@ -340,6 +340,189 @@ const char *dbs_status_string(dbs_status s);
  */
 dbs_status dbs_probe_read(const void *buf, int64_t bytes, uint32_t *sink, uint32_t never, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The layers and steps of a decoded token around the sparse products: 4-bit
+ * weights, logits, rotary positions.  Vectors of several tokens are rows
+ * [token][element] whose row stride is given in elements; `*_dtype` is
+ * DBS_F32 or DBS_BF16.  The calls allocate nothing and use no scratch, so
+ * they may run on several streams at once and be captured into a graph; they
+ * run on the current device, which must hold all their buffers.  No output
+ * may overlap an input, except where stated.
+ * ------------------------------------------------------------------------ */
+typedef struct dbs_q4_matrix *dbs_q4_handle; /* opaque */
+
+/* tokens of one call at most */
+#define DBS_Q4_MAX_TOKENS 524288
+
+/*
+ * dbs_q4_build — lay out an m x n matrix held in 4 bits with group scales:
+ *
+ *   W_ij = scale[i][j / group] * (code_ij - zero[i][j / group])
+ *
+ *   group       32, 64 or 128 columns (the last group of a row may be cut)
+ *   codes       device uint8[m][ceil(n/2)]: code of an even column in the low
+ *               nibble, of the odd column after it in the high one
+ *   scales      device [m][ceil(n/group)], float (DBS_F32) or bf16 (DBS_BF16)
+ *   zeros       device uint8[m][ceil(n/group)], each at most 15, or NULL: 8
+ *   stream      the call is SYNCHRONOUS on it (it reads a check flag back)
+ *   out         receives the new handle; untouched on error
+ *
+ * The inputs may be freed once the call returns.  A zero point above 15 gives
+ * DBS_ERR_INVALID_ARG.  Handles are read only after the build: calls on one
+ * handle may overlap in time.
+ */
+dbs_status dbs_q4_build(int32_t m, int32_t n, int32_t group, const uint8_t *codes, const void *scales,
+                        dbs_dtype scale_dtype, const uint8_t *zeros, void *stream, dbs_q4_handle *out);
+
+/* Device bytes that the handle holds. */
+dbs_status dbs_q4_bytes(dbs_q4_handle A, int64_t *bytes);
+
+/* Releases the handle (waits for the device).  NULL is accepted. */
+dbs_status dbs_q4_free(dbs_q4_handle A);
+
+/*
+ * dbs_q4_product — y_t = W x_t for `tokens` vectors, fp32 accumulation, one
+ * rounding to y's type.
+ *
+ *   tokens   0 <= tokens <= DBS_Q4_MAX_TOKENS.  One call reads the weights once per 64
+ *            tokens
+ *   x        device [tokens][n], row stride ldx >= n elements
+ *   y        device [tokens][m], row stride ldy >= m elements
+ *
+ * Infinities and NaN in x or the scales spread as in the formula, to the
+ * tokens and rows whose sums hold them.
+ */
+dbs_status dbs_q4_product(dbs_q4_handle A, int32_t tokens, const void *x, dbs_dtype x_dtype, int64_t ldx,
+                          void *y, dbs_dtype y_dtype, int64_t ldy, void *stream);
+
+/*
+ * dbs_q4_product_masked — the same where token t wants only the rows i whose
+ * bit i % 32 of row_mask[t][i / 32] is set (a grammar's allowed tokens at the
+ * head): y_ti = fill elsewhere, whatever x holds.  16-row blocks that no
+ * token of a block of tokens wants are not read.  Bits at m and above are
+ * ignored.
+ *
+ *   row_mask   device uint32[tokens][ceil(m/32)], row stride ldmask words
+ *   fill       any float, -INFINITY for logits
+ */
+dbs_status dbs_q4_product_masked(dbs_q4_handle A, int32_t tokens, const void *x, dbs_dtype x_dtype,
+                                 int64_t ldx, const uint32_t *row_mask, int64_t ldmask, float fill, void *y,
+                                 dbs_dtype y_dtype, int64_t ldy, void *stream);
+
+/* activations of dbs_q4_gated: g / (1 + exp(-g)); g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)));
+ * max(g, 0) (whose zeros a following dbs_spmspv_dense skips) */
+typedef enum { DBS_ACT_SILU = 0, DBS_ACT_GELU_TANH = 1, DBS_ACT_RELU = 2 } dbs_activation;
+
+/*
+ * dbs_q4_gated — y_t = act(G x_t) * (U x_t), elementwise: the gate and up
+ * layers in one pass, products and activation in fp32, one rounding to y's
+ * type.  G and U have the same m, n, group and scale type (one handle may be
+ * given twice).  Arguments as for dbs_q4_product.
+ */
+dbs_status dbs_q4_gated(dbs_q4_handle G, dbs_q4_handle U, dbs_activation act, int32_t tokens, const void *x,
+                        dbs_dtype x_dtype, int64_t ldx, void *y, dbs_dtype y_dtype, int64_t ldy,
+                        void *stream);
+
+/* rows of one dbs_logits_adjust call at most */
+#define DBS_LOGITS_MAX_ROWS 65535
+
+/*
+ * dbs_logits_adjust — penalties, biases and a mask on rows of logits, in fp32
+ * with one rounding to the output's type.  Per row b and token v, in order:
+ *
+ *   1. v anywhere in the row's history:  l = l > 0 ? l / repetition : l * repetition
+ *   2. l -= frequency * c, and l -= presence if c > 0, where c counts v among
+ *      the history's entries from hist_new[b] on (the generated ones)
+ *   3. l += the row's bias of v (of several entries of one v the last counts)
+ *   4. mask bit v % 32 of mask[b][v / 32] clear:  l = -inf, whatever l was
+ *
+ * Every step whose pointer is NULL is left out.  Ids outside [0, vocab)
+ * contribute nothing, and the lists' pointers are clamped to the lists, so
+ * bad ones are memory-safe.  A row whose mask is empty is -inf throughout.
+ */
+typedef struct {
+  const int32_t *hist_ptr;   /* device int32[rows+1]: row b's history is hist[hist_ptr[b] .. hist_ptr[b+1]) */
+  const int32_t *hist;       /* device int32[hist_len] token ids */
+  int64_t hist_len;
+  const int32_t *hist_new;   /* device int32[rows], positions within the row's history; NULL: 0 */
+  const float *repetition;   /* device float[rows], > 0 */
+  const float *frequency;    /* device float[rows] */
+  const float *presence;     /* device float[rows] */
+  const int32_t *bias_ptr;   /* device int32[rows+1] */
+  const int32_t *bias_idx;   /* device int32[bias_len] token ids */
+  const float *bias_val;     /* device float[bias_len] */
+  int64_t bias_len;
+  const uint32_t *mask;      /* device uint32[rows][ceil(vocab/32)], row stride ldmask words */
+  int64_t ldmask;
+} dbs_logits_params;
+
+/*
+ *   rows, vocab   0 <= rows <= DBS_LOGITS_MAX_ROWS, vocab >= 1
+ *   logits        device [rows][vocab], row stride ld_in >= vocab
+ *   out           device [rows][vocab], row stride ld_out >= vocab; may be `logits` itself (same
+ *                 type and stride)
+ * hist_ptr and hist go together, as do bias_ptr, bias_idx and bias_val;
+ * repetition, frequency, presence or hist_new without a history is
+ * DBS_ERR_INVALID_ARG.
+ */
+dbs_status dbs_logits_adjust(int32_t rows, int32_t vocab, const void *logits, dbs_dtype in_dtype, int64_t ld_in,
+                             const dbs_logits_params *params, void *out, dbs_dtype out_dtype, int64_t ld_out,
+                             void *stream);
+
+/* pairs of a rotated head: element i with i + rot_dim/2, or 2i with 2i + 1 */
+typedef enum { DBS_ROPE_HALF = 0, DBS_ROPE_INTERLEAVED = 1 } dbs_rope_layout;
+
+/* largest rot_dim */
+#define DBS_ROPE_MAX_DIM 1024
+
+/*
+ * dbs_rope — rotary positions: in each head of each token, pair i (a, b) of
+ * the first rot_dim elements becomes
+ *
+ *   (scale (a cos p - b sin p), scale (a sin p + b cos p)),  p = pos[token] * freq[i]
+ *
+ * and the elements from rot_dim on are copied.  p is formed and reduced in
+ * 64 bits, so far positions keep their phase.
+ *
+ *   tokens, heads  >= 0;  head_dim >= 1;  rot_dim even, 0 <= rot_dim <= head_dim
+ *   pos            device int32[tokens]; a negative position marks padding: the token's
+ *                  rows of `out` are left as they are
+ *   freq           device double[rot_dim/2], radians per position (dbs_rope_frequencies)
+ *   inverse        nonzero: rotate by -p (undoes a rotation; the gradient with respect to x
+ *                  is this rotation of the output's gradient)
+ *   x, out         device, element (t, h, d) at t * token stride + h * head stride + d;
+ *                  `out` may be `x` itself (same type and strides), else they do not overlap
+ */
+dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, int32_t rot_dim, dbs_rope_layout layout,
+                    const int32_t *pos, const double *freq, float scale, int32_t inverse, const void *x,
+                    dbs_dtype x_dtype, int64_t x_token_stride, int64_t x_head_stride, void *out,
+                    dbs_dtype out_dtype, int64_t out_token_stride, int64_t out_head_stride, void *stream);
+
+/* How frequencies f_i = base^(-2i/rot_dim) are scaled for contexts longer than the model's own. */
+typedef enum {
+  DBS_ROPE_PLAIN = 0,   /* not at all */
+  DBS_ROPE_LINEAR = 1,  /* f / factor */
+  DBS_ROPE_BASE = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+  DBS_ROPE_BANDS = 3,   /* by the turns t = context * f / (2 pi) that pair i makes over the model's own
+                           context: t < low: f / factor; t > high: f; between them f ((1 - w) / factor + w),
+                           w = (t - low) / (high - low) */
+  DBS_ROPE_RAMP = 4     /* by pair index: f up to pair floor(d(high)), f / factor from pair ceil(d(low)),
+                           a linear ramp between, d(t) = rot_dim ln(context / (2 pi t)) / (2 ln base);
+                           *scale = 0.1 ln(factor) + 1 */
+} dbs_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim;   /* even, 2 <= rot_dim <= DBS_ROPE_MAX_DIM */
+  int32_t scaling;   /* a dbs_rope_scaling */
+  double base;       /* > 1 */
+  double factor;     /* >= 1, all but PLAIN */
+  double low, high;  /* 0 < low < high, BANDS and RAMP */
+  double context;    /* > 0, BANDS and RAMP: positions of the model's own context */
+} dbs_rope_options;
+
+/* Fills freq[rot_dim/2] (HOST memory) and *scale (may be NULL; 1 but for RAMP).  Touches no device. */
+dbs_status dbs_rope_frequencies(const dbs_rope_options *opt, double *freq, float *scale);
+
 #ifdef __cplusplus
 }
 #endif

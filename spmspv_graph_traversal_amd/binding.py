@@ -28,6 +28,11 @@ DBS_TILE_COO, DBS_TILE_DENSE, DBS_TILE_FORCE_CSR, DBS_TILE_FORCE_CSC, DBS_TILE_C
 DBS_OPT_PATH, DBS_OPT_TH3_NUM, DBS_OPT_TH3_DEN = 0, 1, 2
 DBS_OPT_LOCAL_PUSH_CUTOFF, DBS_OPT_TIMING, DBS_OPT_CHECK = 3, 4, 5
 DBS_OPT_PULL_WIDTH, DBS_OPT_PULL_SHARE = 6, 7
+# activations, rotary layouts and frequency scalings, limits
+DBS_ACT_SILU, DBS_ACT_GELU_TANH, DBS_ACT_RELU = 0, 1, 2
+DBS_ROPE_HALF, DBS_ROPE_INTERLEAVED = 0, 1
+DBS_ROPE_PLAIN, DBS_ROPE_LINEAR, DBS_ROPE_BASE, DBS_ROPE_BANDS, DBS_ROPE_RAMP = 0, 1, 2, 3, 4
+DBS_Q4_MAX_TOKENS, DBS_LOGITS_MAX_ROWS, DBS_ROPE_MAX_DIM = 524288, 65535, 1024
 # exported arrays
 (DBS_ARR_RB_PTR, DBS_ARR_T_CB, DBS_ARR_T_META, DBS_ARR_CB_PTR, DBS_ARR_CSC_RB, DBS_ARR_CSC2CSR,
  DBS_ARR_PAYLOAD, DBS_ARR_SEGMENTS, DBS_ARR_XMASK, DBS_ARR_ACTIVE, DBS_ARR_CSC_CM, DBS_ARR_PAT_SEGS,
@@ -63,10 +68,24 @@ class dbs_stats(C.Structure):
     ]
 
 
+class dbs_logits_params(C.Structure):
+    _fields_ = [("hist_ptr", C.c_void_p), ("hist", C.c_void_p), ("hist_len", C.c_int64), ("hist_new", C.c_void_p),
+                ("repetition", C.c_void_p), ("frequency", C.c_void_p), ("presence", C.c_void_p),
+                ("bias_ptr", C.c_void_p), ("bias_idx", C.c_void_p), ("bias_val", C.c_void_p), ("bias_len", C.c_int64),
+                ("mask", C.c_void_p), ("ldmask", C.c_int64)]
+
+
+class dbs_rope_options(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("scaling", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+                ("low", C.c_double), ("high", C.c_double), ("context", C.c_double)]
+
+
 EXPORTED = ["dbs_build_options_default", "dbs_build", "dbs_spmspv", "dbs_spmspv_dense",
             "dbs_spmspv_dense_threshold", "dbs_bfs", "dbs_bfs_noalloc",
             "dbs_set_option", "dbs_get_option", "dbs_get_stats", "dbs_copy_array", "dbs_free",
-            "dbs_status_string", "dbs_probe_read"]
+            "dbs_status_string", "dbs_probe_read",
+            "dbs_q4_build", "dbs_q4_bytes", "dbs_q4_free", "dbs_q4_product", "dbs_q4_product_masked", "dbs_q4_gated",
+            "dbs_logits_adjust", "dbs_rope", "dbs_rope_frequencies"]
 
 
 def load_library(path: str = LIB_PATH) -> C.CDLL:
@@ -96,6 +115,16 @@ def load_library(path: str = LIB_PATH) -> C.CDLL:
         "dbs_copy_array": [vp, i32, vp, i64, C.POINTER(i64)],
         "dbs_free": [vp],
         "dbs_probe_read": [vp, i64, vp, C.c_uint32, vp],
+        "dbs_q4_build": [i32, i32, i32, vp, vp, C.c_int, vp, vp, C.POINTER(vp)],
+        "dbs_q4_bytes": [vp, C.POINTER(i64)],
+        "dbs_q4_free": [vp],
+        "dbs_q4_product": [vp, i32, vp, C.c_int, i64, vp, C.c_int, i64, vp],
+        "dbs_q4_product_masked": [vp, i32, vp, C.c_int, i64, vp, i64, C.c_float, vp, C.c_int, i64, vp],
+        "dbs_q4_gated": [vp, vp, C.c_int, i32, vp, C.c_int, i64, vp, C.c_int, i64, vp],
+        "dbs_logits_adjust": [i32, i32, vp, C.c_int, i64, C.POINTER(dbs_logits_params), vp, C.c_int, i64, vp],
+        "dbs_rope": [i32, i32, i32, i32, C.c_int, vp, vp, C.c_float, i32, vp, C.c_int, i64, i64, vp, C.c_int, i64,
+                     i64, vp],
+        "dbs_rope_frequencies": [C.POINTER(dbs_rope_options), C.POINTER(C.c_double), C.POINTER(C.c_float)],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -306,3 +335,247 @@ def dbs_free(A: Matrix) -> None:
     if A.handle is not None and A.handle.value:
         _check(_lib.dbs_free(A.handle), "dbs_free")
         A.handle = C.c_void_p()
+
+
+# ---------------------------------------------------------------------------
+# The steps of a decoded token around the sparse products.  Tensors of several
+# tokens are [tokens, elements] with contiguous elements and any row stride;
+# all tensors of a call are on the current device.  Nothing here records
+# gradients.
+# ---------------------------------------------------------------------------
+_VECTOR = {_torch.float32: DBS_F32, _torch.bfloat16: DBS_BF16}
+_MASK_DTYPES = (_torch.int32, _torch.uint32)
+
+
+def _device_of(t):
+    d = t.get_device()
+    if d != _torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {d}, the current device is {_torch.cuda.current_device()}")
+    return d
+
+
+def _rows(t, name, width, device):
+    """(rows, dtype code, row stride) of a vector [width] or of rows [rows, width]."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = _VECTOR.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device")
+    shape = t.shape
+    nd = len(shape)
+    if nd not in (1, 2) or shape[-1] != width:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{width}] or [tokens, {width}]")
+    if nd == 1:
+        rows, ld = 1, width
+        inner = t.stride(0)
+    else:
+        rows = shape[0]
+        ld, inner = t.stride()
+        if rows == 1:
+            ld = width
+    if inner != 1 and width > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if ld < width and rows > 1:
+        raise ValueError(f"{name}: rows overlap (row stride {ld} < {width})")
+    return rows, code, ld
+
+
+def _mask_rows(mask, rows, width, device):
+    words = (width + 31) // 32
+    if not isinstance(mask, _Tensor) or not mask.is_cuda or mask.get_device() != device:
+        raise TypeError("the mask must be a CUDA tensor on the call's device")
+    if mask.dtype not in _MASK_DTYPES:
+        raise TypeError(f"the mask has dtype {mask.dtype}, expected int32 or uint32 words")
+    shape = mask.shape
+    if tuple(shape) != (rows, words) and not (rows == 1 and tuple(shape) == (words,)):
+        raise ValueError(f"the mask has shape {tuple(shape)}, expected [{rows}, {words}]")
+    if mask.stride(-1) != 1 and words > 1:
+        raise ValueError("the mask must have contiguous rows")
+    ld = words if rows == 1 else mask.stride(0)
+    if ld < words:
+        raise ValueError("mask rows overlap")
+    return ld
+
+
+class Q4Matrix:
+    """Owner of a dbs_q4_handle; freed with the object or by dbs_q4_free."""
+
+    def __init__(self, handle: C.c_void_p, m: int, n: int, group: int):
+        self.handle = handle
+        self.m, self.n, self.group = m, n, group
+
+    def __del__(self):
+        try:
+            dbs_q4_free(self)
+        except Exception:
+            pass
+
+
+def dbs_q4_build(m, n, group, codes, scales, zeros=None, stream=None) -> Q4Matrix:
+    """W[i, j] = scales[i, j // group] * (code[i, j] - zeros[i, j // group]) in 4 bits: codes uint8
+    [m, ceil(n/2)] (even column in the low nibble), scales [m, ceil(n/group)] float32 or bfloat16, zeros uint8
+    of that shape (each at most 15) or None (8)."""
+    m, n, group = int(m), int(n), int(group)
+    if group not in (32, 64, 128):
+        raise ValueError(f"group {group}: 32, 64 or 128 expected")
+    groups = (n + group - 1) // group
+    _need(codes, "codes", (_torch.uint8,), m * ((n + 1) // 2))
+    _need(scales, "scales", tuple(_VECTOR), m * groups)
+    device = _device_of(codes)
+    if zeros is not None:
+        _need(zeros, "zeros", (_torch.uint8,), m * groups)
+    if scales.get_device() != device or (zeros is not None and zeros.get_device() != device):
+        raise ValueError("codes, scales and zeros are on different devices")
+    h = C.c_void_p()
+    _check(_lib.dbs_q4_build(m, n, group, _ptr(codes), _ptr(scales), _VECTOR[scales.dtype], _ptr(zeros),
+                             _stream(stream, codes.device), C.byref(h)), "dbs_q4_build")
+    return Q4Matrix(h, m, n, group)
+
+
+def dbs_q4_bytes(A: Q4Matrix) -> int:
+    v = C.c_int64()
+    _check(_lib.dbs_q4_bytes(A.handle, C.byref(v)), "dbs_q4_bytes")
+    return int(v.value)
+
+
+def dbs_q4_free(A: Q4Matrix) -> None:
+    if A.handle is not None and A.handle.value:
+        _check(_lib.dbs_q4_free(A.handle), "dbs_q4_free")
+        A.handle = C.c_void_p()
+
+
+def _q4_operands(m, n, x, y):
+    if not isinstance(y, _Tensor) or not y.is_cuda:
+        raise TypeError("y must be a CUDA tensor")
+    device = _device_of(y)
+    tokens, xd, ldx = _rows(x, "x", n, device)
+    ty, yd, ldy = _rows(y, "y", m, device)
+    if tokens != ty:
+        raise ValueError(f"x has {tokens} tokens, y {ty}")
+    return tokens, xd, ldx, yd, ldy, device
+
+
+def dbs_q4_product(A: Q4Matrix, x, y, stream=None) -> None:
+    """y[t] = W x[t]; x [n] or [tokens, n], y [m] or [tokens, m], each float32 or bfloat16."""
+    tokens, xd, ldx, yd, ldy, _ = _q4_operands(A.m, A.n, x, y)
+    st = _lib.dbs_q4_product(A.handle, tokens, x.data_ptr(), xd, ldx, y.data_ptr(), yd, ldy, _stream(stream, y.device))
+    if st != DBS_OK:
+        raise DBSError(st, "dbs_q4_product")
+
+
+def dbs_q4_product_masked(A: Q4Matrix, x, row_mask, y, fill: float = float("-inf"), stream=None) -> None:
+    """dbs_q4_product for the rows whose bit is set in row_mask (int32 words [tokens, ceil(m/32)]), `fill`
+    elsewhere."""
+    tokens, xd, ldx, yd, ldy, device = _q4_operands(A.m, A.n, x, y)
+    ldmask = _mask_rows(row_mask, tokens, A.m, device)
+    st = _lib.dbs_q4_product_masked(A.handle, tokens, x.data_ptr(), xd, ldx, row_mask.data_ptr(), ldmask, float(fill),
+                                    y.data_ptr(), yd, ldy, _stream(stream, y.device))
+    if st != DBS_OK:
+        raise DBSError(st, "dbs_q4_product_masked")
+
+
+def dbs_q4_gated(G: Q4Matrix, U: Q4Matrix, x, activation: int, y, stream=None) -> None:
+    """y[t] = act(G x[t]) * (U x[t]) for two matrices of one shape, group and scale type."""
+    tokens, xd, ldx, yd, ldy, _ = _q4_operands(G.m, G.n, x, y)
+    st = _lib.dbs_q4_gated(G.handle, U.handle, int(activation), tokens, x.data_ptr(), xd, ldx, y.data_ptr(), yd, ldy,
+                           _stream(stream, y.device))
+    if st != DBS_OK:
+        raise DBSError(st, "dbs_q4_gated")
+
+
+def dbs_logits_adjust(logits, out, hist_ptr=None, hist=None, hist_new=None, repetition=None, frequency=None,
+                      presence=None, bias_ptr=None, bias_idx=None, bias_val=None, mask=None, stream=None) -> None:
+    """Penalties for repeated tokens, sparse biases and a bit mask on rows of logits ([vocab] or [rows, vocab]);
+    `out` may be `logits`.  Lists are ragged: row b's history is hist[hist_ptr[b]:hist_ptr[b + 1]], of which the
+    entries from hist_new[b] on count for frequency and presence; its biases likewise."""
+    if not isinstance(out, _Tensor) or not out.is_cuda:
+        raise TypeError("out must be a CUDA tensor")
+    device = _device_of(out)
+    if not isinstance(logits, _Tensor) or logits.dim() not in (1, 2):
+        raise ValueError("logits must be [vocab] or [rows, vocab]")
+    vocab = logits.shape[-1]
+    rows, ind, ld_in = _rows(logits, "logits", vocab, device)
+    orows, outd, ld_out = _rows(out, "out", vocab, device)
+    if orows != rows:
+        raise ValueError(f"logits have {rows} rows, out {orows}")
+    p = dbs_logits_params()
+    for t, name, dtypes, numel in (
+            (hist_ptr, "hist_ptr", _I32, rows + 1), (hist, "hist", _I32, None), (hist_new, "hist_new", _I32, rows),
+            (repetition, "repetition", _F32, rows), (frequency, "frequency", _F32, rows),
+            (presence, "presence", _F32, rows), (bias_ptr, "bias_ptr", _I32, rows + 1),
+            (bias_idx, "bias_idx", _I32, None), (bias_val, "bias_val", _F32, None)):
+        if t is not None:
+            _need(t, name, dtypes, numel)
+            if t.get_device() != device:
+                raise ValueError(f"{name} is on another device")
+            setattr(p, name, t.data_ptr())
+    if (hist_ptr is None) != (hist is None) or (bias_ptr is None) != (bias_idx is None) or \
+            (bias_idx is None) != (bias_val is None):
+        raise ValueError("hist_ptr and hist go together, as do bias_ptr, bias_idx and bias_val")
+    if hist is not None:
+        p.hist_len = hist.numel()
+    if bias_idx is not None:
+        if bias_idx.numel() != bias_val.numel():
+            raise ValueError("bias_idx and bias_val have different lengths")
+        p.bias_len = bias_idx.numel()
+    if mask is not None:
+        p.ldmask = _mask_rows(mask, rows, vocab, device)
+        p.mask = mask.data_ptr()
+    st = _lib.dbs_logits_adjust(rows, vocab, logits.data_ptr(), ind, ld_in, C.byref(p), out.data_ptr(), outd, ld_out,
+                                _stream(stream, out.device))
+    if st != DBS_OK:
+        raise DBSError(st, "dbs_logits_adjust")
+
+
+def _heads(t, name, device):
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = _VECTOR.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    return code, st, sh
+
+
+def dbs_rope(x, pos, freq, out, layout: int = DBS_ROPE_HALF, scale: float = 1.0, inverse: bool = False,
+             stream=None) -> None:
+    """Rotary positions on x [tokens, heads, head_dim] (any token and head stride) into `out`, which may be x:
+    the first 2 * freq.numel() elements of each head are rotated by pos[token] * freq (int32 positions, float64
+    frequencies, dbs_rope_frequencies), the others copied; tokens of negative position are left alone."""
+    if not isinstance(out, _Tensor) or not out.is_cuda:
+        raise TypeError("out must be a CUDA tensor")
+    device = _device_of(out)
+    xd, xt, xh = _heads(x, "x", device)
+    od, ot, oh = _heads(out, "out", device)
+    tokens, heads, dim = x.shape
+    if out.shape != x.shape:
+        raise ValueError(f"x has shape {tuple(x.shape)}, out {tuple(out.shape)}")
+    _need(pos, "pos", _I32, tokens)
+    _need(freq, "freq", (_torch.float64,))
+    if pos.get_device() != device or freq.get_device() != device:
+        raise ValueError("pos and freq are on another device")
+    st = _lib.dbs_rope(tokens, heads, dim, 2 * freq.numel(), int(layout), pos.data_ptr(), freq.data_ptr(), float(scale),
+                       1 if inverse else 0, x.data_ptr(), xd, xt, xh, out.data_ptr(), od, ot, oh,
+                       _stream(stream, out.device))
+    if st != DBS_OK:
+        raise DBSError(st, "dbs_rope")
+
+
+def dbs_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = DBS_ROPE_PLAIN, factor: float = 1.0,
+                         low: float = 1.0, high: float = 4.0, context: float = 0.0):
+    """(frequencies, scale) for dbs_rope: a float64 CPU tensor [rot_dim / 2] and the factor of the rotated
+    elements (1 but for DBS_ROPE_RAMP)."""
+    o = dbs_rope_options(int(rot_dim), int(scaling), float(base), float(factor), float(low), float(high), float(context))
+    freq = _torch.empty(max(0, int(rot_dim)) // 2, dtype=_torch.float64)
+    scale = C.c_float()
+    _check(_lib.dbs_rope_frequencies(C.byref(o), C.cast(freq.data_ptr(), C.POINTER(C.c_double)) if freq.numel() else None,
+                                     C.byref(scale)), "dbs_rope_frequencies")
+    return freq, float(scale.value)

@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libdbs.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["scan.hip", "build.hip", "spmspv.hip", "bfs.hip", "probe.hip", "api.cpp"]
+SOURCES = ["scan.hip", "build.hip", "spmspv.hip", "bfs.hip", "probe.hip", "q4.hip", "logits.hip", "rope.hip",
+           "api.cpp"]
 
 FLAGS = [
     f"--offload-arch={ARCH}",

@@ -1,0 +1,252 @@
+// Products of a matrix of 4-bit codes with group scales: layout (dbs_q4_build),
+// y = W x (dbs_q4_product), with a row mask (dbs_q4_product_masked) and the
+// gate and up layers in one pass (dbs_q4_gated).
+#include <math.h>
+#include <string.h>
+
+#include <new>
+
+#include "q4.h"
+
+namespace {
+
+// one thread per code dword of the layout
+__global__ __launch_bounds__(256) void k_q4_codes(int m, int n, int group, int mt, int kt, const uint8_t *__restrict__ codes,
+                                                  const uint8_t *__restrict__ zeros, uint32_t *__restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (int64_t)mt * kt * 256) return;
+  const int64_t tile = i >> 8;
+  const int lane = (int)(i >> 2) & 63, s = (int)i & 3;
+  const int64_t row = tile / kt * Q4_ROWS + (lane & 15);
+  const int64_t col0 = tile % kt * Q4_COLS + 32 * s + 8 * (lane >> 4);
+  const int64_t groups = ((int64_t)n + group - 1) / group;
+  uint32_t w = 0u;
+  for (int e = 0; e < 8; ++e) {
+    uint32_t c = 8u;
+    const int64_t col = col0 + e;
+    if (row < m && col < n) {
+      const uint8_t two = codes[row * (((int64_t)n + 1) / 2) + (col >> 1)];
+      c = (col & 1) ? two >> 4 : two & 15u;
+    } else if (row < m && zeros && col / group < groups) {
+      c = zeros[row * groups + col / group] & 15u;  // the rest of a cut group: weight zero
+    }
+    const int b = q4_code_bit(e);
+    w |= c << b;
+    if (b > 28) w |= c >> (32 - b);
+  }
+  out[i] = w;
+}
+
+// one thread per record; a zero point above 15 sets *bad
+template <class S>
+__global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int mt, int kt, const S *__restrict__ scales,
+                                                    const uint8_t *__restrict__ zeros, uint32_t *__restrict__ out,
+                                                    uint32_t *bad) {
+  const int gpt = Q4_COLS / group;
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (int64_t)mt * kt * Q4_ROWS * gpt) return;
+  const int64_t tile = i / (Q4_ROWS * gpt);
+  const int64_t row = tile / kt * Q4_ROWS + (i / gpt) % Q4_ROWS, g = tile % kt * gpt + i % gpt;
+  const int64_t groups = ((int64_t)n + group - 1) / group;
+  const bool in = row < m && g < groups;
+  uint32_t z = 8u;
+  if (in && zeros) z = zeros[row * groups + g];
+  if (z > 15u) *bad = 1u;
+  const float off = (float)(16u + z);
+  if (sizeof(S) == 4) {
+    out[2 * i] = in ? __float_as_uint((float)scales[row * groups + g]) : 0u;
+    out[2 * i + 1] = __float_as_uint(off);
+  } else {
+    out[i] = (in ? (uint32_t)scales[row * groups + g] << 16 : 0u) | __float_as_uint(off) >> 16;
+  }
+}
+
+DBS_DEV float act_apply(int act, float g) {
+  if (act == DBS_ACT_SILU) return g / (1.0f + expf(-g));
+  if (act == DBS_ACT_GELU_TANH) return 0.5f * g * (1.0f + tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g)));
+  return g > 0.0f || g != g ? g : 0.0f;
+}
+
+struct q4_args {
+  const uint32_t *codes, *recs, *codes2, *recs2;  // the second matrix of a gated product
+  int m, n, kt, gpt, act;
+  int tokens;
+  const void *x;
+  int64_t ldx;
+  const uint32_t *mask;
+  int64_t ldmask;
+  float fill;
+  void *y;
+  int64_t ldy;
+};
+
+// sum over the columns of lane's part of one row, every weight as (code - zero) * scale
+template <int WORDS, class X>
+DBS_DEV float row_part(const uint32_t *codes, const uint32_t *recs, const q4_args &q, int row, const X *x, int lane) {
+  const int rt = row >> 4, j = row & 15;
+  float sum = 0.0f;
+  for (int u = lane; u < q.kt * 16; u += DBS_WAVE) {  // dwords of the row
+    const int64_t tile = (int64_t)rt * q.kt + (u >> 4);
+    const int s = (u >> 2) & 3, kq = u & 3;
+    const int64_t col = (int64_t)(u >> 4) * Q4_COLS + 32 * s + 8 * kq;
+    const uint32_t w = codes[(tile * 64 + kq * 16 + j) * 4 + s];
+    float scale, off;
+    q4_record<WORDS>(recs, (tile * Q4_ROWS + j) * q.gpt + s * q.gpt / 4, scale, off);
+    for (int e = 0; e < 8; ++e)
+      if (col + e < q.n) sum += (16.0f + (float)q4_code(w, e) - off) * scale * dbs_value<X>::load(x + col + e);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  return sum;
+}
+
+// One wave per row, token by token.
+template <int WORDS, bool GATED, class X, class Y>
+__global__ __launch_bounds__(256) void k_q4_rows(q4_args q) {
+  const int lane = threadIdx.x & 63;
+  const int row = (int)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= q.m) return;
+  for (int64_t t = blockIdx.y; t < q.tokens; t += gridDim.y) {
+    const X *x = (const X *)q.x + t * q.ldx;
+    float v = q.fill;
+    if (!q.mask || (q.mask[t * q.ldmask + (row >> 5)] >> (row & 31)) & 1u) {
+      v = row_part<WORDS>(q.codes, q.recs, q, row, x, lane);
+      if (GATED) v = act_apply(q.act, v) * row_part<WORDS>(q.codes2, q.recs2, q, row, x, lane);
+    }
+    if (lane == 0) ((Y *)q.y)[t * q.ldy + row] = dbs_value<Y>::of(v);
+  }
+}
+
+template <int WORDS, bool GATED, class X, class Y>
+dbs_status launch(const q4_args &q, hipStream_t s) {
+  hipLaunchKernelGGL((k_q4_rows<WORDS, GATED, X, Y>), dim3((q.m + 3) / 4, q.tokens < 1024 ? q.tokens : 1024), dim3(256), 0, s, q);
+  return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
+}
+
+template <int WORDS, bool GATED>
+dbs_status launch_types(const q4_args &q, dbs_dtype xd, dbs_dtype yd, hipStream_t s) {
+  if (xd == DBS_F32) return yd == DBS_F32 ? launch<WORDS, GATED, float, float>(q, s) : launch<WORDS, GATED, float, bf16_bits>(q, s);
+  return yd == DBS_F32 ? launch<WORDS, GATED, bf16_bits, float>(q, s) : launch<WORDS, GATED, bf16_bits, bf16_bits>(q, s);
+}
+
+// checks shared by the products, then the launch
+dbs_status product(dbs_q4_handle A, dbs_q4_handle U, int act, int32_t tokens, const void *x, dbs_dtype xd, int64_t ldx,
+                   const uint32_t *mask, int64_t ldmask, float fill, void *y, dbs_dtype yd, int64_t ldy, void *stream) {
+  if (!A || tokens < 0 || !dbs_is_vector_dtype(xd) || !dbs_is_vector_dtype(yd)) return DBS_ERR_INVALID_ARG;
+  if (tokens > DBS_Q4_MAX_TOKENS) return DBS_ERR_UNSUPPORTED;
+  int dev = -1;
+  if (DBS_NOTE(hipGetDevice(&dev)) != hipSuccess) return DBS_ERR_DEVICE;
+  if (dev != A->device) return DBS_ERR_INVALID_ARG;
+  if (U && (U->device != dev || U->m != A->m || U->n != A->n || U->group != A->group || U->scale_dtype != A->scale_dtype))
+    return DBS_ERR_INVALID_ARG;
+  if (tokens == 0) return DBS_OK;
+  if (!x || !y) return DBS_ERR_INVALID_ARG;
+  if (tokens > 1 && (ldx < A->n || ldy < A->m || (mask && ldmask < ((int64_t)A->m + 31) / 32))) return DBS_ERR_INVALID_ARG;
+  const int64_t last = tokens - 1;
+  const int64_t ybytes = (last * ldy + A->m) * dbs_vector_size(yd);
+  if (dbs_overlap(x, (last * ldx + A->n) * dbs_vector_size(xd), y, ybytes)) return DBS_ERR_INVALID_ARG;
+  if (mask && dbs_overlap(mask, (last * ldmask + ((int64_t)A->m + 31) / 32) * 4, y, ybytes)) return DBS_ERR_INVALID_ARG;
+  q4_args q = {A->codes, A->recs, U ? U->codes : nullptr, U ? U->recs : nullptr, A->m, A->n, A->kt, A->gpt, act,
+               tokens, x, ldx, mask, ldmask, fill, y, ldy};
+  hipStream_t s = (hipStream_t)stream;
+  if (A->scale_dtype == DBS_F32) return U ? launch_types<2, true>(q, xd, yd, s) : launch_types<2, false>(q, xd, yd, s);
+  return U ? launch_types<1, true>(q, xd, yd, s) : launch_types<1, false>(q, xd, yd, s);
+}
+
+void q4_free(dbs_q4_matrix *A) {
+  if (A->codes) (void)hipFree(A->codes);
+  if (A->recs) (void)hipFree(A->recs);
+  delete A;
+}
+
+dbs_status map_err(hipError_t e) {
+  if (e == hipSuccess) return DBS_OK;
+  (void)hipGetLastError();
+  return e == hipErrorOutOfMemory || e == hipErrorMemoryAllocation ? DBS_ERR_OUT_OF_MEMORY : DBS_ERR_DEVICE;
+}
+
+dbs_status q4_build(dbs_q4_matrix *A, const uint8_t *codes, const void *scales, const uint8_t *zeros, hipStream_t s) {
+  const int64_t tiles = (int64_t)A->mt * A->kt;
+  const int64_t nrec = tiles * Q4_ROWS * A->gpt;
+  const int64_t code_bytes = tiles * Q4_TILE_BYTES, rec_bytes = nrec * 4 * q4_record_words(A->scale_dtype);
+  hipError_t e;
+  // the check flag behind the records
+  if ((e = DBS_NOTE(hipMalloc((void **)&A->codes, (size_t)code_bytes))) != hipSuccess) return map_err(e);
+  if ((e = DBS_NOTE(hipMalloc((void **)&A->recs, (size_t)rec_bytes + 4))) != hipSuccess) return map_err(e);
+  A->bytes = code_bytes + rec_bytes + 4;
+  uint32_t *bad = A->recs + rec_bytes / 4;
+  if ((e = DBS_NOTE(hipMemsetAsync(bad, 0, 4, s))) != hipSuccess) return map_err(e);
+  const int64_t g1 = tiles, g2 = (nrec + 255) / 256;
+  if (g1 > 0x7FFFFFFF || g2 > 0x7FFFFFFF) return DBS_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(k_q4_codes, dim3((unsigned)g1), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt, codes, zeros, A->codes);
+  if (A->scale_dtype == DBS_F32)
+    hipLaunchKernelGGL(k_q4_records<float>, dim3((unsigned)g2), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt,
+                       (const float *)scales, zeros, A->recs, bad);
+  else
+    hipLaunchKernelGGL(k_q4_records<bf16_bits>, dim3((unsigned)g2), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt,
+                       (const bf16_bits *)scales, zeros, A->recs, bad);
+  if ((e = DBS_NOTE(hipGetLastError())) != hipSuccess) return map_err(e);
+  uint32_t h = 0;
+  if ((e = DBS_NOTE(hipMemcpyAsync(&h, bad, 4, hipMemcpyDeviceToHost, s))) != hipSuccess) return map_err(e);
+  if ((e = DBS_NOTE(hipStreamSynchronize(s))) != hipSuccess) return map_err(e);
+  return h ? DBS_ERR_INVALID_ARG : DBS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dbs_status dbs_q4_build(int32_t m, int32_t n, int32_t group, const uint8_t *codes, const void *scales,
+                        dbs_dtype scale_dtype, const uint8_t *zeros, void *stream, dbs_q4_handle *out) {
+  if (!out || m < 1 || n < 1 || !codes || !scales || !dbs_is_vector_dtype(scale_dtype)) return DBS_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group != 128) return DBS_ERR_INVALID_ARG;
+  dbs_q4_matrix *A = new (std::nothrow) dbs_q4_matrix;
+  if (!A) return DBS_ERR_OUT_OF_MEMORY;
+  memset((void *)A, 0, sizeof(*A));
+  A->m = m;
+  A->n = n;
+  A->group = group;
+  A->scale_dtype = scale_dtype;
+  A->mt = (int32_t)(((int64_t)m + Q4_ROWS - 1) / Q4_ROWS);
+  A->kt = (int32_t)(((int64_t)n + Q4_COLS - 1) / Q4_COLS);
+  A->gpt = Q4_COLS / group;
+  dbs_status st = map_err(DBS_NOTE(hipGetDevice(&A->device)));
+  if (st == DBS_OK) st = q4_build(A, codes, scales, zeros, (hipStream_t)stream);
+  if (st != DBS_OK) {
+    q4_free(A);
+    return st;
+  }
+  *out = A;
+  return DBS_OK;
+}
+
+dbs_status dbs_q4_bytes(dbs_q4_handle A, int64_t *bytes) {
+  if (!A || !bytes) return DBS_ERR_INVALID_ARG;
+  *bytes = A->bytes;
+  return DBS_OK;
+}
+
+dbs_status dbs_q4_free(dbs_q4_handle A) {
+  if (A) q4_free(A);
+  return DBS_OK;
+}
+
+dbs_status dbs_q4_product(dbs_q4_handle A, int32_t tokens, const void *x, dbs_dtype x_dtype, int64_t ldx, void *y,
+                          dbs_dtype y_dtype, int64_t ldy, void *stream) {
+  return product(A, nullptr, 0, tokens, x, x_dtype, ldx, nullptr, 0, 0.0f, y, y_dtype, ldy, stream);
+}
+
+dbs_status dbs_q4_product_masked(dbs_q4_handle A, int32_t tokens, const void *x, dbs_dtype x_dtype, int64_t ldx,
+                                 const uint32_t *row_mask, int64_t ldmask, float fill, void *y, dbs_dtype y_dtype,
+                                 int64_t ldy, void *stream) {
+  if (!row_mask && tokens != 0) return DBS_ERR_INVALID_ARG;
+  return product(A, nullptr, 0, tokens, x, x_dtype, ldx, row_mask, ldmask, fill, y, y_dtype, ldy, stream);
+}
+
+dbs_status dbs_q4_gated(dbs_q4_handle G, dbs_q4_handle U, dbs_activation act, int32_t tokens, const void *x,
+                        dbs_dtype x_dtype, int64_t ldx, void *y, dbs_dtype y_dtype, int64_t ldy, void *stream) {
+  if (!U || (act != DBS_ACT_SILU && act != DBS_ACT_GELU_TANH && act != DBS_ACT_RELU)) return DBS_ERR_INVALID_ARG;
+  return product(G, U, act, tokens, x, x_dtype, ldx, nullptr, 0, 0.0f, y, y_dtype, ldy, stream);
+}
+
+}  // extern "C"
