@@ -347,10 +347,16 @@ _VECTOR = {_torch.float32: DBS_F32, _torch.bfloat16: DBS_BF16}
 _MASK_DTYPES = (_torch.int32, _torch.uint32)
 
 
-def _device_of(t):
+_CURRENT_DEVICE = getattr(_torch._C, "_cuda_getDevice", None) or _torch.cuda.current_device
+
+
+def _device_of(t, name):
+    """The current device, which `t` must be on (-1 is the CPU)."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
     d = t.get_device()
-    if d != _torch.cuda.current_device():
-        raise ValueError(f"the tensors are on device {d}, the current device is {_torch.cuda.current_device()}")
+    if d != _CURRENT_DEVICE():
+        raise ValueError(f"{name} is on device {d}, the current device is {_CURRENT_DEVICE()}")
     return d
 
 
@@ -358,24 +364,23 @@ def _rows(t, name, width, device):
     """(rows, dtype code, row stride) of a vector [width] or of rows [rows, width]."""
     if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device")
     code = _VECTOR.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on another device")
-    shape = t.shape
-    nd = len(shape)
-    if nd not in (1, 2) or shape[-1] != width:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{width}] or [tokens, {width}]")
-    if nd == 1:
-        rows, ld = 1, width
-        inner = t.stride(0)
-    else:
-        rows = shape[0]
-        ld, inner = t.stride()
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        rows, ld = shape[0], stride[0]
         if rows == 1:
             ld = width
-    if inner != 1 and width > 1:
+    elif len(shape) == 1:
+        rows, ld = 1, width
+    else:
+        rows = ld = 0
+    if not len(shape) or shape[-1] != width or len(shape) > 2:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{width}] or [tokens, {width}]")
+    if stride[-1] != 1 and width > 1:
         raise ValueError(f"{name} must have contiguous rows")
     if ld < width and rows > 1:
         raise ValueError(f"{name}: rows overlap (row stride {ld} < {width})")
@@ -423,7 +428,7 @@ def dbs_q4_build(m, n, group, codes, scales, zeros=None, stream=None) -> Q4Matri
     groups = (n + group - 1) // group
     _need(codes, "codes", (_torch.uint8,), m * ((n + 1) // 2))
     _need(scales, "scales", tuple(_VECTOR), m * groups)
-    device = _device_of(codes)
+    device = _device_of(codes, "codes")
     if zeros is not None:
         _need(zeros, "zeros", (_torch.uint8,), m * groups)
     if scales.get_device() != device or (zeros is not None and zeros.get_device() != device):
@@ -447,9 +452,7 @@ def dbs_q4_free(A: Q4Matrix) -> None:
 
 
 def _q4_operands(m, n, x, y):
-    if not isinstance(y, _Tensor) or not y.is_cuda:
-        raise TypeError("y must be a CUDA tensor")
-    device = _device_of(y)
+    device = _device_of(y, "y")
     tokens, xd, ldx = _rows(x, "x", n, device)
     ty, yd, ldy = _rows(y, "y", m, device)
     if tokens != ty:
@@ -490,9 +493,7 @@ def dbs_logits_adjust(logits, out, hist_ptr=None, hist=None, hist_new=None, repe
     """Penalties for repeated tokens, sparse biases and a bit mask on rows of logits ([vocab] or [rows, vocab]);
     `out` may be `logits`.  Lists are ragged: row b's history is hist[hist_ptr[b]:hist_ptr[b + 1]], of which the
     entries from hist_new[b] on count for frequency and presence; its biases likewise."""
-    if not isinstance(out, _Tensor) or not out.is_cuda:
-        raise TypeError("out must be a CUDA tensor")
-    device = _device_of(out)
+    device = _device_of(out, "out")
     if not isinstance(logits, _Tensor) or logits.dim() not in (1, 2):
         raise ValueError("logits must be [vocab] or [rows, vocab]")
     vocab = logits.shape[-1]
@@ -501,25 +502,37 @@ def dbs_logits_adjust(logits, out, hist_ptr=None, hist=None, hist_new=None, repe
     if orows != rows:
         raise ValueError(f"logits have {rows} rows, out {orows}")
     p = dbs_logits_params()
-    for t, name, dtypes, numel in (
-            (hist_ptr, "hist_ptr", _I32, rows + 1), (hist, "hist", _I32, None), (hist_new, "hist_new", _I32, rows),
-            (repetition, "repetition", _F32, rows), (frequency, "frequency", _F32, rows),
-            (presence, "presence", _F32, rows), (bias_ptr, "bias_ptr", _I32, rows + 1),
-            (bias_idx, "bias_idx", _I32, None), (bias_val, "bias_val", _F32, None)):
-        if t is not None:
-            _need(t, name, dtypes, numel)
-            if t.get_device() != device:
-                raise ValueError(f"{name} is on another device")
-            setattr(p, name, t.data_ptr())
-    if (hist_ptr is None) != (hist is None) or (bias_ptr is None) != (bias_idx is None) or \
-            (bias_idx is None) != (bias_val is None):
-        raise ValueError("hist_ptr and hist go together, as do bias_ptr, bias_idx and bias_val")
+
+    def given(t, name, dtypes, numel):
+        if not isinstance(t, _Tensor) or t.get_device() != device:
+            raise TypeError(f"{name} must be a CUDA tensor on the call's device")
+        if t.dtype not in dtypes or not t.is_contiguous():
+            raise TypeError(f"{name} must be contiguous {dtypes[0]}")
+        if numel is not None and t.numel() != numel:
+            raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+        return t.data_ptr()
+
+    if (hist_ptr is None) != (hist is None):
+        raise ValueError("hist_ptr and hist go together")
+    if (bias_ptr is None) != (bias_idx is None) or (bias_idx is None) != (bias_val is None):
+        raise ValueError("bias_ptr, bias_idx and bias_val go together")
     if hist is not None:
+        p.hist_ptr = given(hist_ptr, "hist_ptr", _I32, rows + 1)
+        p.hist = given(hist, "hist", _I32, None)
         p.hist_len = hist.numel()
+    if hist_new is not None:
+        p.hist_new = given(hist_new, "hist_new", _I32, rows)
+    if repetition is not None:
+        p.repetition = given(repetition, "repetition", _F32, rows)
+    if frequency is not None:
+        p.frequency = given(frequency, "frequency", _F32, rows)
+    if presence is not None:
+        p.presence = given(presence, "presence", _F32, rows)
     if bias_idx is not None:
-        if bias_idx.numel() != bias_val.numel():
-            raise ValueError("bias_idx and bias_val have different lengths")
+        p.bias_ptr = given(bias_ptr, "bias_ptr", _I32, rows + 1)
+        p.bias_idx = given(bias_idx, "bias_idx", _I32, None)
         p.bias_len = bias_idx.numel()
+        p.bias_val = given(bias_val, "bias_val", _F32, p.bias_len)
     if mask is not None:
         p.ldmask = _mask_rows(mask, rows, vocab, device)
         p.mask = mask.data_ptr()
@@ -550,9 +563,7 @@ def dbs_rope(x, pos, freq, out, layout: int = DBS_ROPE_HALF, scale: float = 1.0,
     """Rotary positions on x [tokens, heads, head_dim] (any token and head stride) into `out`, which may be x:
     the first 2 * freq.numel() elements of each head are rotated by pos[token] * freq (int32 positions, float64
     frequencies, dbs_rope_frequencies), the others copied; tokens of negative position are left alone."""
-    if not isinstance(out, _Tensor) or not out.is_cuda:
-        raise TypeError("out must be a CUDA tensor")
-    device = _device_of(out)
+    device = _device_of(out, "out")
     xd, xt, xh = _heads(x, "x", device)
     od, ot, oh = _heads(out, "out", device)
     tokens, heads, dim = x.shape

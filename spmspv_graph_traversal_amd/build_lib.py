@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libdbs.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["scan.hip", "build.hip", "spmspv.hip", "bfs.hip", "probe.hip", "q4.hip", "logits.hip", "rope.hip",
+SOURCES = ["scan.hip", "build.hip", "spmspv.hip", "bfs.hip", "probe.hip", "q4.hip", "q4_bf16.hip", "q4_bf16_gated.hip",
+           "q4_f32.hip", "q4_f32_gated.hip", "logits.hip", "rope.hip",
            "api.cpp"]
 
 FLAGS = [

@@ -1,12 +1,11 @@
 // Products of a matrix of 4-bit codes with group scales: layout (dbs_q4_build),
 // y = W x (dbs_q4_product), with a row mask (dbs_q4_product_masked) and the
 // gate and up layers in one pass (dbs_q4_gated).
-#include <math.h>
 #include <string.h>
 
 #include <new>
 
-#include "q4.h"
+#include "q4_tiles.h"
 
 namespace {
 
@@ -61,72 +60,23 @@ __global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int
   }
 }
 
-DBS_DEV float act_apply(int act, float g) {
-  if (act == DBS_ACT_SILU) return g / (1.0f + expf(-g));
-  if (act == DBS_ACT_GELU_TANH) return 0.5f * g * (1.0f + tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g)));
-  return g > 0.0f || g != g ? g : 0.0f;
-}
+// LDS of a workgroup for x: two such workgroups fit a compute unit
+constexpr int kFewLds = 72 * 1024;
 
-struct q4_args {
-  const uint32_t *codes, *recs, *codes2, *recs2;  // the second matrix of a gated product
-  int m, n, kt, gpt, act;
-  int tokens;
-  const void *x;
-  int64_t ldx;
-  const uint32_t *mask;
-  int64_t ldmask;
-  float fill;
-  void *y;
-  int64_t ldy;
-};
-
-// sum over the columns of lane's part of one row, every weight as (code - zero) * scale
-template <int WORDS, class X>
-DBS_DEV float row_part(const uint32_t *codes, const uint32_t *recs, const q4_args &q, int row, const X *x, int lane) {
-  const int rt = row >> 4, j = row & 15;
-  float sum = 0.0f;
-  for (int u = lane; u < q.kt * 16; u += DBS_WAVE) {  // dwords of the row
-    const int64_t tile = (int64_t)rt * q.kt + (u >> 4);
-    const int s = (u >> 2) & 3, kq = u & 3;
-    const int64_t col = (int64_t)(u >> 4) * Q4_COLS + 32 * s + 8 * kq;
-    const uint32_t w = codes[(tile * 64 + kq * 16 + j) * 4 + s];
-    float scale, off;
-    q4_record<WORDS>(recs, (tile * Q4_ROWS + j) * q.gpt + s * q.gpt / 4, scale, off);
-    for (int e = 0; e < 8; ++e)
-      if (col + e < q.n) sum += (16.0f + (float)q4_code(w, e) - off) * scale * dbs_value<X>::load(x + col + e);
+q4_shape pick_shape(const dbs_q4_matrix *A, int tokens, dbs_dtype xd, bool masked) {
+  q4_shape p = {};
+  if (tokens <= 4) {
+    const int rows = tokens * (xd == DBS_F32 ? 3 : 1);
+    p.token_tiles = 0;
+    p.waves = A->kt >= 32 && A->mt <= 512 ? 16 : A->kt >= 8 ? 8 : A->kt >= 4 ? 4 : A->kt >= 2 ? 2 : 1;
+    p.groups = masked && A->mt > 1024 ? 1024 : A->mt;
+    const int unit = Q4_COLS * p.waves, fit = kFewLds / (2 * rows) - q4::kFewPad;
+    p.cols = A->kt * Q4_COLS <= fit ? A->kt * Q4_COLS : fit / unit * unit;
+    return p;
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-  return sum;
-}
-
-// One wave per row, token by token.
-template <int WORDS, bool GATED, class X, class Y>
-__global__ __launch_bounds__(256) void k_q4_rows(q4_args q) {
-  const int lane = threadIdx.x & 63;
-  const int row = (int)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= q.m) return;
-  for (int64_t t = blockIdx.y; t < q.tokens; t += gridDim.y) {
-    const X *x = (const X *)q.x + t * q.ldx;
-    float v = q.fill;
-    if (!q.mask || (q.mask[t * q.ldmask + (row >> 5)] >> (row & 31)) & 1u) {
-      v = row_part<WORDS>(q.codes, q.recs, q, row, x, lane);
-      if (GATED) v = act_apply(q.act, v) * row_part<WORDS>(q.codes2, q.recs2, q, row, x, lane);
-    }
-    if (lane == 0) ((Y *)q.y)[t * q.ldy + row] = dbs_value<Y>::of(v);
-  }
-}
-
-template <int WORDS, bool GATED, class X, class Y>
-dbs_status launch(const q4_args &q, hipStream_t s) {
-  hipLaunchKernelGGL((k_q4_rows<WORDS, GATED, X, Y>), dim3((q.m + 3) / 4, q.tokens < 1024 ? q.tokens : 1024), dim3(256), 0, s, q);
-  return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
-}
-
-template <int WORDS, bool GATED>
-dbs_status launch_types(const q4_args &q, dbs_dtype xd, dbs_dtype yd, hipStream_t s) {
-  if (xd == DBS_F32) return yd == DBS_F32 ? launch<WORDS, GATED, float, float>(q, s) : launch<WORDS, GATED, float, bf16_bits>(q, s);
-  return yd == DBS_F32 ? launch<WORDS, GATED, bf16_bits, float>(q, s) : launch<WORDS, GATED, bf16_bits, bf16_bits>(q, s);
+  p.token_tiles = tokens <= 16 ? 1 : tokens <= 32 || xd == DBS_F32 ? 2 : 4;
+  p.waves = A->kt >= 8 ? 8 : A->kt >= 4 ? 4 : A->kt >= 2 ? 2 : 1;
+  return p;
 }
 
 // checks shared by the products, then the launch
@@ -146,11 +96,12 @@ dbs_status product(dbs_q4_handle A, dbs_q4_handle U, int act, int32_t tokens, co
   const int64_t ybytes = (last * ldy + A->m) * dbs_vector_size(yd);
   if (dbs_overlap(x, (last * ldx + A->n) * dbs_vector_size(xd), y, ybytes)) return DBS_ERR_INVALID_ARG;
   if (mask && dbs_overlap(mask, (last * ldmask + ((int64_t)A->m + 31) / 32) * 4, y, ybytes)) return DBS_ERR_INVALID_ARG;
-  q4_args q = {A->codes, A->recs, U ? U->codes : nullptr, U ? U->recs : nullptr, A->m, A->n, A->kt, A->gpt, act,
-               tokens, x, ldx, mask, ldmask, fill, y, ldy};
-  hipStream_t s = (hipStream_t)stream;
-  if (A->scale_dtype == DBS_F32) return U ? launch_types<2, true>(q, xd, yd, s) : launch_types<2, false>(q, xd, yd, s);
-  return U ? launch_types<1, true>(q, xd, yd, s) : launch_types<1, false>(q, xd, yd, s);
+  q4_args q = {{A->codes, U ? U->codes : nullptr}, {A->recs, U ? U->recs : nullptr}, A->m, A->n, A->mt, A->kt, act,
+               tokens, x, ldx, mask, ldmask, fill, yd == DBS_BF16, y, ldy};
+  const auto run = xd == DBS_BF16 ? (U ? dbs_q4_launch_bf16_gated : dbs_q4_launch_bf16)
+                                  : (U ? dbs_q4_launch_f32_gated : dbs_q4_launch_f32);
+  const hipError_t e = run(q, q4_record_words(A->scale_dtype), A->gpt, pick_shape(A, tokens, xd, mask != nullptr), (hipStream_t)stream);
+  return e == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
 
 void q4_free(dbs_q4_matrix *A) {
