@@ -60,22 +60,28 @@ __global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int
   }
 }
 
-// LDS of a workgroup for x: two such workgroups fit a compute unit
-constexpr int kFewLds = 72 * 1024;
-
-q4_shape pick_shape(const dbs_q4_matrix *A, int tokens, dbs_dtype xd, bool masked) {
+/*
+ * How a call is cut, from times of graphs of launches (us; rows x columns, 128 columns a group unless noted).
+ *   One to four tokens.  Few row blocks need every wave that shares one (eight splits): 4096 x 4096, one token, 4.1
+ *   against 4.5 with four splits.  With more row blocks than that fills the chip with, four splits do (11008 x 4096
+ *   6.9 against 7.1), and from 2048 on two row blocks a wave keep more bytes in flight for the same waves (65536 x
+ *   4096 26.2 against 29.2).  Under a mask one row block is the unit: 256 of 65536 rows wanted 6.6 against 8.1.
+ *   More tokens, 16 at a time.  Up to 512 workgroups of one row block: one row block, eight splits (4096 x 4096, 16 tokens, 5.4
+ *   against 8.2).  Else four row blocks that share x (11008 x 4096, 16 tokens, 8.7 against 9.9; fp32 13.9 against 20.4; gated
+ *   12.6 against 13.0), with two splits once that fills the chip (64 tokens 19.1 against 20.0).
+ */
+q4_shape pick_shape(const dbs_q4_matrix *A, int tokens, bool gated, bool masked) {
   q4_shape p = {};
-  if (tokens <= 4) {
-    const int rows = tokens * (xd == DBS_F32 ? 3 : 1);
-    p.token_tiles = 0;
-    p.waves = A->kt >= 32 && A->mt <= 512 ? 16 : A->kt >= 8 ? 8 : A->kt >= 4 ? 4 : A->kt >= 2 ? 2 : 1;
-    p.groups = masked && A->mt > 1024 ? 1024 : A->mt;
-    const int unit = Q4_COLS * p.waves, fit = kFewLds / (2 * rows) - q4::kFewPad;
-    p.cols = A->kt * Q4_COLS <= fit ? A->kt * Q4_COLS : fit / unit * unit;
-    return p;
+  p.few = tokens <= 4;
+  if (p.few) {
+    p.rows = !gated && !masked && A->mt >= 2048 ? 2 : 1;
+    p.splits = A->mt <= 512 ? 8 : 4;
+  } else {
+    const int64_t blocks = (tokens + 15) / 16;
+    p.rows = A->mt * blocks <= 512 ? 1 : 4;
+    p.splits = p.rows == 1 ? 8 : A->mt * blocks <= 2048 ? 4 : 2;
   }
-  p.token_tiles = tokens <= 16 ? 1 : tokens <= 32 || xd == DBS_F32 ? 2 : 4;
-  p.waves = A->kt >= 8 ? 8 : A->kt >= 4 ? 4 : A->kt >= 2 ? 2 : 1;
+  while (p.splits > 1 && p.splits / 2 >= A->kt) p.splits /= 2;  // a wave without columns would only wait
   return p;
 }
 
@@ -100,7 +106,7 @@ dbs_status product(dbs_q4_handle A, dbs_q4_handle U, int act, int32_t tokens, co
                tokens, x, ldx, mask, ldmask, fill, yd == DBS_BF16, y, ldy};
   const auto run = xd == DBS_BF16 ? (U ? dbs_q4_launch_bf16_gated : dbs_q4_launch_bf16)
                                   : (U ? dbs_q4_launch_f32_gated : dbs_q4_launch_f32);
-  const hipError_t e = run(q, q4_record_words(A->scale_dtype), A->gpt, pick_shape(A, tokens, xd, mask != nullptr), (hipStream_t)stream);
+  const hipError_t e = run(q, q4_record_words(A->scale_dtype), A->gpt, pick_shape(A, tokens, U != nullptr, mask != nullptr), (hipStream_t)stream);
   return e == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
 

@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "q4.h"
+#include "tile_kernels.h"
 
 struct q4_args {
   const uint32_t *codes[2], *recs[2];  // [1]: the second matrix of a gated product
@@ -19,11 +20,11 @@ struct q4_args {
   int64_t ldy;
 };
 
-// How a call is cut into workgroups of `waves` waves that split the columns.
+// How a call is cut into workgroups.
 struct q4_shape {
-  int token_tiles;   // of 16 tokens; 0: the kernel of one to four tokens
-  int waves;
-  int groups, cols;  // one to four tokens: workgroups, and columns of x in LDS at once
+  bool few;    // one to four tokens, else sixteen a workgroup
+  int rows;    // row blocks a workgroup: 1, 2 (few) or 4
+  int splits;  // waves that split the columns
 };
 
 namespace q4 {
@@ -38,23 +39,30 @@ DBS_DEV bf16x8 operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return r;
 }
 
-// the eight codes of a dword as bf16 16 + q: four mantissa bits under the exponent of 16, an "and or" each
-DBS_DEV bf16x8 codes_operand(uint32_t w) {
-  const uint32_t keep = 0x00780078u, sixteen = 0x41804180u;
-  return operand((w & keep) | sixteen, ((w >> 4) & keep) | sixteen, ((w >> 8) & keep) | sixteen,
-                 (__builtin_amdgcn_alignbit(w, w, 12) & keep) | sixteen);
+// The eight codes of a dword as bf16 16 + q: four mantissa bits under the exponent of 16, an "and or" each.  The two
+// constants come in registers: from literals the compiler makes two instructions.  (The empty asm only hides their value;
+// an instruction in it would escape the compiler's wait states between matrix and vector instructions.)
+struct code_masks {
+  uint32_t keep, sixteen;
+  DBS_DEV code_masks() : keep(0x00780078u), sixteen(0x41804180u) { asm("" : "+s"(keep), "+v"(sixteen)); }
+};
+DBS_DEV bf16x8 codes_operand(uint32_t w, const code_masks &m) {
+  return operand((w & m.keep) | m.sixteen, ((w >> 4) & m.keep) | m.sixteen, ((w >> 8) & m.keep) | m.sixteen,
+                 (__builtin_amdgcn_alignbit(w, w, 12) & m.keep) | m.sixteen);
 }
 
-// x as matrix operands: eight consecutive columns of one token per lane.  bf16 goes in as it is; fp32 is cut
-// into three bf16 parts of eight mantissa bits each, which sum to it exactly.
+// x on its way to the operands.  A lane takes 16 bytes of a token's row, so that adjacent lanes read adjacent bytes
+// (one operand's lanes are 16 tokens: read directly, each would be a memory request of its own, 64 cycles a load
+// instead of 16), and puts them into LDS as bf16: bf16 as it is, fp32 cut into three bf16 parts of eight mantissa bits,
+// which sum to it exactly.
 template <class X>
-struct x_part;
+struct x_piece;
 template <>
-struct x_part<bf16_bits> {
-  static constexpr int parts = 1;
+struct x_piece<bf16_bits> {
+  static constexpr int parts = 1, columns = 8;
   uint4 v;
-  DBS_DEV void load(const bf16_bits *p) { __builtin_memcpy(&v, p, 16); }
-  // columns col .. col + 7 of a row of n, zero from n on; loads of clamped addresses and no branches
+  DBS_DEV void load(const bf16_bits *row, int col) { __builtin_memcpy(&v, row + col, 16); }
+  // columns from n on are zero; loads of clamped addresses and no branches
   DBS_DEV void load_cut(const bf16_bits *row, int col, int n) {
     uint32_t h[8];
 #pragma unroll
@@ -63,34 +71,37 @@ struct x_part<bf16_bits> {
     for (int e = 0; e < 8; ++e) h[e] = col + e < n ? h[e] : 0u;
     v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   }
-  DBS_DEV void split(bf16x8 *out) const { out[0] = operand(v.x, v.y, v.z, v.w); }
+  // place(p): where part p of this piece goes
+  template <class F>
+  DBS_DEV void put(F place) const { *(uint4 *)place(0) = v; }
 };
 template <>
-struct x_part<float> {
-  static constexpr int parts = 3;
-  float v[8];
-  DBS_DEV void load(const float *p) { __builtin_memcpy(v, p, 32); }
+struct x_piece<float> {
+  static constexpr int parts = 3, columns = 4;
+  float v[4];
+  DBS_DEV void load(const float *row, int col) { __builtin_memcpy(v, row + col, 16); }
   DBS_DEV void load_cut(const float *row, int col, int n) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = row[min(col + e, n - 1)];
+    for (int e = 0; e < 4; ++e) v[e] = row[min(col + e, n - 1)];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = col + e < n ? v[e] : 0.0f;
+    for (int e = 0; e < 4; ++e) v[e] = col + e < n ? v[e] : 0.0f;
   }
-  DBS_DEV void split(bf16x8 *out) const {
-    float r[8];
+  template <class F>
+  DBS_DEV void put(F place) const {
+    float r[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = v[e];
+    for (int e = 0; e < 4; ++e) r[e] = v[e];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      uint32_t w[4];
+    for (int p = 0; p < 3; ++p) {
+      uint32_t w[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 2; ++e) {
         const uint32_t a = __float_as_uint(r[2 * e]), b = __float_as_uint(r[2 * e + 1]);
         w[e] = __builtin_amdgcn_perm(b, a, 0x07060302u);  // the upper halves
         r[2 * e] -= __uint_as_float(a & 0xFFFF0000u);
         r[2 * e + 1] -= __uint_as_float(b & 0xFFFF0000u);
       }
-      out[k] = operand(w[0], w[1], w[2], w[3]);
+      *(uint2 *)place(p) = make_uint2(w[0], w[1]);
     }
   }
 };
@@ -122,6 +133,44 @@ __device__ __noinline__ float row_dot(const uint32_t *codes, const uint32_t *rec
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
   return sum;
+}
+
+// a barrier that waits for LDS only, not for loads from memory in flight
+DBS_DEV void barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// LDS written by lanes of a wave and read by others of it: in order, no barrier
+DBS_DEV void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+DBS_DEV uint4 bld128(brsrc_t r, uint32_t off) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <int N>
+DBS_DEV void load_record_words(brsrc_t r, uint32_t off, uint32_t *to) {
+  if (N == 1) to[0] = bld32(r, off);
+  else if (N == 2) {
+    const uint64_t v = bld64(r, off);
+    to[0] = (uint32_t)v;
+    to[N - 1] = (uint32_t)(v >> 32);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = bld128(r, off + 16 * i);
+      to[4 * i] = v.x;
+      to[4 * i + 1] = v.y;
+      to[4 * i + 2] = v.z;
+      to[4 * i + 3] = v.w;
+    }
+  }
 }
 
 DBS_DEV uint32_t dword(const uint4 &v, int s) { return s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w; }
@@ -189,7 +238,9 @@ DBS_DEV void finish(const q4_args &q, const float *part, int parts, int stride, 
 }
 
 /*
- * Both kernels below: with off = 16 + zero, a group's part of y is
+ * y_t = W x_t for a workgroup's 16 R row_waves rows (of MATS matrices) and 16 TT tokens (FEW: up to four).
+ *
+ * Mathematics: with off = 16 + zero, a group's part of y is
  *   scale (sum (16 + q) x - off sum x),
  * so the codes go into the matrix cores as bf16 16 + q (exact, one "and or" for two of them) and sum x is a second
  * product, with ones, shared by all rows.  Both sums run in fp32 on exact products; scale and off are applied once
@@ -197,162 +248,53 @@ DBS_DEV void finish(const q4_args &q, const float *part, int parts, int stride, 
  * what loses bits, and the first part's products have few bits.  A result that is not finite is computed again
  * weight by weight.
  *
- * Split: the waves of a workgroup share its rows and take every waves-th block of 128 columns; their sums meet in LDS in a
- * fixed order.  Nothing is atomic, so results do not depend on timing.
+ * Split: `splits` waves share the rows of a row wave and take every splits-th block of 128 columns; their sums meet in LDS
+ * in a fixed order.  Nothing is atomic, so results do not depend on timing.
+ *
+ * x: each wave takes its own columns through LDS of its own (no barrier), rows of 256 bytes whose 16-byte pieces are
+ * rotated by the row (exclusive or) so that neither side meets bank conflicts.  FEW: the parts of an fp32 x are rows of one
+ * operand, token t's in rows 4t .. 4t + 2.
+ *
+ * Loads come back in order, and x (from L2) must not queue behind codes (from HBM) of a later block.  So while block b is
+ * multiplied, first x of block b + 1 is fetched, and when b's codes are used up, the codes of b + 2 into their
+ * registers: x has one block's time, codes almost two.  Blocks past a wave's last are out of range of the codes' buffer
+ * descriptor and read nothing.
  */
+template <class X, int MATS, int R, int TT, int RW, bool FEW>
+struct tiling {
+  static constexpr int P = x_piece<X>::parts;
+  static constexpr int kOps = FEW ? 1 : P;               // operands of a token tile and step
+  static constexpr int kSums = kOps > 1 ? 2 : 1;         // sums: first part, other parts
+  static constexpr int kRowsPerLoad = 64 * x_piece<X>::columns / Q4_COLS;
+  static constexpr int kTokens = FEW ? 4 : 16 * TT;
+  static constexpr int kLoads = kTokens / kRowsPerLoad / RW;  // of a column block's x, per wave
+  static constexpr int kPlane = TT * 16 * 256;           // bytes of a part of x
+  static constexpr int kBuffers = RW > 1 ? 2 : 1;
+  static constexpr int kLds = kBuffers * kOps * kPlane;  // per split
+  static constexpr int kDepth = 2;                // column blocks in flight
+  // waves of 256 registers come eight to a compute unit, of 128 sixteen
+  static constexpr int kThreads = RW > 1 && MATS * R * TT * kOps <= 2 ? 1024 : 512;
+  static_assert(kLoads >= 1, "");
+};
 
-/*
- * One to four tokens.  The parts of x, of every token, are rows of one 16-row operand: bf16 token i in row i, fp32 token t
- * in rows 4t .. 4t + 2, and stand in LDS, so that the registers hold the codes of DEPTH column blocks in flight.
- * A workgroup goes through the row blocks from blockIdx.x on in steps of the grid, so that few workgroups pass over a
- * mask that leaves little.  `cols`: columns of x in LDS at once, a multiple of 128 * waves, or all of them.
- */
-constexpr int kDepth = 4;
-constexpr int kFewPad = 32;  // elements behind a row of x in LDS: the rows start in different banks
-
-template <class X, int WORDS, int GPT, int MATS>
-__global__ __launch_bounds__(1024) void k_q4_few(q4_args q, int cols) {
+template <class X, int WORDS, int GPT, int MATS, int R, int TT, int RW, bool FEW>
+__global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k_q4(q4_args q) {
   extern __shared__ uint4 lds[];
-  constexpr int P = x_part<X>::parts;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  typedef tiling<X, MATS, R, TT, RW, FEW> T;
+  constexpr int kRec = GPT * WORDS, kTokens = T::kTokens, rows = Q4_ROWS * R * RW;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % RW, split = wave / RW, splits = (blockDim.x >> 6) / RW;
   const int j = lane & 15, kq = lane >> 4;
-  const int tokens = q.tokens;
-  bf16_bits *xs = (bf16_bits *)lds;  // [tokens * P][cols + kFewPad]
-  const int pitch = cols + kFewPad;
-  float *part = (float *)(lds + (tokens * P * pitch + 7) / 8);  // [waves][MATS][4][16]
-  // this lane's operand row: tokens past the last one repeat it, the fourth part repeats the third; dropped
-  const int arow = P == 1 ? min(j, tokens - 1) : min(j >> 2, tokens - 1) * P + min(j & 3, P - 1);
-  const bf16_bits *xrow = xs + arow * pitch + 8 * kq;
-  const bf16x8 ones = operand(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const X *x = (const X *)q.x;
-  bool staged = false;
-
-  for (int rt = blockIdx.x; rt < q.mt; rt += gridDim.x) {
-    if (q.mask && !any_wanted(q, 0, tokens, rt * Q4_ROWS, Q4_ROWS)) {
-      fill_rows(q, 0, tokens, rt * Q4_ROWS, Q4_ROWS);
-      continue;
-    }
-    const int64_t base = (int64_t)rt * q.kt;
-    f32x4 acc[MATS];
-#pragma unroll
-    for (int a = 0; a < MATS; ++a) acc[a] = zero;
-    uint4 codes[kDepth][MATS];
-    uint32_t recs[kDepth][MATS][GPT * WORDS];
-    auto fetch = [&](int d, int k) {
-#pragma unroll
-      for (int a = 0; a < MATS; ++a) {
-        codes[d][a] = ((const uint4 *)q.codes[a])[(base + k) * 64 + lane];
-        __builtin_memcpy(recs[d][a], q.recs[a] + ((base + k) * Q4_ROWS + j) * (GPT * WORDS), GPT * WORDS * 4);
-      }
-    };
-    for (int c0 = 0; c0 < q.kt * Q4_COLS; c0 += cols) {
-      const int first = c0 / Q4_COLS + wave, end = min(q.kt, (c0 + cols) / Q4_COLS);
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d)
-        if (first + d * waves < end) fetch(d, first + d * waves);
-      if (!staged || cols < q.kt * Q4_COLS) {
-        if (staged) __syncthreads();  // the columns before these are done with
-        const int width = min(cols, q.kt * Q4_COLS - c0);
-        for (int u = threadIdx.x; u < tokens * (width / 8); u += blockDim.x) {
-          const int t = u / (width / 8), c = u % (width / 8) * 8;
-          x_part<X> v;
-          const X *row = x + t * q.ldx;
-          if (c0 + c + 8 <= q.n) v.load(row + c0 + c);
-          else v.load_cut(row, c0 + c, q.n);
-          bf16x8 p[P];
-          v.split(p);
-#pragma unroll
-          for (int i = 0; i < P; ++i) *(bf16x8 *)(xs + (t * P + i) * pitch + c) = p[i];
-        }
-        staged = true;
-        __syncthreads();
-      }
-      auto multiply = [&](int d, int k) {
-        const bf16_bits *xk = xrow + (k * Q4_COLS - c0);
-#pragma unroll
-        for (int g = 0; g < GPT; ++g) {
-          constexpr int S = 4 / GPT;  // steps of 32 columns per group
-          f32x4 sum, dot[MATS];
-#pragma unroll
-          for (int s = 0; s < S; ++s) {
-            const bf16x8 xv = *(const bf16x8 *)(xk + 32 * (g * S + s));
-            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, s ? sum : zero, 0, 0, 0);
-#pragma unroll
-            for (int a = 0; a < MATS; ++a)
-              dot[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, codes_operand(dword(codes[d][a], g * S + s)), s ? dot[a] : zero, 0, 0, 0);
-          }
-#pragma unroll
-          for (int a = 0; a < MATS; ++a) {
-            float scale, off;
-            q4_record<WORDS>(recs[d][a], g, scale, off);
-            if (P == 1) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[a][i] = fmaf(scale, fmaf(-off, sum[i], dot[a][i]), acc[a][i]);
-            } else {  // smallest part first
-              const float v = fmaf(-off, sum[2], dot[a][2]) + fmaf(-off, sum[1], dot[a][1]);
-              acc[a][0] = fmaf(scale, v + fmaf(-off, sum[0], dot[a][0]), acc[a][0]);
-            }
-          }
-        }
-      };
-      int k = first;
-      for (; k + (2 * kDepth - 1) * waves < end; k += kDepth * waves) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-          multiply(d, k + d * waves);
-          fetch(d, k + (d + kDepth) * waves);
-        }
-      }
-      for (; k < end; k += kDepth * waves) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d)
-          if (k + d * waves < end) {
-            multiply(d, k + d * waves);
-            if (k + (d + kDepth) * waves < end) fetch(d, k + (d + kDepth) * waves);
-          }
-      }
-    }
-    // bf16: lanes kq = 0 hold token i in register i; fp32: lanes kq = t hold token t
-#pragma unroll
-    for (int a = 0; a < MATS; ++a) {
-      float *p = part + (wave * MATS + a) * 64 + j;
-      if (P == 1) {
-        if (kq == 0)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[16 * i] = acc[a][i];
-      } else {
-        p[16 * kq] = acc[a][0];
-      }
-    }
-    __syncthreads();
-    finish<X, WORDS, GPT, MATS>(q, part, waves, 4, Q4_ROWS, 0, tokens, rt * Q4_ROWS);
-    __syncthreads();
-  }
-}
-
-/*
- * More tokens: R x 16 rows (of each matrix) and TT x 16 tokens per workgroup; x goes from memory to the operands'
- * registers, as each wave needs its own columns of it, RING steps of 32 columns ahead, the codes one column block ahead.
- */
-template <class X, int WORDS, int GPT, int MATS, int R, int TT>
-__global__ __launch_bounds__(512) void k_q4_many(q4_args q) {
-  extern __shared__ uint4 lds[];
-  float *part = (float *)lds;  // [waves / 2][MATS][16 TT][16 R]
-  constexpr int P = x_part<X>::parts, L = P > 1 ? 2 : 1;  // sums: first part, other parts
-  constexpr int RING = TT * P <= 2 ? 4 : 2;
-  constexpr int kRows = Q4_ROWS * R, kTokens = 16 * TT, kOut = MATS * kTokens * kRows;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const int j = lane & 15, kq = lane >> 4;
-  const int rt0 = blockIdx.x * R, t0 = blockIdx.y * kTokens;
+  const int row0 = blockIdx.x * rows, rt0 = row0 / Q4_ROWS + rw * R, t0 = blockIdx.y * kTokens;
   const int tokens = min(kTokens, q.tokens - t0);
   const X *x = (const X *)q.x + (int64_t)t0 * q.ldx;
-  if (q.mask && !any_wanted(q, t0, tokens, rt0 * Q4_ROWS, kRows)) {
-    fill_rows(q, t0, tokens, rt0 * Q4_ROWS, kRows);
+  if (q.mask && !any_wanted(q, t0, tokens, row0, rows)) {
+    fill_rows(q, t0, tokens, row0, rows);
     return;
   }
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   const bf16x8 ones = operand(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  const code_masks masks;
   f32x4 acc[MATS][R][TT];
 #pragma unroll
   for (int a = 0; a < MATS; ++a)
@@ -360,79 +302,85 @@ __global__ __launch_bounds__(512) void k_q4_many(q4_args q) {
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int t = 0; t < TT; ++t) acc[a][r][t] = zero;
-  // lanes of tokens past the last one read the last one's x; their sums are dropped
-  const X *xl[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) xl[t] = x + (int64_t)min(16 * t + j, tokens - 1) * q.ldx;
-  int64_t base[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) base[r] = (int64_t)min(rt0 + r, q.mt - 1) * q.kt;  // past the last row: dropped too
 
-  uint4 codes[MATS][R];
-  x_part<X> ring[RING][TT];
-  auto fetch_codes = [&](uint4 (&to)[MATS][R], int k) {
+  // load i of this row wave takes its lanes' pieces of tokens kRowsPerLoad (RW i + rw) + lane / kPieces; tokens past the
+  // last one repeat it, their sums are dropped
+  constexpr int kPieces = 64 / T::kRowsPerLoad;
+  const int piece = lane % kPieces;
+  const X *from[T::kLoads];
+  int to[T::kLoads];
+  char *const xlds = (char *)lds + split * T::kLds;
+#pragma unroll
+  for (int i = 0; i < T::kLoads; ++i) {
+    const int token = T::kRowsPerLoad * (RW * i + rw) + lane / kPieces;
+    from[i] = x + (int64_t)min(token, tokens - 1) * q.ldx + piece * x_piece<X>::columns;
+    // FEW fp32: part p of a token in row 4 token + p; otherwise parts are kPlane bytes apart
+    const int row = FEW && T::P > 1 ? token * 4 : token, chunk = piece * x_piece<X>::columns / 8;
+    to[i] = row * 256 + ((chunk ^ row) & 15) * 16 + piece * x_piece<X>::columns % 8 * 2;
+  }
+  const int whole = q.n / Q4_COLS;  // column blocks that n does not end in
+  brsrc_t rc[MATS][R], rr[MATS][R];
+#pragma unroll
+  for (int a = 0; a < MATS; ++a)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t first = (int64_t)min(rt0 + r, q.mt - 1) * q.kt;  // past the last row block: dropped too
+      rc[a][r] = make_rsrc((const char *)q.codes[a] + first * Q4_TILE_BYTES, (uint64_t)q.kt * Q4_TILE_BYTES);
+      rr[a][r] = make_rsrc(q.recs[a] + first * (Q4_ROWS * kRec), (uint64_t)q.kt * (Q4_ROWS * kRec * 4));
+    }
+
+  constexpr int D = T::kDepth;
+  uint4 codes[D][MATS][R];
+  uint32_t recs[D][MATS][R][kRec];
+  x_piece<X> xr[D][T::kLoads];
+  auto fetch_codes = [&](int d, int k, int end) {
+    const uint32_t oc = k < end ? (uint32_t)k * Q4_TILE_BYTES + lane * 16 : OOB_OFF;
+    const uint32_t orec = k < end ? ((uint32_t)k * Q4_ROWS + j) * (kRec * 4) : OOB_OFF;
 #pragma unroll
     for (int a = 0; a < MATS; ++a)
 #pragma unroll
-      for (int r = 0; r < R; ++r) to[a][r] = ((const uint4 *)q.codes[a])[(base[r] + k) * 64 + lane];
+      for (int r = 0; r < R; ++r) {
+        codes[d][a][r] = bld128(rc[a][r], oc);
+        load_record_words<kRec>(rr[a][r], orec, recs[d][a][r]);
+      }
   };
-  auto fetch_x = [&](int slot, int k, int s) {
+  auto put_x = [&](int d) {
+    char *at = xlds + (RW > 1 ? d % 2 * (T::kOps * T::kPlane) : 0);
 #pragma unroll
-    for (int t = 0; t < TT; ++t) ring[slot][t].load(xl[t] + k * Q4_COLS + 32 * s + 8 * kq);
+    for (int i = 0; i < T::kLoads; ++i)
+      xr[d][i].put([&](int p) { return FEW ? at + (to[i] ^ p << 4) + p * 256 : at + to[i] + p * T::kPlane; });
   };
-  // Column block k, whose codes and first RING steps of x are in registers; unless it is the wave's LAST, those of block
-  // `next` are fetched meanwhile.  CUT: the block that n ends in, whose x is fetched here.  Nothing in it branches: the
-  // compiler would move a group's scaling behind the branch and keep its sums in registers till then.
-  auto block = [&](auto last_, auto cut_, int k, int next) {
-    constexpr bool LAST = decltype(last_)::value, CUT = decltype(cut_)::value;
-    uint32_t recs[MATS][R][GPT * WORDS];
-#pragma unroll
-    for (int a = 0; a < MATS; ++a)
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        __builtin_memcpy(recs[a][r], q.recs[a] + ((base[r] + k) * Q4_ROWS + j) * (GPT * WORDS), GPT * WORDS * 4);
-    uint4 after[MATS][R];
-    if (!LAST) fetch_codes(after, next);
+  // The products of one column block.  Nothing in it branches: the compiler would move a group's scaling behind the branch
+  // and keep its sums in registers till then.
+  auto multiply = [&](int d) {
     constexpr int S = 4 / GPT;  // steps of 32 columns per group
+    const char *at = xlds + (RW > 1 ? d % 2 * (T::kOps * T::kPlane) : 0) + j * 256;
 #pragma unroll
     for (int g = 0; g < GPT; ++g) {
-      f32x4 sum[TT][L], dot[MATS][R][TT][L];
+      f32x4 sum[TT][T::kSums], dot[MATS][R][TT][T::kSums];
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         const int step = g * S + s;
-        bf16x8 xs[TT][P];
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          if (CUT) {
-            x_part<X> v;
-            v.load_cut(xl[t], k * Q4_COLS + 32 * step + 8 * kq, q.n);
-            v.split(xs[t]);
-          } else {
-            ring[step % RING][t].split(xs[t]);
-          }
-        }
-        if (!CUT) {
-          if (step + RING < 4) fetch_x(step % RING, k, step + RING);
-          else if (!LAST) fetch_x(step % RING, next, step + RING - 4);
-        }
+        bf16x8 xs[TT][T::kOps];
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
-          for (int p = 0; p < P; ++p) {
-            f32x4 &to = sum[t][p ? L - 1 : 0];
-            to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[t][p], ones, s || p > 1 ? to : zero, 0, 0, 0);
+          for (int p = 0; p < T::kOps; ++p) {
+            xs[t][p] = *(const bf16x8 *)(at + p * T::kPlane + t * 4096 + (((4 * step + kq) ^ j) & 15) * 16);
+            f32x4 &into = sum[t][p ? T::kSums - 1 : 0];
+            into = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[t][p], ones, s || p > 1 ? into : zero, 0, 0, 0);
           }
 #pragma unroll
         for (int a = 0; a < MATS; ++a)
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const bf16x8 w = codes_operand(dword(codes[a][r], step));
+            const bf16x8 w = codes_operand(dword(codes[d][a][r], step), masks);
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
-              for (int p = 0; p < P; ++p) {
-                f32x4 &to = dot[a][r][t][p ? L - 1 : 0];
-                to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[t][p], w, s || p > 1 ? to : zero, 0, 0, 0);
+              for (int p = 0; p < T::kOps; ++p) {
+                f32x4 &into = dot[a][r][t][p ? T::kSums - 1 : 0];
+                into = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[t][p], w, s || p > 1 ? into : zero, 0, 0, 0);
               }
           }
       }
@@ -441,53 +389,83 @@ __global__ __launch_bounds__(512) void k_q4_many(q4_args q) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           float scale, off;
-          q4_record<WORDS>(recs[a][r], g, scale, off);
+          q4_record<WORDS>(recs[d][a][r], g, scale, off);
+          if (FEW && T::P > 1) {  // registers 0 .. 2 hold the parts' sums; smallest first
+            const f32x4 d = dot[a][r][0][0], m = sum[0][0];
+            const float low = fmaf(-off, m[2], d[2]) + fmaf(-off, m[1], d[1]);
+            acc[a][r][0][0] = fmaf(scale, low + fmaf(-off, m[0], d[0]), acc[a][r][0][0]);
+          } else {
 #pragma unroll
-          for (int t = 0; t < TT; ++t)
+            for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float v = fmaf(-off, sum[t][0][i], dot[a][r][t][0][i]);
-              if (L > 1) v += fmaf(-off, sum[t][L - 1][i], dot[a][r][t][L - 1][i]);
-              acc[a][r][t][i] = fmaf(scale, v, acc[a][r][t][i]);
-            }
+              for (int i = 0; i < 4; ++i) {
+                float v = fmaf(-off, sum[t][0][i], dot[a][r][t][0][i]);
+                if (T::kSums > 1) v += fmaf(-off, sum[t][T::kSums - 1][i], dot[a][r][t][T::kSums - 1][i]);
+                acc[a][r][t][i] = fmaf(scale, v, acc[a][r][t][i]);
+              }
+          }
         }
     }
-    if (!LAST) {
-#pragma unroll
-      for (int a = 0; a < MATS; ++a)
-#pragma unroll
-        for (int r = 0; r < R; ++r) codes[a][r] = after[a][r];
-    }
   };
-  const int whole = q.n / Q4_COLS;  // blocks that n does not end in
-  if (wave < whole) {
-    fetch_codes(codes, wave);
+  // A block from its registers: x through LDS, for this wave or for all that share it.  Two buffers there: who writes one
+  // again has passed a barrier since its readers were done.
+  auto block = [&](int d) {
+    put_x(d);
+    if (RW > 1) barrier();
+    else wave_fence();
+    multiply(d);
+    if (RW == 1) wave_fence();
+  };
+  // Row waves meet at barriers, so all splits go the same number of rounds; rounds without a block multiply by zero.
+  const int rounds = RW > 1 ? (whole + splits - 1) / splits : split < whole ? (whole - split + splits - 1) / splits : 0;
+  if (rounds > 0) {
+    int k = split;
+    auto fetch = [&](int d, int k) {
+      __builtin_amdgcn_sched_barrier(0);  // in the order in which they are used
 #pragma unroll
-    for (int s = 0; s < RING; ++s) fetch_x(s, wave, s);
-    int k = wave;
-    for (; k + waves < whole; k += waves) block(std::false_type(), std::false_type(), k, k + waves);
-    block(std::true_type(), std::false_type(), k, k);
+      for (int i = 0; i < T::kLoads; ++i) xr[d][i].load(from[i], min(k, whole - 1) * Q4_COLS);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_codes(d, k, whole);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d, k + d * splits);
+    // one way through each turn: where paths with and without loads met, the compiler would wait for all of them
+    const int turns = (rounds - 1) / D;
+    for (int i = 0; i < turns; ++i) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        block(d);
+        k += splits;
+        fetch(d, k + (D - 1) * splits);
+      }
+    }
+    const int left = rounds - turns * D;
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (d == left) break;
+      block(d);
+    }
   }
-  if (whole < q.kt && whole % waves == wave) {
-    fetch_codes(codes, whole);
-    block(std::true_type(), std::true_type(), whole, whole);
+  if (whole < q.kt) {  // the block that n ends in: the first split's
+    barrier();
+    if (split == 0) {
+      fetch_codes(0, whole, q.kt);
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i)
+        xr[0][i].load_cut(from[i] - piece * x_piece<X>::columns, whole * Q4_COLS + piece * x_piece<X>::columns, q.n);
+      put_x(0);
+    }
+    barrier();
+    if (split == 0) multiply(0);
   }
 
-  // lane (kq, j), register i: token 16 t + 4 kq + i of row 16 r + j
-  auto slot = [&](int a, int r, int t, int i) { return (a * kTokens + 16 * t + 4 * kq + i) * kRows + 16 * r + j; };
-  const int half = (waves + 1) / 2;  // the upper half of the waves adds to the lower one first: half the LDS
-  if (wave >= half) {
-#pragma unroll
-    for (int a = 0; a < MATS; ++a)
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) part[(wave - half) * kOut + slot(a, r, t, i)] = acc[a][r][t][i];
-  }
+  // part[splits / 2][MATS][kTokens][rows], over the x of before.  Lane (kq, j), register i: token 16 t + 4 kq + i of row
+  // 16 r + j; FEW bf16: lanes kq = 0 only, FEW fp32: token kq in register 0
   __syncthreads();
-  if (wave < half) {
+  float *part = (float *)lds;
+  const int out_size = MATS * kTokens * rows, half = (splits + 1) / 2;
+  auto each = [&](auto &&use) {
 #pragma unroll
     for (int a = 0; a < MATS; ++a)
 #pragma unroll
@@ -496,55 +474,55 @@ __global__ __launch_bounds__(512) void k_q4_many(q4_args q) {
         for (int t = 0; t < TT; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float *p = part + wave * kOut + slot(a, r, t, i);
-            *p = acc[a][r][t][i] + (wave + half < waves ? *p : 0.0f);
+            if (FEW && T::P > 1 && i) continue;
+            if (FEW && T::P == 1 && kq) continue;
+            const int token = FEW ? (T::P > 1 ? kq : i) : 16 * t + 4 * kq + i;
+            use((a * kTokens + token) * rows + 16 * (rw * R + r) + j, acc[a][r][t][i]);
           }
-  }
+  };
+  // the upper half of the splits adds to the lower one first: half the LDS
+  if (split >= half) each([&](int at, float v) { part[(split - half) * out_size + at] = v; });
   __syncthreads();
-  finish<X, WORDS, GPT, MATS>(q, part, half, kTokens, kRows, t0, tokens, rt0 * Q4_ROWS);
+  if (split < half)
+    each([&](int at, float v) {
+      float *p = part + split * out_size + at;
+      *p = v + (split + half < splits ? *p : 0.0f);
+    });
+  __syncthreads();
+  finish<X, WORDS, GPT, MATS>(q, part, half, kTokens, rows, t0, tokens, row0);
 }
 
-template <class X, int WORDS, int GPT, int MATS>
-hipError_t launch_few(const q4_args &q, const q4_shape &p, hipStream_t s) {
-  constexpr int P = x_part<X>::parts;
-  const size_t lds = (size_t)((q.tokens * P * (p.cols + kFewPad) + 7) / 8) * 16 + (size_t)p.waves * MATS * 256;
-  hipLaunchKernelGGL((k_q4_few<X, WORDS, GPT, MATS>), dim3((unsigned)p.groups), dim3(64 * p.waves), lds, s, q, p.cols);
-  return DBS_NOTE(hipGetLastError());
-}
-
-template <class X, int WORDS, int GPT, int MATS, int R, int TT>
-hipError_t launch_many(const q4_args &q, const q4_shape &p, hipStream_t s) {
-  const dim3 grid((unsigned)((q.mt + R - 1) / R), (unsigned)((q.tokens + 16 * TT - 1) / (16 * TT)));
-  const size_t lds = (size_t)((p.waves + 1) / 2) * MATS * R * TT * 1024;
-  hipLaunchKernelGGL((k_q4_many<X, WORDS, GPT, MATS, R, TT>), grid, dim3(64 * p.waves), lds, s, q);
+template <class X, int WORDS, int GPT, int MATS, int R, int TT, int RW, bool FEW>
+hipError_t launch_tiles(const q4_args &q, int splits, hipStream_t s) {
+  typedef tiling<X, MATS, R, TT, RW, FEW> T;
+  constexpr int rows = R * RW;
+  while (splits * T::kLds > 160 * 1024 || 64 * splits * RW > T::kThreads) splits /= 2;
+  const auto kernel = k_q4<X, WORDS, GPT, MATS, R, TT, RW, FEW>;
+  const dim3 grid((unsigned)((q.mt + rows - 1) / rows), (unsigned)((q.tokens + T::kTokens - 1) / T::kTokens));
+  const size_t parts = (size_t)((splits + 1) / 2) * MATS * rows * Q4_ROWS * T::kTokens * 4;
+  const size_t xs = (size_t)splits * T::kLds, lds = parts > xs ? parts : xs;
+  if (lds > 65536) {  // more than a launch gets unasked
+    static const hipError_t asked = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (asked != hipSuccess) return DBS_NOTE(asked);
+  }
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * splits * RW), lds, s, q);
   return DBS_NOTE(hipGetLastError());
 }
 
 template <class X, int WORDS, int GPT, int MATS>
 hipError_t launch_shape(const q4_args &q, const q4_shape &p, hipStream_t s) {
-  if (p.token_tiles == 0) return launch_few<X, WORDS, GPT, MATS>(q, p, s);
-#ifdef Q4_TUNE
-  if (getenv("Q4T")) {
-    int tt, r, w;
-    sscanf(getenv("Q4T"), "%d,%d,%d", &tt, &r, &w);
-    q4_shape z = p; z.waves = w;
-    switch (tt * 10 + r) {
-      case 11: return launch_many<X, WORDS, GPT, MATS, 1, 1>(q, z, s);
-      case 12: return launch_many<X, WORDS, GPT, MATS, 2, 1>(q, z, s);
-      case 14: return launch_many<X, WORDS, GPT, MATS, 4, 1>(q, z, s);
-      case 21: return launch_many<X, WORDS, GPT, MATS, 1, 2>(q, z, s);
-      case 22: return launch_many<X, WORDS, GPT, MATS, 2, 2>(q, z, s);
-      case 24: return launch_many<X, WORDS, GPT, MATS, 4, 2>(q, z, s);
-      case 41: return launch_many<X, WORDS, GPT, MATS, 1, 4>(q, z, s);
-      case 42: return launch_many<X, WORDS, GPT, MATS, 2, 4>(q, z, s);
-      case 43: return launch_many<X, WORDS, GPT, MATS, 3, 4>(q, z, s);
-      case 44: return launch_many<X, WORDS, GPT, MATS, 4, 4>(q, z, s);
+  if (p.few) {
+    if constexpr (MATS == 1) {
+      if (p.rows == 2) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 1, true>(q, p.splits, s);
     }
+    return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 1, true>(q, p.splits, s);
   }
-#endif
-  if (p.token_tiles == 1) return launch_many<X, WORDS, GPT, MATS, 1, 1>(q, p, s);
-  if (p.token_tiles == 2) return launch_many<X, WORDS, GPT, MATS, 2, 2>(q, p, s);
-  return launch_many<X, WORDS, GPT, MATS, 2, 4>(q, p, s);
+  if (p.rows == 1) return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 1, false>(q, p.splits, s);
+  if (p.rows == 4) {
+    if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 2, false>(q, p.splits, s);
+    else return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 4, false>(q, p.splits, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <class X, int MATS>

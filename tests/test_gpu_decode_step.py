@@ -75,6 +75,34 @@ def test_product_is_exact_on_integers(dbs, m, n, group, zeros, scales, x_kind):
 
 
 @pytest.mark.parametrize("x_kind", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,group,zeros,scales", [(8300, 300, 32, True, "bf16"), (8207, 1408, 128, False, "bf16"),
+                                                    (33000, 130, 64, True, "f32"), (600, 9000, 128, True, "bf16")])
+def test_products_of_many_rows_are_exact_on_integers(dbs, m, n, group, zeros, scales, x_kind):
+    """Sizes that take each way of cutting a call into workgroups, for one matrix and for two."""
+    import torch
+
+    rng = np.random.default_rng(m)
+    w, u = ref.Q4(rng, m, n, group, zeros, scales), ref.Q4(rng, m, n, group, zeros, scales)
+    A, U = w.build(dbs), u.build(dbs)
+    w64, u64 = torch.from_numpy(w.w).cuda().t(), torch.from_numpy(u.w).cuda().t()
+    for t in (1, 4, 7, 16, 40, 130):
+        x = cuda(integers(rng, t, n))
+        xx = x.bfloat16() if x_kind == "bf16" else x
+        g, h = x.double() @ w64, x.double() @ u64
+        y = empty((t, m), "f32")
+        dbs.dbs_q4_product(A, xx, y)
+        assert torch.equal(y.double(), g), f"{t} tokens"
+        dbs.dbs_q4_gated(A, U, xx, dbs.DBS_ACT_RELU, y)
+        assert torch.equal(y, (g.clamp_min(0) * h).float()), f"{t} tokens, gated"
+        words = cuda(rng.integers(-2 ** 31, 2 ** 31, (t, (m + 31) // 32)).astype(np.int32))
+        words[:, : m // 80] = 0
+        row = torch.arange(m, device="cuda")
+        wanted = (words[:, row // 32] >> (row % 32)) & 1 != 0
+        dbs.dbs_q4_product_masked(A, xx, words, y)
+        assert torch.equal(y.double(), torch.where(wanted, g, -np.inf)), f"{t} tokens, masked"
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32"])
 @pytest.mark.parametrize("tokens", [1, 3, 8, 30, 64])
 def test_product_of_real_values(dbs, tokens, x_kind):
     rng = np.random.default_rng(tokens)
