@@ -3,76 +3,143 @@
 
 namespace {
 
-constexpr int kSlab = 4096;  // tokens of one workgroup
-constexpr uint32_t kSeen = 0x80000000u;
-
 // the part [lo, hi) of list `b`, clamped to the list's length
 DBS_DEV void list_range(const int32_t *ptr, int64_t len, int64_t b, int64_t &lo, int64_t &hi) {
   lo = ptr[b] < 0 ? 0 : ptr[b];
   hi = ptr[b + 1] > len ? len : ptr[b + 1];
 }
 
-// One workgroup per row and slab of the vocabulary.  The history is sparse
-// and unordered, so each workgroup counts the ids that fall into its slab in
-// LDS (integer adds: any order gives the same counts) instead of a count
-// array in memory that would have to be cleared, filled and read per call.
-// The bias of an id that comes twice is its last entry's: the slab keeps the
-// highest entry number.
-template <class X, class Y>
-__global__ __launch_bounds__(256) void k_logits(int vocab, const X *logits, int64_t ld_in, dbs_logits_params q, Y *out,
+// calls use(position, id) for the list's entries [lo, hi), four to a load
+template <class F>
+DBS_DEV void each_id(const int32_t *list, int64_t lo, int64_t hi, F use) {
+  const int64_t step = 4 * blockDim.x;
+  int64_t i = lo + 4 * threadIdx.x;
+  for (; i + 4 <= hi; i += step) {
+    int32_t v[4];
+    __builtin_memcpy(v, list + i, 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) use(i + e, v[e]);
+  }
+  for (; i < hi; ++i) use(i, list[i]);  // of one thread: the list's last one to three
+}
+
+template <class T>
+struct four {
+  T v[4];
+};
+// entries [0, count) of four values at p
+template <class T>
+DBS_DEV four<T> load_four(const T *p, int count) {
+  four<T> f = {};
+  if (count >= 4) __builtin_memcpy(&f, p, sizeof f);
+  else
+    for (int e = 0; e < count; ++e) f.v[e] = p[e];
+  return f;
+}
+template <class T>
+DBS_DEV void store_four(T *p, const four<T> &f, int count) {
+  if (count >= 4) __builtin_memcpy(p, &f, sizeof f);
+  else
+    for (int e = 0; e < count; ++e) p[e] = f.v[e];
+}
+
+/*
+ * One workgroup per row and slab of the vocabulary, four neighbouring tokens to a thread PIECES times.
+ *
+ * The history is sparse and unordered, so each workgroup counts the ids that fall into its slab in LDS (integers: any
+ * order gives the same counts) instead of in an array in memory that would have to be cleared, filled and read again
+ * in every call.  A word holds twice the count of the generated entries, and an odd word or a count means that the id was
+ * seen.  The bias of an id that comes twice is its last entry's: the slab keeps the highest entry number.
+ *
+ * Bound by memory: logits read and written once; the lists come from L2 for every slab.  The logits are loaded before the
+ * lists are gone through, so that their way from memory is no wait; those that a mask closes are not read at all.
+ */
+template <class X, class Y, int PIECES>
+__global__ __launch_bounds__(512) void k_logits(int vocab, const X *logits, int64_t ld_in, dbs_logits_params q, Y *out,
                                                 int64_t ld_out) {
-  __shared__ uint32_t count[kSlab], entry[kSlab];
+  extern __shared__ uint4 lds[];
   const int64_t b = blockIdx.y;
-  const int base = blockIdx.x * kSlab, width = min(kSlab, vocab - base);
-  const bool hist = q.hist_ptr != nullptr, bias = q.bias_ptr != nullptr;
-  for (int i = threadIdx.x; i < kSlab; i += blockDim.x) count[i] = entry[i] = 0u;
-  __syncthreads();
-  int64_t lo, hi;
-  if (hist) {
-    list_range(q.hist_ptr, q.hist_len, b, lo, hi);
-    const int64_t fresh = lo + (q.hist_new ? q.hist_new[b] : 0);
-    for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
-      const uint32_t v = (uint32_t)q.hist[i] - (uint32_t)base;
-      if (v < (uint32_t)width) {
-        atomicOr(&count[v], kSeen);
-        if (i >= fresh) atomicAdd(&count[v], 1u);
-      }
-    }
+  const int slab = PIECES * 4 * blockDim.x;
+  const int base = blockIdx.x * slab, width = min(slab, vocab - base);
+  uint32_t *count = (uint32_t *)lds, *entry = count + (q.hist_ptr ? slab : 0);
+  uint32_t open[PIECES];  // a bit for each token of a piece
+  four<X> in[PIECES];
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    const int i = 4 * (p * (int)blockDim.x + (int)threadIdx.x);
+    open[p] = 15u;
+    if (q.mask && i < width) open[p] = q.mask[b * q.ldmask + ((base + i) >> 5)] >> ((base + i) & 31) & 15u;
   }
-  int64_t blo = 0, bhi = 0;
-  if (bias) {
-    list_range(q.bias_ptr, q.bias_len, b, blo, bhi);
-    for (int64_t i = blo + threadIdx.x; i < bhi; i += blockDim.x) {
-      const uint32_t v = (uint32_t)q.bias_idx[i] - (uint32_t)base;
-      if (v < (uint32_t)width) atomicMax(&entry[v], (uint32_t)(i - blo) + 1u);
-    }
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    const int i = 4 * (p * (int)blockDim.x + (int)threadIdx.x);
+    in[p] = {};
+    if (open[p] && i < width) in[p] = load_four(logits + b * ld_in + base + i, width - i);
   }
-  __syncthreads();
+
+  int64_t blo = 0;
+  if (q.hist_ptr || q.bias_ptr) {
+    const int words = (q.hist_ptr ? slab : 0) + (q.bias_ptr ? slab : 0);
+    for (int i = threadIdx.x; i < words / 4; i += blockDim.x) lds[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    if (q.hist_ptr) {
+      int64_t lo, hi;
+      list_range(q.hist_ptr, q.hist_len, b, lo, hi);
+      const int64_t fresh = lo + (q.hist_new ? q.hist_new[b] : 0);
+      each_id(q.hist, lo, hi, [&](int64_t at, int32_t id) {
+        const uint32_t v = (uint32_t)id - (uint32_t)base;
+        if (v < (uint32_t)width) {
+          if (at >= fresh) atomicAdd(&count[v], 2u);
+          else atomicOr(&count[v], 1u);
+        }
+      });
+    }
+    if (q.bias_ptr) {
+      int64_t hi;
+      list_range(q.bias_ptr, q.bias_len, b, blo, hi);
+      each_id(q.bias_idx, blo, hi, [&](int64_t at, int32_t id) {
+        const uint32_t v = (uint32_t)id - (uint32_t)base;
+        if (v < (uint32_t)width) atomicMax(&entry[v], (uint32_t)(at - blo) + 1u);
+      });
+    }
+    __syncthreads();
+  }
+
   const float rep = q.repetition ? q.repetition[b] : 1.0f;
   const float freq = q.frequency ? q.frequency[b] : 0.0f, pres = q.presence ? q.presence[b] : 0.0f;
-  for (int i = threadIdx.x; i < width; i += blockDim.x) {
-    const int v = base + i;
-    float l = -__builtin_inff();
-    if (!q.mask || (q.mask[b * q.ldmask + (v >> 5)] >> (v & 31)) & 1u) {
-      l = dbs_value<X>::load(logits + b * ld_in + v);
-      const uint32_t c = count[i];
-      if (c) {
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    const int at = p * (int)blockDim.x + (int)threadIdx.x, i = 4 * at;
+    if (i >= width) continue;
+    uint32_t c[4] = {0u, 0u, 0u, 0u}, e[4] = {0u, 0u, 0u, 0u};
+    if (q.hist_ptr) __builtin_memcpy(c, (const uint4 *)count + at, 16);
+    if (q.bias_ptr) __builtin_memcpy(e, (const uint4 *)entry + at, 16);
+    four<Y> o;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float l = dbs_value<X>::load(&in[p].v[t]);
+      if (c[t]) {
         if (q.repetition) l = l > 0.0f ? l / rep : l * rep;
-        const uint32_t fresh = c & ~kSeen;
-        if (fresh) l -= freq * (float)fresh + pres;
+        if (c[t] > 1u) l -= freq * (float)(c[t] >> 1) + pres;
       }
-      if (entry[i]) l += q.bias_val[blo + entry[i] - 1];
+      if (e[t]) l += q.bias_val[blo + e[t] - 1];
+      if (!(open[p] >> t & 1u)) l = -__builtin_inff();
+      o.v[t] = dbs_value<Y>::of(l);
     }
-    out[b * ld_out + v] = dbs_value<Y>::of(l);
+    store_four(out + b * ld_out + base + i, o, width - i);
   }
 }
 
 template <class X, class Y>
 dbs_status launch_logits(int rows, int vocab, const void *logits, int64_t ld_in, const dbs_logits_params &q, void *out,
                          int64_t ld_out, hipStream_t s) {
-  const unsigned slabs = ((unsigned)vocab + kSlab - 1) / kSlab;
-  hipLaunchKernelGGL((k_logits<X, Y>), dim3(slabs, (unsigned)rows), dim3(256), 0, s, vocab, (const X *)logits, ld_in, q,
-                     (Y *)out, ld_out);
+  // Slabs of 4096 tokens: fewer read the lists.  Where they leave compute units idle, slabs of 1024.
+  const bool small = (int64_t)rows * ((vocab + 4095ll) / 4096) < 512;
+  const int threads = small ? 256 : 512, slab = small ? 1024 : 4096;
+  const size_t lds = (size_t)((q.hist_ptr != nullptr) + (q.bias_ptr != nullptr)) * slab * 4;
+  const dim3 grid((unsigned)(((int64_t)vocab + slab - 1) / slab), (unsigned)rows);
+  const auto kernel = small ? k_logits<X, Y, 1> : k_logits<X, Y, 2>;
+  hipLaunchKernelGGL(kernel, grid, dim3(threads), lds, s, vocab, (const X *)logits, ld_in, q, (Y *)out, ld_out);
   return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
 

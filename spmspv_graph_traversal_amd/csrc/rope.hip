@@ -5,14 +5,20 @@
 
 namespace {
 
-// One workgroup per token.  Its cosines and sines are computed once, in 64
-// bits up to the fraction of a turn (a position times a frequency is many
-// turns; 32 bits would lose its phase), and used by every head.
-template <class X, class Y>
-__global__ __launch_bounds__(256) void k_rope(int heads, int head_dim, int rot_dim, int interleaved,
+/*
+ * Mathematics: a pair (a, b) of a head turns by p = position * freq[i].  Cosine and sine depend on the token and the pair
+ * alone, so a workgroup computes them once per token into LDS and uses them for its heads.  The turn is formed and reduced in 64
+ * bits (a far position is many turns, of which 32 bits would keep no fraction), the sine of its fraction in 32.
+ *
+ * One workgroup per token and `per` heads.  W elements a lane go in 16-byte (bf16: also 8-byte) loads and stores; W = 1
+ * takes any rot_dim and head_dim.  Bound by memory for a prompt, by the chain of loads and the 64-bit product for one
+ * token.
+ */
+template <class X, class Y, int W, bool INTERLEAVED>
+__global__ __launch_bounds__(256) void k_rope(int heads, int per, int head_dim, int rot_dim,
                                               const int32_t *__restrict__ pos, const double *__restrict__ freq,
-                                              float scale, float direction, const X *x, int64_t xt, int64_t xh,
-                                              Y *out, int64_t ot, int64_t oh) {
+                                              float scale, float direction, const X *x, int64_t xt, int64_t xh, Y *out,
+                                              int64_t ot, int64_t oh) {
   __shared__ float2 turn[DBS_ROPE_MAX_DIM / 2];
   const int64_t t = blockIdx.x;
   const int p = pos[t];
@@ -24,35 +30,84 @@ __global__ __launch_bounds__(256) void k_rope(int heads, int head_dim, int rot_d
     sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
     turn[i] = make_float2(scale * c, scale * direction * s);
   }
+  const int h0 = blockIdx.y * per, count = min(per, heads - h0);
+  x += t * xt + h0 * xh;
+  out += t * ot + h0 * oh;
+  // units of a head: W pairs, then W copied elements
+  const int turned = half / W, units = turned + (head_dim - rot_dim) / W;
   __syncthreads();
-  const X *xb = x + t * xt;
-  Y *ob = out + t * ot;
-  const int units = half + (head_dim - rot_dim);  // pairs, then copied elements
-  const int64_t total = (int64_t)heads * units;
-  for (int64_t u = threadIdx.x; u < total; u += blockDim.x) {
-    const int h = (int)(u / units), i = (int)(u % units);
-    const X *xp = xb + h * xh;
-    Y *op = ob + h * oh;
-    if (i < half) {
-      const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + half;
-      const float a = dbs_value<X>::load(xp + ia), b = dbs_value<X>::load(xp + ib);
-      const float2 w = turn[i];
-      op[ia] = dbs_value<Y>::of(a * w.x - b * w.y);
-      op[ib] = dbs_value<Y>::of(a * w.y + b * w.x);
+  for (int u = threadIdx.x; u < count * units; u += blockDim.x) {
+    const int h = u / units, i = u % units;
+    const X *xp = x + h * xh;
+    Y *op = out + h * oh;
+    X a[W], b[W];
+    Y oa[W], ob[W];
+    if (i < turned) {
+      if (INTERLEAVED) {  // 2 W neighbours
+        __builtin_memcpy(a, xp + 2 * W * i, sizeof a);
+        __builtin_memcpy(b, xp + 2 * W * i + W, sizeof b);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float2 w = turn[W * i + e];
+          const int ka = 2 * e, kb = 2 * e + 1;
+          const float va = dbs_value<X>::load(ka < W ? &a[ka % W] : &b[ka % W]);
+          const float vb = dbs_value<X>::load(kb < W ? &a[kb % W] : &b[kb % W]);
+          (ka < W ? oa[ka % W] : ob[ka % W]) = dbs_value<Y>::of(va * w.x - vb * w.y);
+          (kb < W ? oa[kb % W] : ob[kb % W]) = dbs_value<Y>::of(va * w.y + vb * w.x);
+        }
+        __builtin_memcpy(op + 2 * W * i, oa, sizeof oa);
+        __builtin_memcpy(op + 2 * W * i + W, ob, sizeof ob);
+      } else {
+        __builtin_memcpy(a, xp + W * i, sizeof a);
+        __builtin_memcpy(b, xp + half + W * i, sizeof b);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float2 w = turn[W * i + e];
+          const float va = dbs_value<X>::load(&a[e]), vb = dbs_value<X>::load(&b[e]);
+          oa[e] = dbs_value<Y>::of(va * w.x - vb * w.y);
+          ob[e] = dbs_value<Y>::of(va * w.y + vb * w.x);
+        }
+        __builtin_memcpy(op + W * i, oa, sizeof oa);
+        __builtin_memcpy(op + half + W * i, ob, sizeof ob);
+      }
     } else {
-      const int d = rot_dim + (i - half);
-      op[d] = dbs_value<Y>::of(dbs_value<X>::load(xp + d));
+      const int d = rot_dim + W * (i - turned);
+      __builtin_memcpy(a, xp + d, sizeof a);
+#pragma unroll
+      for (int e = 0; e < W; ++e) oa[e] = dbs_value<Y>::of(dbs_value<X>::load(&a[e]));
+      __builtin_memcpy(op + d, oa, sizeof oa);
     }
   }
 }
 
+struct rope_args {
+  int tokens, heads, head_dim, rot_dim;
+  bool interleaved;
+  const int32_t *pos;
+  const double *freq;
+  float scale, direction;
+  const void *x;
+  int64_t xt, xh;
+  void *out;
+  int64_t ot, oh;
+};
+
 template <class X, class Y>
-dbs_status launch_rope(int tokens, int heads, int head_dim, int rot_dim, int layout, const int32_t *pos,
-                       const double *freq, float scale, int inverse, const void *x, int64_t xt, int64_t xh, void *out,
-                       int64_t ot, int64_t oh, hipStream_t s) {
-  hipLaunchKernelGGL((k_rope<X, Y>), dim3((unsigned)tokens), dim3(256), 0, s, heads, head_dim, rot_dim,
-                     layout == DBS_ROPE_INTERLEAVED, pos, freq, scale, inverse ? -1.0f : 1.0f, (const X *)x, xt, xh,
-                     (Y *)out, ot, oh);
+dbs_status launch_rope(const rope_args &r, hipStream_t s) {
+  // eight elements a lane where rotated and copied parts are made of eights
+  const int w = r.rot_dim % 16 == 0 && (r.head_dim - r.rot_dim) % 8 == 0 ? 8 : 1;
+  // All heads of a token share its sines; few tokens are spread over workgroups of 256 lanes by head, or one would do the
+  // work of a chip.
+  const int units = (r.rot_dim / 2 + r.head_dim - r.rot_dim) / w;
+  int per = r.heads;
+  if (r.tokens < 512) per = units >= 256 ? 1 : 256 / units;
+  if (per > r.heads) per = r.heads;
+  if ((r.heads + per - 1) / per > 65535) per = (r.heads + 65534) / 65535;
+  const dim3 grid((unsigned)r.tokens, (unsigned)((r.heads + per - 1) / per));
+  const auto kernel = w == 8 ? (r.interleaved ? k_rope<X, Y, 8, true> : k_rope<X, Y, 8, false>)
+                             : (r.interleaved ? k_rope<X, Y, 1, true> : k_rope<X, Y, 1, false>);
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, r.heads, per, r.head_dim, r.rot_dim, r.pos, r.freq, r.scale,
+                     r.direction, (const X *)r.x, r.xt, r.xh, (Y *)r.out, r.ot, r.oh);
   return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
 
@@ -74,11 +129,12 @@ extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, 
   if (tokens > 1 && ot < head_dim && ot > -(int64_t)head_dim) return DBS_ERR_INVALID_ARG;
   if (x == out && (x_dtype != out_dtype || (tokens > 1 && xt != ot) || (heads > 1 && xh != oh)))
     return DBS_ERR_INVALID_ARG;
-  hipStream_t s = (hipStream_t)stream;
+  const rope_args r = {tokens, heads, head_dim, rot_dim, layout == DBS_ROPE_INTERLEAVED, pos, freq, scale,
+                       inverse ? -1.0f : 1.0f, x, xt, xh, out, ot, oh};
   const bool fx = x_dtype == DBS_F32, fy = out_dtype == DBS_F32;
   auto run = fx ? (fy ? launch_rope<float, float> : launch_rope<float, bf16_bits>)
                 : (fy ? launch_rope<bf16_bits, float> : launch_rope<bf16_bits, bf16_bits>);
-  return run(tokens, heads, head_dim, rot_dim, layout, pos, freq, scale, inverse, x, xt, xh, out, ot, oh, s);
+  return run(r, (hipStream_t)stream);
 }
 
 extern "C" dbs_status dbs_rope_frequencies(const dbs_rope_options *o, double *freq, float *scale) {
