@@ -484,7 +484,7 @@ typedef enum { DBS_ROPE_HALF = 0, DBS_ROPE_INTERLEAVED = 1 } dbs_rope_layout;
  * and the elements from rot_dim on are copied.  p is formed and reduced in
  * 64 bits, so far positions keep their phase.
  *
- *   tokens, heads  >= 0;  head_dim >= 1;  rot_dim even, 0 <= rot_dim <= head_dim
+ *   tokens, heads  >= 0;  head_dim >= 1, heads * head_dim < 2^31;  rot_dim even, 0 <= rot_dim <= head_dim
  *   pos            device int32[tokens]; a negative position marks padding: the token's
  *                  rows of `out` are left as they are
  *   freq           device double[rot_dim/2], radians per position (dbs_rope_frequencies)

@@ -1,7 +1,7 @@
 """ctypes binding of ``libdbs.so`` (declared in ``include/dbs.h``).
 
-Argument marshalling only: every step of the computation runs in the HIP
-library.  Tensors are torch tensors on the current GPU (torch provides the
+Argument marshalling only (that of the decode-step calls in C++, ``csrc/calls.cpp``): every step of the
+computation runs in the HIP library.  Tensors are torch tensors on the current GPU (torch provides the
 device memory and the stream); the functions carry the C names.  Importing
 this module without the built library raises ``ImportError`` — there is no
 fallback.
@@ -121,7 +121,7 @@ def load_library(path: str = LIB_PATH) -> C.CDLL:
         "dbs_q4_product": [vp, i32, vp, C.c_int, i64, vp, C.c_int, i64, vp],
         "dbs_q4_product_masked": [vp, i32, vp, C.c_int, i64, vp, i64, C.c_float, vp, C.c_int, i64, vp],
         "dbs_q4_gated": [vp, vp, C.c_int, i32, vp, C.c_int, i64, vp, C.c_int, i64, vp],
-        "dbs_logits_adjust": [i32, i32, vp, C.c_int, i64, C.POINTER(dbs_logits_params), vp, C.c_int, i64, vp],
+        "dbs_logits_adjust": [i32, i32, vp, C.c_int, i64, C.c_char_p, vp, C.c_int, i64, vp],
         "dbs_rope": [i32, i32, i32, i32, C.c_int, vp, vp, C.c_float, i32, vp, C.c_int, i64, i64, vp, C.c_int, i64,
                      i64, vp],
         "dbs_rope_frequencies": [C.POINTER(dbs_rope_options), C.POINTER(C.c_double), C.POINTER(C.c_float)],
@@ -344,64 +344,21 @@ def dbs_free(A: Matrix) -> None:
 # gradients.
 # ---------------------------------------------------------------------------
 _VECTOR = {_torch.float32: DBS_F32, _torch.bfloat16: DBS_BF16}
-_MASK_DTYPES = (_torch.int32, _torch.uint32)
 
 
-_CURRENT_DEVICE = getattr(_torch._C, "_cuda_getDevice", None) or _torch.cuda.current_device
+def _load_calls():
+    path = os.path.join(_HERE, "_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build the HIP library first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')")
+    from . import _calls
+
+    _calls.bind(*(C.cast(getattr(_lib, f), C.c_void_p).value for f in (
+        "dbs_q4_product", "dbs_q4_product_masked", "dbs_q4_gated", "dbs_logits_adjust", "dbs_rope")))
+    return _calls
 
 
-def _device_of(t, name):
-    """The current device, which `t` must be on (-1 is the CPU)."""
-    if not isinstance(t, _Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    d = t.get_device()
-    if d != _CURRENT_DEVICE():
-        raise ValueError(f"{name} is on device {d}, the current device is {_CURRENT_DEVICE()}")
-    return d
-
-
-def _rows(t, name, width, device):
-    """(rows, dtype code, row stride) of a vector [width] or of rows [rows, width]."""
-    if not isinstance(t, _Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on another device")
-    code = _VECTOR.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2:
-        rows, ld = shape[0], stride[0]
-        if rows == 1:
-            ld = width
-    elif len(shape) == 1:
-        rows, ld = 1, width
-    else:
-        rows = ld = 0
-    if not len(shape) or shape[-1] != width or len(shape) > 2:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{width}] or [tokens, {width}]")
-    if stride[-1] != 1 and width > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if ld < width and rows > 1:
-        raise ValueError(f"{name}: rows overlap (row stride {ld} < {width})")
-    return rows, code, ld
-
-
-def _mask_rows(mask, rows, width, device):
-    words = (width + 31) // 32
-    if not isinstance(mask, _Tensor) or not mask.is_cuda or mask.get_device() != device:
-        raise TypeError("the mask must be a CUDA tensor on the call's device")
-    if mask.dtype not in _MASK_DTYPES:
-        raise TypeError(f"the mask has dtype {mask.dtype}, expected int32 or uint32 words")
-    shape = mask.shape
-    if tuple(shape) != (rows, words) and not (rows == 1 and tuple(shape) == (words,)):
-        raise ValueError(f"the mask has shape {tuple(shape)}, expected [{rows}, {words}]")
-    if mask.stride(-1) != 1 and words > 1:
-        raise ValueError("the mask must have contiguous rows")
-    ld = words if rows == 1 else mask.stride(0)
-    if ld < words:
-        raise ValueError("mask rows overlap")
-    return ld
+_calls = _load_calls()
 
 
 class Q4Matrix:
@@ -428,11 +385,11 @@ def dbs_q4_build(m, n, group, codes, scales, zeros=None, stream=None) -> Q4Matri
     groups = (n + group - 1) // group
     _need(codes, "codes", (_torch.uint8,), m * ((n + 1) // 2))
     _need(scales, "scales", tuple(_VECTOR), m * groups)
-    device = _device_of(codes, "codes")
     if zeros is not None:
         _need(zeros, "zeros", (_torch.uint8,), m * groups)
-    if scales.get_device() != device or (zeros is not None and zeros.get_device() != device):
-        raise ValueError("codes, scales and zeros are on different devices")
+    for t, name in ((codes, "codes"), (scales, "scales"), (zeros, "zeros")):
+        if t is not None and t.get_device() != _torch.cuda.current_device():
+            raise ValueError(f"{name} is not on the current device")
     h = C.c_void_p()
     _check(_lib.dbs_q4_build(m, n, group, _ptr(codes), _ptr(scales), _VECTOR[scales.dtype], _ptr(zeros),
                              _stream(stream, codes.device), C.byref(h)), "dbs_q4_build")
@@ -451,40 +408,25 @@ def dbs_q4_free(A: Q4Matrix) -> None:
         A.handle = C.c_void_p()
 
 
-def _q4_operands(m, n, x, y):
-    device = _device_of(y, "y")
-    tokens, xd, ldx = _rows(x, "x", n, device)
-    ty, yd, ldy = _rows(y, "y", m, device)
-    if tokens != ty:
-        raise ValueError(f"x has {tokens} tokens, y {ty}")
-    return tokens, xd, ldx, yd, ldy, device
-
-
 def dbs_q4_product(A: Q4Matrix, x, y, stream=None) -> None:
     """y[t] = W x[t]; x [n] or [tokens, n], y [m] or [tokens, m], each float32 or bfloat16."""
-    tokens, xd, ldx, yd, ldy, _ = _q4_operands(A.m, A.n, x, y)
-    st = _lib.dbs_q4_product(A.handle, tokens, x.data_ptr(), xd, ldx, y.data_ptr(), yd, ldy, _stream(stream, y.device))
-    if st != DBS_OK:
+    st = _calls.q4_product(A.handle.value, A.m, A.n, x, y, stream)
+    if st:
         raise DBSError(st, "dbs_q4_product")
 
 
 def dbs_q4_product_masked(A: Q4Matrix, x, row_mask, y, fill: float = float("-inf"), stream=None) -> None:
     """dbs_q4_product for the rows whose bit is set in row_mask (int32 words [tokens, ceil(m/32)]), `fill`
     elsewhere."""
-    tokens, xd, ldx, yd, ldy, device = _q4_operands(A.m, A.n, x, y)
-    ldmask = _mask_rows(row_mask, tokens, A.m, device)
-    st = _lib.dbs_q4_product_masked(A.handle, tokens, x.data_ptr(), xd, ldx, row_mask.data_ptr(), ldmask, float(fill),
-                                    y.data_ptr(), yd, ldy, _stream(stream, y.device))
-    if st != DBS_OK:
+    st = _calls.q4_product_masked(A.handle.value, A.m, A.n, x, row_mask, fill, y, stream)
+    if st:
         raise DBSError(st, "dbs_q4_product_masked")
 
 
 def dbs_q4_gated(G: Q4Matrix, U: Q4Matrix, x, activation: int, y, stream=None) -> None:
     """y[t] = act(G x[t]) * (U x[t]) for two matrices of one shape, group and scale type."""
-    tokens, xd, ldx, yd, ldy, _ = _q4_operands(G.m, G.n, x, y)
-    st = _lib.dbs_q4_gated(G.handle, U.handle, int(activation), tokens, x.data_ptr(), xd, ldx, y.data_ptr(), yd, ldy,
-                           _stream(stream, y.device))
-    if st != DBS_OK:
+    st = _calls.q4_gated(G.handle.value, U.handle.value, G.m, G.n, x, activation, y, stream)
+    if st:
         raise DBSError(st, "dbs_q4_gated")
 
 
@@ -493,69 +435,10 @@ def dbs_logits_adjust(logits, out, hist_ptr=None, hist=None, hist_new=None, repe
     """Penalties for repeated tokens, sparse biases and a bit mask on rows of logits ([vocab] or [rows, vocab]);
     `out` may be `logits`.  Lists are ragged: row b's history is hist[hist_ptr[b]:hist_ptr[b + 1]], of which the
     entries from hist_new[b] on count for frequency and presence; its biases likewise."""
-    device = _device_of(out, "out")
-    if not isinstance(logits, _Tensor) or logits.dim() not in (1, 2):
-        raise ValueError("logits must be [vocab] or [rows, vocab]")
-    vocab = logits.shape[-1]
-    rows, ind, ld_in = _rows(logits, "logits", vocab, device)
-    orows, outd, ld_out = _rows(out, "out", vocab, device)
-    if orows != rows:
-        raise ValueError(f"logits have {rows} rows, out {orows}")
-    p = dbs_logits_params()
-
-    def given(t, name, dtypes, numel):
-        if not isinstance(t, _Tensor) or t.get_device() != device:
-            raise TypeError(f"{name} must be a CUDA tensor on the call's device")
-        if t.dtype not in dtypes or not t.is_contiguous():
-            raise TypeError(f"{name} must be contiguous {dtypes[0]}")
-        if numel is not None and t.numel() != numel:
-            raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-        return t.data_ptr()
-
-    if (hist_ptr is None) != (hist is None):
-        raise ValueError("hist_ptr and hist go together")
-    if (bias_ptr is None) != (bias_idx is None) or (bias_idx is None) != (bias_val is None):
-        raise ValueError("bias_ptr, bias_idx and bias_val go together")
-    if hist is not None:
-        p.hist_ptr = given(hist_ptr, "hist_ptr", _I32, rows + 1)
-        p.hist = given(hist, "hist", _I32, None)
-        p.hist_len = hist.numel()
-    if hist_new is not None:
-        p.hist_new = given(hist_new, "hist_new", _I32, rows)
-    if repetition is not None:
-        p.repetition = given(repetition, "repetition", _F32, rows)
-    if frequency is not None:
-        p.frequency = given(frequency, "frequency", _F32, rows)
-    if presence is not None:
-        p.presence = given(presence, "presence", _F32, rows)
-    if bias_idx is not None:
-        p.bias_ptr = given(bias_ptr, "bias_ptr", _I32, rows + 1)
-        p.bias_idx = given(bias_idx, "bias_idx", _I32, None)
-        p.bias_len = bias_idx.numel()
-        p.bias_val = given(bias_val, "bias_val", _F32, p.bias_len)
-    if mask is not None:
-        p.ldmask = _mask_rows(mask, rows, vocab, device)
-        p.mask = mask.data_ptr()
-    st = _lib.dbs_logits_adjust(rows, vocab, logits.data_ptr(), ind, ld_in, C.byref(p), out.data_ptr(), outd, ld_out,
-                                _stream(stream, out.device))
-    if st != DBS_OK:
+    st = _calls.logits_adjust(logits, out, hist_ptr, hist, hist_new, repetition, frequency, presence, bias_ptr, bias_idx,
+                              bias_val, mask, stream)
+    if st:
         raise DBSError(st, "dbs_logits_adjust")
-
-
-def _heads(t, name, device):
-    if not isinstance(t, _Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    code = _VECTOR.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on another device")
-    st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name} must have contiguous heads")
-    return code, st, sh
 
 
 def dbs_rope(x, pos, freq, out, layout: int = DBS_ROPE_HALF, scale: float = 1.0, inverse: bool = False,
@@ -563,20 +446,8 @@ def dbs_rope(x, pos, freq, out, layout: int = DBS_ROPE_HALF, scale: float = 1.0,
     """Rotary positions on x [tokens, heads, head_dim] (any token and head stride) into `out`, which may be x:
     the first 2 * freq.numel() elements of each head are rotated by pos[token] * freq (int32 positions, float64
     frequencies, dbs_rope_frequencies), the others copied; tokens of negative position are left alone."""
-    device = _device_of(out, "out")
-    xd, xt, xh = _heads(x, "x", device)
-    od, ot, oh = _heads(out, "out", device)
-    tokens, heads, dim = x.shape
-    if out.shape != x.shape:
-        raise ValueError(f"x has shape {tuple(x.shape)}, out {tuple(out.shape)}")
-    _need(pos, "pos", _I32, tokens)
-    _need(freq, "freq", (_torch.float64,))
-    if pos.get_device() != device or freq.get_device() != device:
-        raise ValueError("pos and freq are on another device")
-    st = _lib.dbs_rope(tokens, heads, dim, 2 * freq.numel(), int(layout), pos.data_ptr(), freq.data_ptr(), float(scale),
-                       1 if inverse else 0, x.data_ptr(), xd, xt, xh, out.data_ptr(), od, ot, oh,
-                       _stream(stream, out.device))
-    if st != DBS_OK:
+    st = _calls.rope(x, pos, freq, out, layout, scale, inverse, stream)
+    if st:
         raise DBSError(st, "dbs_rope")
 
 

@@ -1,4 +1,4 @@
-"""Compile the HIP library ``libdbs.so`` for gfx950 with hipcc.
+"""Compile the HIP library ``libdbs.so`` for gfx950 with hipcc, and the binding's compiled part with the host compiler.
 
 Run ``python -m spmspv_graph_traversal_amd.build_lib`` (the repository's
 ``build()`` calls :func:`build`).  Objects go to ``_build/`` next to this file,
@@ -15,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdbs.so")
+CALLS = os.path.join(HERE, "_calls.so")  # argument marshalling of the decode-step calls (csrc/calls.cpp)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -48,10 +49,32 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_calls() -> None:
+    import sysconfig
+
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    tmp = CALLS + ".tmp"
+    # the macros tell torch's headers which device backend it was built with
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-I" + os.path.join(at, "include"), "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(rocm, "include"), "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "calls.cpp"), "-o", tmp, "-L" + os.path.join(at, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"calls.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(_compile, SOURCES))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-mcode-object-version=5", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -59,7 +82,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {CALLS}")
     return LIB
 
 

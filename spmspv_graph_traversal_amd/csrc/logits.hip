@@ -3,45 +3,75 @@
 
 namespace {
 
-// the part [lo, hi) of list `b`, clamped to the list's length
-DBS_DEV void list_range(const int32_t *ptr, int64_t len, int64_t b, int64_t &lo, int64_t &hi) {
-  lo = ptr[b] < 0 ? 0 : ptr[b];
-  hi = ptr[b + 1] > len ? len : ptr[b + 1];
+// read in place of an absent list's pointers or an absent row value
+__device__ const uint32_t kNothing = 0u;
+
+template <class T>
+DBS_DEV T or_nothing(const T *p, int64_t i) {
+  typedef const T __attribute__((address_space(1))) *global;
+  const global g = p ? (global)(p + i) : (global)(const T *)&kNothing;
+  return *g;
 }
 
-// calls use(position, id) for the list's entries [lo, hi), four to a load
-template <class F>
-DBS_DEV void each_id(const int32_t *list, int64_t lo, int64_t hi, F use) {
-  const int64_t step = 4 * blockDim.x;
-  int64_t i = lo + 4 * threadIdx.x;
-  for (; i + 4 <= hi; i += step) {
-    int32_t v[4];
-    __builtin_memcpy(v, list + i, 16);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) use(i + e, v[e]);
-  }
-  for (; i < hi; ++i) use(i, list[i]);  // of one thread: the list's last one to three
-}
-
+// Four neighbours, at any alignment of their type.  A vector type: from an array the compiler makes four accesses, of which it
+// joins those that the cut case below does not share.
 template <class T>
 struct four {
-  T v[4];
+  typedef T type __attribute__((ext_vector_type(4)));
+  typedef T at_any __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+  type v;
+  DBS_DEV void load(const T *p, int count) {
+    if (count >= 4) v = *(const at_any *)p;
+    else
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < count) v[e] = p[e];
+  }
+  DBS_DEV void store(T *p, int count) const {
+    if (count >= 4) *(at_any *)p = v;
+    else
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < count) p[e] = v[e];
+  }
 };
-// entries [0, count) of four values at p
-template <class T>
-DBS_DEV four<T> load_four(const T *p, int count) {
-  four<T> f = {};
-  if (count >= 4) __builtin_memcpy(&f, p, sizeof f);
-  else
-    for (int e = 0; e < count; ++e) f.v[e] = p[e];
-  return f;
-}
-template <class T>
-DBS_DEV void store_four(T *p, const four<T> &f, int count) {
-  if (count >= 4) __builtin_memcpy(p, &f, sizeof f);
-  else
-    for (int e = 0; e < count; ++e) p[e] = f.v[e];
-}
+
+// The entries [lo, hi) of a list by all threads, four neighbours to a load; the first AHEAD rounds' loads come before
+// whatever stands between fetch() and each().
+template <int AHEAD>
+struct id_list {
+  const int32_t *list;
+  int64_t lo, hi;
+  four<int32_t> v[AHEAD];
+
+  // row b's part, clamped to the list's length
+  DBS_DEV id_list(const int32_t *ids, const int32_t *ptr, int64_t len, int64_t b) : list(ids) {
+    const int32_t first = or_nothing(ptr, b), end = or_nothing(ptr, b + 1);
+    lo = first < 0 ? 0 : first;
+    hi = end > len ? len : end;
+  }
+  DBS_DEV int64_t at(int round) const { return lo + 4 * ((int64_t)round * blockDim.x + threadIdx.x); }
+  DBS_DEV int left(int64_t i) const { return (int)(hi - i < 4 ? hi - i : 4); }
+  DBS_DEV void fetch() {
+#pragma unroll
+    for (int r = 0; r < AHEAD; ++r) v[r].load(list + at(r), left(at(r)));
+  }
+  template <class F>
+  DBS_DEV void each(F use) const {
+    auto round = [&](const four<int32_t> &ids, int64_t i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < hi) use(i + e, ids.v[e]);
+    };
+#pragma unroll
+    for (int r = 0; r < AHEAD; ++r) round(v[r], at(r));
+    for (int r = AHEAD; at(r) < hi; ++r) {
+      four<int32_t> ids;
+      ids.load(list + at(r), left(at(r)));
+      round(ids, at(r));
+    }
+  }
+};
 
 /*
  * One workgroup per row and slab of the vocabulary, four neighbouring tokens to a thread PIECES times.
@@ -51,8 +81,8 @@ DBS_DEV void store_four(T *p, const four<T> &f, int count) {
  * in every call.  A word holds twice the count of the generated entries, and an odd word or a count means that the id was
  * seen.  The bias of an id that comes twice is its last entry's: the slab keeps the highest entry number.
  *
- * Bound by memory: logits read and written once; the lists come from L2 for every slab.  The logits are loaded before the
- * lists are gone through, so that their way from memory is no wait; those that a mask closes are not read at all.
+ * Bound by memory, if a workgroup's chain of loads is kept short: first the logits or, with a mask, its words (logits that
+ * it closes are not read at all), the row's scalars at once, the lists, and only then the counting.
  */
 template <class X, class Y, int PIECES>
 __global__ __launch_bounds__(512) void k_logits(int vocab, const X *logits, int64_t ld_in, dbs_logits_params q, Y *out,
@@ -62,51 +92,50 @@ __global__ __launch_bounds__(512) void k_logits(int vocab, const X *logits, int6
   const int slab = PIECES * 4 * blockDim.x;
   const int base = blockIdx.x * slab, width = min(slab, vocab - base);
   uint32_t *count = (uint32_t *)lds, *entry = count + (q.hist_ptr ? slab : 0);
+
   uint32_t open[PIECES];  // a bit for each token of a piece
   four<X> in[PIECES];
+  auto fetch_logits = [&]() {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const int i = 4 * (p * (int)blockDim.x + (int)threadIdx.x);
+      in[p].v = 0;
+      if (open[p]) in[p].load(logits + b * ld_in + base + i, width - i);
+    }
+  };
 #pragma unroll
   for (int p = 0; p < PIECES; ++p) {
     const int i = 4 * (p * (int)blockDim.x + (int)threadIdx.x);
-    open[p] = 15u;
+    open[p] = i < width ? 15u : 0u;
     if (q.mask && i < width) open[p] = q.mask[b * q.ldmask + ((base + i) >> 5)] >> ((base + i) & 31) & 15u;
   }
-#pragma unroll
-  for (int p = 0; p < PIECES; ++p) {
-    const int i = 4 * (p * (int)blockDim.x + (int)threadIdx.x);
-    in[p] = {};
-    if (open[p] && i < width) in[p] = load_four(logits + b * ld_in + base + i, width - i);
-  }
-
-  int64_t blo = 0;
+  if (!q.mask) fetch_logits();
+  id_list<2> hist(q.hist, q.hist_ptr, q.hist_len, b);
+  id_list<1> bias(q.bias_idx, q.bias_ptr, q.bias_len, b);
+  const int64_t fresh = hist.lo + or_nothing(q.hist_new, b);
+  const float rep = or_nothing(q.repetition, b);
+  const float freq = or_nothing(q.frequency, b), pres = or_nothing(q.presence, b);
+  hist.fetch();
+  bias.fetch();
   if (q.hist_ptr || q.bias_ptr) {
     const int words = (q.hist_ptr ? slab : 0) + (q.bias_ptr ? slab : 0);
     for (int i = threadIdx.x; i < words / 4; i += blockDim.x) lds[i] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-    if (q.hist_ptr) {
-      int64_t lo, hi;
-      list_range(q.hist_ptr, q.hist_len, b, lo, hi);
-      const int64_t fresh = lo + (q.hist_new ? q.hist_new[b] : 0);
-      each_id(q.hist, lo, hi, [&](int64_t at, int32_t id) {
-        const uint32_t v = (uint32_t)id - (uint32_t)base;
-        if (v < (uint32_t)width) {
-          if (at >= fresh) atomicAdd(&count[v], 2u);
-          else atomicOr(&count[v], 1u);
-        }
-      });
-    }
-    if (q.bias_ptr) {
-      int64_t hi;
-      list_range(q.bias_ptr, q.bias_len, b, blo, hi);
-      each_id(q.bias_idx, blo, hi, [&](int64_t at, int32_t id) {
-        const uint32_t v = (uint32_t)id - (uint32_t)base;
-        if (v < (uint32_t)width) atomicMax(&entry[v], (uint32_t)(at - blo) + 1u);
-      });
-    }
-    __syncthreads();
   }
+  if (q.mask) fetch_logits();
+  dbs_barrier_lds();
+  hist.each([&](int64_t at, int32_t id) {
+    const uint32_t v = (uint32_t)id - (uint32_t)base;
+    if (v < (uint32_t)width) {
+      if (at >= fresh) atomicAdd(&count[v], 2u);
+      else atomicOr(&count[v], 1u);
+    }
+  });
+  bias.each([&](int64_t at, int32_t id) {
+    const uint32_t v = (uint32_t)id - (uint32_t)base;
+    if (v < (uint32_t)width) atomicMax(&entry[v], (uint32_t)(at - bias.lo) + 1u);
+  });
+  dbs_barrier_lds();
 
-  const float rep = q.repetition ? q.repetition[b] : 1.0f;
-  const float freq = q.frequency ? q.frequency[b] : 0.0f, pres = q.presence ? q.presence[b] : 0.0f;
 #pragma unroll
   for (int p = 0; p < PIECES; ++p) {
     const int at = p * (int)blockDim.x + (int)threadIdx.x, i = 4 * at;
@@ -117,16 +146,17 @@ __global__ __launch_bounds__(512) void k_logits(int vocab, const X *logits, int6
     four<Y> o;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      float l = dbs_value<X>::load(&in[p].v[t]);
+      const X raw = in[p].v[t];
+      float l = dbs_value<X>::load(&raw);
       if (c[t]) {
         if (q.repetition) l = l > 0.0f ? l / rep : l * rep;
         if (c[t] > 1u) l -= freq * (float)(c[t] >> 1) + pres;
       }
-      if (e[t]) l += q.bias_val[blo + e[t] - 1];
+      if (e[t]) l += q.bias_val[bias.lo + e[t] - 1];
       if (!(open[p] >> t & 1u)) l = -__builtin_inff();
       o.v[t] = dbs_value<Y>::of(l);
     }
-    store_four(out + b * ld_out + base + i, o, width - i);
+    o.store(out + b * ld_out + base + i, width - i);
   }
 }
 

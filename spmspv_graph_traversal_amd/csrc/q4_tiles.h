@@ -135,13 +135,6 @@ __device__ __noinline__ float row_dot(const uint32_t *codes, const uint32_t *rec
   return sum;
 }
 
-// a barrier that waits for LDS only, not for loads from memory in flight
-DBS_DEV void barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // LDS written by lanes of a wave and read by others of it: in order, no barrier
 DBS_DEV void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
@@ -411,7 +404,7 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k
   // again has passed a barrier since its readers were done.
   auto block = [&](int d) {
     put_x(d);
-    if (RW > 1) barrier();
+    if (RW > 1) dbs_barrier_lds();
     else wave_fence();
     multiply(d);
     if (RW == 1) wave_fence();
@@ -448,7 +441,7 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k
     }
   }
   if (whole < q.kt) {  // the block that n ends in: the first split's
-    barrier();
+    dbs_barrier_lds();
     if (split == 0) {
       fetch_codes(0, whole, q.kt);
 #pragma unroll
@@ -456,7 +449,7 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k
         xr[0][i].load_cut(from[i] - piece * x_piece<X>::columns, whole * Q4_COLS + piece * x_piece<X>::columns, q.n);
       put_x(0);
     }
-    barrier();
+    dbs_barrier_lds();
     if (split == 0) multiply(0);
   }
 

@@ -10,12 +10,51 @@ namespace {
  * alone, so a workgroup computes them once per token into LDS and uses them for its heads.  The turn is formed and reduced in 64
  * bits (a far position is many turns, of which 32 bits would keep no fraction), the sine of its fraction in 32.
  *
- * One workgroup per token and `per` heads.  W elements a lane go in 16-byte (bf16: also 8-byte) loads and stores; W = 1
- * takes any rot_dim and head_dim.  Bound by memory for a prompt, by the chain of loads and the 64-bit product for one
- * token.
+ * One workgroup per token and `per` heads, W pairs or W copied elements to a lane at a time.  W = 8 makes loads and stores of
+ * 16 bytes, W = 1 takes any rot_dim and head_dim.  Bound by memory for a prompt; x is loaded before the sines, so that a token's
+ * chain is not position, frequencies, sines and then x.
  */
 template <class X, class Y, int W, bool INTERLEAVED>
-__global__ __launch_bounds__(256) void k_rope(int heads, int per, int head_dim, int rot_dim,
+struct rope_unit {
+  X a[W], b[W];  // half layout: first and second elements of W pairs; interleaved: 2 W neighbours
+  int h, i;
+
+  DBS_DEV void load(const X *x, int64_t xh, int u, int units, int turned, int half) {
+    h = u / units;
+    i = u % units;
+    const X *p = x + h * xh;
+    if (i < turned) {
+      __builtin_memcpy(a, p + (INTERLEAVED ? 2 * W * i : W * i), sizeof a);
+      __builtin_memcpy(b, p + (INTERLEAVED ? 2 * W * i + W : half + W * i), sizeof b);
+    } else {
+      __builtin_memcpy(a, p + 2 * half + W * (i - turned), sizeof a);
+    }
+  }
+  DBS_DEV void store(Y *out, int64_t oh, const float2 *turn, int turned, int half) const {
+    Y oa[W], ob[W];
+    Y *p = out + h * oh;
+    if (i < turned) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float2 w = turn[W * i + e];
+        const int ka = INTERLEAVED ? 2 * e : e, kb = INTERLEAVED ? 2 * e + 1 : W + e;  // within a, b
+        const float va = dbs_value<X>::load(ka < W ? &a[ka % W] : &b[ka % W]);
+        const float vb = dbs_value<X>::load(kb < W ? &a[kb % W] : &b[kb % W]);
+        (ka < W ? oa[ka % W] : ob[ka % W]) = dbs_value<Y>::of(va * w.x - vb * w.y);
+        (kb < W ? oa[kb % W] : ob[kb % W]) = dbs_value<Y>::of(va * w.y + vb * w.x);
+      }
+      __builtin_memcpy(p + (INTERLEAVED ? 2 * W * i : W * i), oa, sizeof oa);
+      __builtin_memcpy(p + (INTERLEAVED ? 2 * W * i + W : half + W * i), ob, sizeof ob);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) oa[e] = dbs_value<Y>::of(dbs_value<X>::load(&a[e]));
+      __builtin_memcpy(p + 2 * half + W * (i - turned), oa, sizeof oa);
+    }
+  }
+};
+
+template <class X, class Y, int W, bool INTERLEAVED>
+__global__ __launch_bounds__(512) void k_rope(int heads, int per, int head_dim, int rot_dim,
                                               const int32_t *__restrict__ pos, const double *__restrict__ freq,
                                               float scale, float direction, const X *x, int64_t xt, int64_t xh, Y *out,
                                               int64_t ot, int64_t oh) {
@@ -23,60 +62,24 @@ __global__ __launch_bounds__(256) void k_rope(int heads, int per, int head_dim, 
   const int64_t t = blockIdx.x;
   const int p = pos[t];
   if (p < 0) return;
-  const int half = rot_dim / 2;
+  const int half = rot_dim / 2, h0 = blockIdx.y * per, count = min(per, heads - h0);
+  x += t * xt + h0 * xh;
+  out += t * ot + h0 * oh;
+  const int turned = half / W, units = turned + (head_dim - rot_dim) / W, all = count * units;
+  rope_unit<X, Y, W, INTERLEAVED> now;
+  int u = threadIdx.x;
+  if (u < all) now.load(x, xh, u, units, turned, half);
   for (int i = threadIdx.x; i < half; i += blockDim.x) {
     const double turns = (double)p * freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
     float s, c;
     sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
     turn[i] = make_float2(scale * c, scale * direction * s);
   }
-  const int h0 = blockIdx.y * per, count = min(per, heads - h0);
-  x += t * xt + h0 * xh;
-  out += t * ot + h0 * oh;
-  // units of a head: W pairs, then W copied elements
-  const int turned = half / W, units = turned + (head_dim - rot_dim) / W;
-  __syncthreads();
-  for (int u = threadIdx.x; u < count * units; u += blockDim.x) {
-    const int h = u / units, i = u % units;
-    const X *xp = x + h * xh;
-    Y *op = out + h * oh;
-    X a[W], b[W];
-    Y oa[W], ob[W];
-    if (i < turned) {
-      if (INTERLEAVED) {  // 2 W neighbours
-        __builtin_memcpy(a, xp + 2 * W * i, sizeof a);
-        __builtin_memcpy(b, xp + 2 * W * i + W, sizeof b);
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const float2 w = turn[W * i + e];
-          const int ka = 2 * e, kb = 2 * e + 1;
-          const float va = dbs_value<X>::load(ka < W ? &a[ka % W] : &b[ka % W]);
-          const float vb = dbs_value<X>::load(kb < W ? &a[kb % W] : &b[kb % W]);
-          (ka < W ? oa[ka % W] : ob[ka % W]) = dbs_value<Y>::of(va * w.x - vb * w.y);
-          (kb < W ? oa[kb % W] : ob[kb % W]) = dbs_value<Y>::of(va * w.y + vb * w.x);
-        }
-        __builtin_memcpy(op + 2 * W * i, oa, sizeof oa);
-        __builtin_memcpy(op + 2 * W * i + W, ob, sizeof ob);
-      } else {
-        __builtin_memcpy(a, xp + W * i, sizeof a);
-        __builtin_memcpy(b, xp + half + W * i, sizeof b);
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const float2 w = turn[W * i + e];
-          const float va = dbs_value<X>::load(&a[e]), vb = dbs_value<X>::load(&b[e]);
-          oa[e] = dbs_value<Y>::of(va * w.x - vb * w.y);
-          ob[e] = dbs_value<Y>::of(va * w.y + vb * w.x);
-        }
-        __builtin_memcpy(op + W * i, oa, sizeof oa);
-        __builtin_memcpy(op + half + W * i, ob, sizeof ob);
-      }
-    } else {
-      const int d = rot_dim + W * (i - turned);
-      __builtin_memcpy(a, xp + d, sizeof a);
-#pragma unroll
-      for (int e = 0; e < W; ++e) oa[e] = dbs_value<Y>::of(dbs_value<X>::load(&a[e]));
-      __builtin_memcpy(op + d, oa, sizeof oa);
-    }
+  dbs_barrier_lds();
+  if (u < all) now.store(out, oh, turn, turned, half);
+  for (u += blockDim.x; u < all; u += blockDim.x) {
+    now.load(x, xh, u, units, turned, half);
+    now.store(out, oh, turn, turned, half);
   }
 }
 
@@ -102,11 +105,14 @@ dbs_status launch_rope(const rope_args &r, hipStream_t s) {
   int per = r.heads;
   if (r.tokens < 512) per = units >= 256 ? 1 : 256 / units;
   if (per > r.heads) per = r.heads;
-  if ((r.heads + per - 1) / per > 65535) per = (r.heads + 65534) / 65535;
+  if (per < (r.heads + 65534) / 65535) per = (r.heads + 65534) / 65535;  // the grid's limit
+  // rounds of at most 512 lanes, all nearly full
+  const int64_t all = (int64_t)per * units, rounds = (all + 511) / 512;
+  const int threads = (int)((all + rounds * 64 - 1) / (rounds * 64)) * 64;
   const dim3 grid((unsigned)r.tokens, (unsigned)((r.heads + per - 1) / per));
   const auto kernel = w == 8 ? (r.interleaved ? k_rope<X, Y, 8, true> : k_rope<X, Y, 8, false>)
                              : (r.interleaved ? k_rope<X, Y, 1, true> : k_rope<X, Y, 1, false>);
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, r.heads, per, r.head_dim, r.rot_dim, r.pos, r.freq, r.scale,
+  hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, r.heads, per, r.head_dim, r.rot_dim, r.pos, r.freq, r.scale,
                      r.direction, (const X *)r.x, r.xt, r.xh, (Y *)r.out, r.ot, r.oh);
   return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
@@ -121,7 +127,7 @@ extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, 
     return DBS_ERR_INVALID_ARG;
   if (layout != DBS_ROPE_HALF && layout != DBS_ROPE_INTERLEAVED) return DBS_ERR_INVALID_ARG;
   if (!dbs_is_vector_dtype(x_dtype) || !dbs_is_vector_dtype(out_dtype)) return DBS_ERR_INVALID_ARG;
-  if (rot_dim > DBS_ROPE_MAX_DIM) return DBS_ERR_UNSUPPORTED;
+  if (rot_dim > DBS_ROPE_MAX_DIM || (int64_t)heads * head_dim > INT32_MAX) return DBS_ERR_UNSUPPORTED;
   if (tokens == 0 || heads == 0) return DBS_OK;
   if (!pos || (rot_dim > 0 && !freq) || !x || !out) return DBS_ERR_INVALID_ARG;
   // rows of one output may not overlap each other, and an in-place call reads what it writes

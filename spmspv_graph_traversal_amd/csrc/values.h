@@ -33,3 +33,10 @@ inline bool dbs_overlap(const void *a, int64_t abytes, const void *b, int64_t bb
   const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
   return abytes > 0 && bbytes > 0 && p < q + (uintptr_t)bbytes && q < p + (uintptr_t)abytes;
 }
+
+// a barrier that waits for LDS only, not for loads from memory in flight
+DBS_DEV void dbs_barrier_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}

@@ -35,7 +35,7 @@ def test_q4_calls_without_a_handle():
 
 def logits(rows=2, vocab=40, x=P, xd=0, ldx=40, out=2 * P, od=0, ldo=40, params=True, **fields):
     p = b.dbs_logits_params(**fields)
-    return _lib.dbs_logits_adjust(rows, vocab, x, xd, ldx, C.byref(p) if params else None, out, od, ldo, None)
+    return _lib.dbs_logits_adjust(rows, vocab, x, xd, ldx, bytes(p) if params else None, out, od, ldo, None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -74,6 +74,7 @@ def test_rope_limits_and_nothing_to_do():
     assert rope(tokens=0, pos=None, freq=None, x=None, out=None) == OK
     assert rope(heads=0) == OK
     assert rope(dim=2048, rot=1026, oh=2048, ot=3 * 2048) == UNSUPPORTED
+    assert rope(heads=1 << 20, dim=1 << 11, oh=1 << 11, ot=1 << 31) == UNSUPPORTED
 
 
 def frequencies(**kw):

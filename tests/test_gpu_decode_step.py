@@ -521,3 +521,45 @@ def test_decode_step(dbs):
     same_kind(host(logit), want)
     fine = np.isfinite(want)
     assert (np.abs(host(logit)[fine] - want[fine]) <= 4 * ref.U24 * np.abs(raw[fine]) * 1.3).all()
+
+
+# --------------------------------------------------------------------------- refusals by the binding
+def test_refusals_of_tensors(dbs):
+    import torch
+
+    rng = np.random.default_rng(80)
+    A, B = ref.Q4(rng, 20, 64, 32, False).build(dbs), ref.Q4(rng, 20, 64, 64, False).build(dbs)
+    x, y = torch.zeros(3, 64, device="cuda"), torch.full((3, 20), 5.0, device="cuda")
+    z = torch.zeros(3, 128, device="cuda")
+    for error, call in (
+            (ValueError, lambda: dbs.dbs_q4_product(A, x[:2], y)),
+            (ValueError, lambda: dbs.dbs_q4_product(A, x[:, :63], y)),
+            (ValueError, lambda: dbs.dbs_q4_product(A, z[:, ::2], y)),
+            (ValueError, lambda: dbs.dbs_q4_product(A, x[:1].expand(3, 64), y)),
+            (ValueError, lambda: dbs.dbs_q4_product(A, x[None], y)),
+            (TypeError, lambda: dbs.dbs_q4_product(A, x.half(), y)),
+            (TypeError, lambda: dbs.dbs_q4_product(A, x.cpu(), y)),
+            (TypeError, lambda: dbs.dbs_q4_product(A, x, None)),
+            (AttributeError, lambda: dbs.dbs_q4_product(A, x, y, stream=5)),
+            (dbs.DBSError, lambda: dbs.dbs_q4_product(A, z.view(-1)[:64], z.view(-1)[60:80])),  # overlapping
+            (dbs.DBSError, lambda: dbs.dbs_q4_gated(A, B, x, dbs.DBS_ACT_RELU, y)),  # two group sizes
+            (dbs.DBSError, lambda: dbs.dbs_q4_gated(A, A, x, 3, y)),
+            (ValueError, lambda: dbs.dbs_q4_product_masked(A, x, torch.zeros(3, 2, dtype=torch.int32, device="cuda"), y)),
+            (TypeError, lambda: dbs.dbs_q4_product_masked(A, x, torch.zeros(3, 1, dtype=torch.int64, device="cuda"), y)),
+            (ValueError, lambda: dbs.dbs_logits_adjust(y, y, hist=torch.zeros(2, dtype=torch.int32, device="cuda"))),
+            (ValueError, lambda: dbs.dbs_logits_adjust(y, x[:, :20][:2])),
+            (TypeError, lambda: dbs.dbs_logits_adjust(y, y, repetition=torch.zeros(3, dtype=torch.float64, device="cuda"))),
+            (dbs.DBSError, lambda: dbs.dbs_logits_adjust(y, y, repetition=torch.ones(3, device="cuda"))),  # of no history
+            (dbs.DBSError, lambda: dbs.dbs_q4_product(A, x, x[:, :20])),  # into x
+            (ValueError, lambda: dbs.dbs_rope(x, x, x, x)),
+            (TypeError, lambda: dbs.dbs_rope(x[:, None], torch.zeros(3, dtype=torch.int64, device="cuda"), torch.zeros(2, dtype=torch.float64, device="cuda"), x[:, None])),
+            (dbs.DBSError, lambda: dbs.dbs_rope(x[:, None], torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(33, dtype=torch.float64, device="cuda"), x[:, None])),
+            (ValueError, lambda: dbs.dbs_q4_build(20, 64, 48, torch.zeros(20, 32, dtype=torch.uint8, device="cuda"), x[:, :2])),
+            (dbs.DBSError, lambda: dbs.dbs_q4_build(3, 64, 64, torch.zeros(3, 32, dtype=torch.uint8, device="cuda"), torch.ones(3, 1, device="cuda"), torch.full((3, 1), 16, dtype=torch.uint8, device="cuda")))):
+        with pytest.raises(error):
+            call()
+    dbs.dbs_q4_free(A)
+    with pytest.raises(dbs.DBSError):
+        dbs.dbs_q4_product(A, x, y)  # a freed matrix
+    torch.cuda.synchronize()
+    assert (y == 5).all() and (x == 0).all()
