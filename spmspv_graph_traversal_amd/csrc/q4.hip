@@ -61,27 +61,29 @@ __global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int
 }
 
 /*
- * How a call is cut, from times of graphs of launches (us; rows x columns, 128 columns a group unless noted).
- *   One to four tokens.  Few row blocks need every wave that shares one (eight splits): 4096 x 4096, one token, 4.1
- *   against 4.5 with four splits.  With more row blocks than that fills the chip with, four splits do (11008 x 4096
- *   6.9 against 7.1), and from 2048 on two row blocks a wave keep more bytes in flight for the same waves (65536 x
- *   4096 26.2 against 29.2).  Under a mask one row block is the unit: 256 of 65536 rows wanted 6.6 against 8.1.
- *   More tokens, 16 at a time.  Up to 512 workgroups of one row block: one row block, eight splits (4096 x 4096, 16 tokens, 5.4
- *   against 8.2).  Else four row blocks that share x (11008 x 4096, 16 tokens, 8.7 against 9.9; fp32 13.9 against 20.4; gated
- *   12.6 against 13.0), with two splits once that fills the chip (64 tokens 19.1 against 20.0).
+ * How a call is cut, from times of graphs of launches (us; rows x columns).
+ *   One to four tokens.  Up to 256 row blocks need every wave that shares one: 4096 x 4096, one token, 4.1 with eight splits
+ *   against 4.5 with four; 300 x 16384 is worth sixteen.  More row blocks fill the chip with four (7000 x 14000 13.6
+ *   against 15.1), and from 2048 on two row blocks a wave keep more bytes in flight for the same waves (65536 x 4096
+ *   26.2 against 29.2).  Under a mask one row block is the unit: 256 of 65536 rows wanted 6.6 against 8.1.
+ *   More tokens, 16 at a time.  Up to 512 workgroups of one row block: one row block (4096 x 4096, 16 tokens, 5.1 against 8.2
+ *   with four).  Else four row blocks that share x (11008 x 4096, 16 tokens, 8.9 against 9.9; gated 12.6 against 13.0), with
+ *   two splits once that fills the chip (64 tokens 17.4); cutting an fp32 x costs more, so eight share it (8640 x 1856, 29
+ *   tokens, 12.6 against 14.5).
+ *   A wave gets two column blocks at least: 42752 x 512, one token, 5.4 against 6.0 with one.
  */
-q4_shape pick_shape(const dbs_q4_matrix *A, int tokens, bool gated, bool masked) {
+q4_shape pick_shape(const dbs_q4_matrix *A, int tokens, dbs_dtype xd, bool gated, bool masked) {
   q4_shape p = {};
   p.few = tokens <= 4;
   if (p.few) {
     p.rows = !gated && !masked && A->mt >= 2048 ? 2 : 1;
-    p.splits = A->mt <= 512 ? 8 : 4;
+    p.splits = A->mt <= 64 ? 16 : A->mt <= 256 ? 8 : 4;
   } else {
-    const int64_t blocks = (tokens + 15) / 16;
-    p.rows = A->mt * blocks <= 512 ? 1 : 4;
-    p.splits = p.rows == 1 ? 8 : A->mt * blocks <= 2048 ? 4 : 2;
+    const int64_t work = A->mt * (int64_t)((tokens + 15) / 16);
+    p.rows = work <= 512 ? 1 : work > 1024 && xd == DBS_F32 && !gated ? 8 : 4;
+    p.splits = p.rows == 1 ? (work <= 256 ? 8 : 4) : p.rows == 4 && work <= 2048 ? 4 : 2;
   }
-  while (p.splits > 1 && p.splits / 2 >= A->kt) p.splits /= 2;  // a wave without columns would only wait
+  while (p.splits > 1 && A->kt < 2 * p.splits) p.splits /= 2;
   return p;
 }
 
@@ -106,7 +108,7 @@ dbs_status product(dbs_q4_handle A, dbs_q4_handle U, int act, int32_t tokens, co
                tokens, x, ldx, mask, ldmask, fill, yd == DBS_BF16, y, ldy};
   const auto run = xd == DBS_BF16 ? (U ? dbs_q4_launch_bf16_gated : dbs_q4_launch_bf16)
                                   : (U ? dbs_q4_launch_f32_gated : dbs_q4_launch_f32);
-  const hipError_t e = run(q, q4_record_words(A->scale_dtype), A->gpt, pick_shape(A, tokens, U != nullptr, mask != nullptr), (hipStream_t)stream);
+  const hipError_t e = run(q, q4_record_words(A->scale_dtype), A->gpt, pick_shape(A, tokens, xd, U != nullptr, mask != nullptr), (hipStream_t)stream);
   return e == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
 

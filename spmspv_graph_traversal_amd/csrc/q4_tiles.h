@@ -23,7 +23,7 @@ struct q4_args {
 // How a call is cut into workgroups.
 struct q4_shape {
   bool few;    // one to four tokens, else sixteen a workgroup
-  int rows;    // row blocks a workgroup: 1, 2 (few) or 4
+  int rows;    // row blocks a workgroup: 1 or 2 (few), 1, 4 or 8 (fp32, one matrix)
   int splits;  // waves that split the columns
 };
 
@@ -265,8 +265,8 @@ struct tiling {
   static constexpr int kBuffers = RW > 1 ? 2 : 1;
   static constexpr int kLds = kBuffers * kOps * kPlane;  // per split
   static constexpr int kDepth = 2;                // column blocks in flight
-  // waves of 256 registers come eight to a compute unit, of 128 sixteen
-  static constexpr int kThreads = RW > 1 && MATS * R * TT * kOps <= 2 ? 1024 : 512;
+  // sixteen waves may use 128 registers each, eight 256
+  static constexpr int kThreads = FEW || MATS * R * TT * kOps <= 2 ? 1024 : 512;
   static_assert(kLoads >= 1, "");
 };
 
@@ -278,7 +278,11 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rw = wave % RW, split = wave / RW, splits = (blockDim.x >> 6) / RW;
   const int j = lane & 15, kq = lane >> 4;
-  const int row0 = blockIdx.x * rows, rt0 = row0 / Q4_ROWS + rw * R, t0 = blockIdx.y * kTokens;
+  // Workgroups go to the eight dies in turn, and each die has an L2 of its own: the token blocks (y) of one row group are a
+  // multiple of eight apart, so that they run on one die at one time and the codes come from memory once.
+  const unsigned first = (blockIdx.z * gridDim.x + blockIdx.x) * rows;
+  if (first >= (unsigned)q.m) return;
+  const int row0 = (int)first, rt0 = row0 / Q4_ROWS + rw * R, t0 = blockIdx.y * kTokens;
   const int tokens = min(kTokens, q.tokens - t0);
   const X *x = (const X *)q.x + (int64_t)t0 * q.ldx;
   if (q.mask && !any_wanted(q, t0, tokens, row0, rows)) {
@@ -491,7 +495,8 @@ hipError_t launch_tiles(const q4_args &q, int splits, hipStream_t s) {
   constexpr int rows = R * RW;
   while (splits * T::kLds > 160 * 1024 || 64 * splits * RW > T::kThreads) splits /= 2;
   const auto kernel = k_q4<X, WORDS, GPT, MATS, R, TT, RW, FEW>;
-  const dim3 grid((unsigned)((q.mt + rows - 1) / rows), (unsigned)((q.tokens + T::kTokens - 1) / T::kTokens));
+  const unsigned groups = (unsigned)((q.mt + rows - 1) / rows), eights = (groups + 7) / 8, wide = (eights + 65534) / 65535;
+  const dim3 grid(8 * wide, (unsigned)((q.tokens + T::kTokens - 1) / T::kTokens), (eights + wide - 1) / wide);
   const size_t parts = (size_t)((splits + 1) / 2) * MATS * rows * Q4_ROWS * T::kTokens * 4;
   const size_t xs = (size_t)splits * T::kLds, lds = parts > xs ? parts : xs;
   if (lds > 65536) {  // more than a launch gets unasked
@@ -514,6 +519,9 @@ hipError_t launch_shape(const q4_args &q, const q4_shape &p, hipStream_t s) {
   if (p.rows == 4) {
     if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 2, false>(q, p.splits, s);
     else return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 4, false>(q, p.splits, s);
+  }
+  if constexpr (MATS == 1 && sizeof(X) == 4) {
+    if (p.rows == 8) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 4, false>(q, p.splits, s);
   }
   return hipErrorInvalidValue;
 }
