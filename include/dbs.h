@@ -347,12 +347,17 @@ dbs_status dbs_probe_read(const void *buf, int64_t bytes, uint32_t *sink, uint32
  * DBS_F32 or DBS_BF16.  The calls allocate nothing and use no scratch, so
  * they may run on several streams at once and be captured into a graph; they
  * run on the current device, which must hold all their buffers.  No output
- * may overlap an input, except where stated.
+ * may overlap an input, from its first byte to its last, except where stated.
+ * Sums are in fp32; nothing depends on timing, so a call on the same inputs
+ * gives the same bits again.
  * ------------------------------------------------------------------------ */
 typedef struct dbs_q4_matrix *dbs_q4_handle; /* opaque */
 
-/* tokens of one call at most */
+/* tokens of one call, rows (row numbers of a last workgroup stay below 2^31) and columns (offsets in a
+ * row of tiles stay below 2^32) at most */
 #define DBS_Q4_MAX_TOKENS 524288
+#define DBS_Q4_MAX_ROWS 2147483520
+#define DBS_Q4_MAX_COLUMNS 268435456
 
 /*
  * dbs_q4_build — lay out an m x n matrix held in 4 bits with group scales:
@@ -384,8 +389,8 @@ dbs_status dbs_q4_free(dbs_q4_handle A);
  * dbs_q4_product — y_t = W x_t for `tokens` vectors, fp32 accumulation, one
  * rounding to y's type.
  *
- *   tokens   0 <= tokens <= DBS_Q4_MAX_TOKENS.  One call reads the weights once per 64
- *            tokens
+ *   tokens   0 <= tokens <= DBS_Q4_MAX_TOKENS; made for one to 64 (16 at a time, each 16
+ *            going through the weights, which come from memory once if the tokens are few)
  *   x        device [tokens][n], row stride ldx >= n elements
  *   y        device [tokens][m], row stride ldy >= m elements
  *

@@ -159,6 +159,7 @@ dbs_status dbs_q4_build(int32_t m, int32_t n, int32_t group, const uint8_t *code
                         dbs_dtype scale_dtype, const uint8_t *zeros, void *stream, dbs_q4_handle *out) {
   if (!out || m < 1 || n < 1 || !codes || !scales || !dbs_is_vector_dtype(scale_dtype)) return DBS_ERR_INVALID_ARG;
   if (group != 32 && group != 64 && group != 128) return DBS_ERR_INVALID_ARG;
+  if (m > DBS_Q4_MAX_ROWS || n > DBS_Q4_MAX_COLUMNS) return DBS_ERR_UNSUPPORTED;
   dbs_q4_matrix *A = new (std::nothrow) dbs_q4_matrix;
   if (!A) return DBS_ERR_OUT_OF_MEMORY;
   memset((void *)A, 0, sizeof(*A));

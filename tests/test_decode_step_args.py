@@ -24,6 +24,11 @@ def test_q4_build_refusals(bad):
     assert q4_build(**bad) == INVALID
 
 
+def test_q4_build_limits():
+    assert q4_build(m=b.DBS_Q4_MAX_ROWS + 1) == UNSUPPORTED
+    assert q4_build(n=b.DBS_Q4_MAX_COLUMNS + 1) == UNSUPPORTED
+
+
 def test_q4_calls_without_a_handle():
     v = C.c_int64()
     assert _lib.dbs_q4_bytes(None, C.byref(v)) == INVALID
