@@ -44,11 +44,11 @@ struct id_list {
   int64_t lo, hi;
   four<int32_t> v[AHEAD];
 
-  // row b's part, clamped to the list's length
+  // row b's part, 0 <= lo <= hi <= len whatever the pointers hold: left() counts on it
   DBS_DEV id_list(const int32_t *ids, const int32_t *ptr, int64_t len, int64_t b) : list(ids) {
     const int32_t first = or_nothing(ptr, b), end = or_nothing(ptr, b + 1);
-    lo = first < 0 ? 0 : first;
-    hi = end > len ? len : end;
+    lo = first < 0 ? 0 : first > len ? len : first;
+    hi = end < lo ? lo : end > len ? len : end;
   }
   DBS_DEV int64_t at(int round) const { return lo + 4 * ((int64_t)round * blockDim.x + threadIdx.x); }
   DBS_DEV int left(int64_t i) const { return (int)(hi - i < 4 ? hi - i : 4); }

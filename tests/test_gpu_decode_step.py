@@ -344,6 +344,21 @@ def test_logits_rows_with_strides_and_bad_lists_stay_in_bounds(dbs):
     assert (out[:, 0] == 9).all() and (out[:, 71:] == 9).all()
 
 
+def test_logits_lists_of_extreme_pointers_are_empty(dbs):
+    rng = np.random.default_rng(51)
+    lo, hi = np.iinfo(np.int32).min, np.iinfo(np.int32).max
+    ptr = np.array([hi, lo, lo + 2, hi, hi - 5, 0, lo, 0], np.int32)  # only row 2's part is not empty: all three entries
+    l = rng.normal(0, 3, (7, 60)).astype(np.float32)
+    ids, ones = np.array([7, 8, 7], np.int32), np.ones(7, np.float32)
+    out = empty((7, 60), "f32")
+    dbs.dbs_logits_adjust(cuda(l), out, hist_ptr=cuda(ptr), hist=cuda(ids), hist_new=cuda(np.zeros(7, np.int32)),
+                          frequency=cuda(ones), bias_ptr=cuda(ptr), bias_idx=cuda(ids), bias_val=cuda(ones[:3]))
+    rows = [ids if b == 2 else [] for b in range(7)]
+    expect = ref.logits(l, hist=rows, freq=ones, bias=[[(v, 1.0) for v in r] for r in rows])
+    # two sums, each rounded on a magnitude below 16
+    np.testing.assert_allclose(host(out), expect, rtol=0, atol=2 * 16 * ref.U24)
+
+
 # --------------------------------------------------------------------------- rope
 @pytest.mark.parametrize("x_kind,y_kind", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
 @pytest.mark.parametrize("interleaved", [False, True])
