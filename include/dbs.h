@@ -477,8 +477,9 @@ dbs_status dbs_logits_adjust(int32_t rows, int32_t vocab, const void *logits, db
 /* pairs of a rotated head: element i with i + rot_dim/2, or 2i with 2i + 1 */
 typedef enum { DBS_ROPE_HALF = 0, DBS_ROPE_INTERLEAVED = 1 } dbs_rope_layout;
 
-/* largest rot_dim */
+/* largest rot_dim, and heads * head_dim */
 #define DBS_ROPE_MAX_DIM 1024
+#define DBS_ROPE_MAX_ELEMENTS 1073741824
 
 /*
  * dbs_rope — rotary positions: in each head of each token, pair i (a, b) of
@@ -489,7 +490,7 @@ typedef enum { DBS_ROPE_HALF = 0, DBS_ROPE_INTERLEAVED = 1 } dbs_rope_layout;
  * and the elements from rot_dim on are copied.  p is formed and reduced in
  * 64 bits, so far positions keep their phase.
  *
- *   tokens, heads  >= 0;  head_dim >= 1, heads * head_dim < 2^31;  rot_dim even, 0 <= rot_dim <= head_dim
+ *   tokens, heads  >= 0;  head_dim >= 1;  rot_dim even, 0 <= rot_dim <= head_dim
  *   pos            device int32[tokens]; a negative position marks padding: the token's
  *                  rows of `out` are left as they are
  *   freq           device double[rot_dim/2], radians per position (dbs_rope_frequencies)

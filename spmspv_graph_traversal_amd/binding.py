@@ -33,7 +33,7 @@ DBS_ACT_SILU, DBS_ACT_GELU_TANH, DBS_ACT_RELU = 0, 1, 2
 DBS_ROPE_HALF, DBS_ROPE_INTERLEAVED = 0, 1
 DBS_ROPE_PLAIN, DBS_ROPE_LINEAR, DBS_ROPE_BASE, DBS_ROPE_BANDS, DBS_ROPE_RAMP = 0, 1, 2, 3, 4
 DBS_Q4_MAX_TOKENS, DBS_Q4_MAX_ROWS, DBS_Q4_MAX_COLUMNS = 524288, 2147483520, 1 << 28
-DBS_LOGITS_MAX_ROWS, DBS_ROPE_MAX_DIM = 65535, 1024
+DBS_LOGITS_MAX_ROWS, DBS_ROPE_MAX_DIM, DBS_ROPE_MAX_ELEMENTS = 65535, 1024, 1 << 30
 # exported arrays
 (DBS_ARR_RB_PTR, DBS_ARR_T_CB, DBS_ARR_T_META, DBS_ARR_CB_PTR, DBS_ARR_CSC_RB, DBS_ARR_CSC2CSR,
  DBS_ARR_PAYLOAD, DBS_ARR_SEGMENTS, DBS_ARR_XMASK, DBS_ARR_ACTIVE, DBS_ARR_CSC_CM, DBS_ARR_PAT_SEGS,

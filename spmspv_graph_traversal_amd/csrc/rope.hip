@@ -127,7 +127,8 @@ extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, 
     return DBS_ERR_INVALID_ARG;
   if (layout != DBS_ROPE_HALF && layout != DBS_ROPE_INTERLEAVED) return DBS_ERR_INVALID_ARG;
   if (!dbs_is_vector_dtype(x_dtype) || !dbs_is_vector_dtype(out_dtype)) return DBS_ERR_INVALID_ARG;
-  if (rot_dim > DBS_ROPE_MAX_DIM || (int64_t)heads * head_dim > INT32_MAX) return DBS_ERR_UNSUPPORTED;
+  // a lane's counter passes the number of elements by up to a workgroup's lanes, in 32 bits
+  if (rot_dim > DBS_ROPE_MAX_DIM || (int64_t)heads * head_dim > DBS_ROPE_MAX_ELEMENTS) return DBS_ERR_UNSUPPORTED;
   if (tokens == 0 || heads == 0) return DBS_OK;
   if (!pos || (rot_dim > 0 && !freq) || !x || !out) return DBS_ERR_INVALID_ARG;
   // rows of one output may not overlap each other, and an in-place call reads what it writes

@@ -82,6 +82,13 @@ def test_rope_limits_and_nothing_to_do():
     assert rope(heads=1 << 20, dim=1 << 11, oh=1 << 11, ot=1 << 31) == UNSUPPORTED
 
 
+def test_rope_largest_head_that_a_lane_can_count():
+    last = b.DBS_ROPE_MAX_ELEMENTS
+    assert rope(heads=1, dim=last + 8, oh=last + 8, ot=last + 8) == UNSUPPORTED
+    assert rope(heads=1, dim=2**31 - 1, rot=0, oh=2**31 - 1, ot=2**31 - 1) == UNSUPPORTED
+    assert rope(tokens=0, heads=1, dim=last, oh=last, ot=last) == OK
+
+
 def frequencies(**kw):
     o = dict(rot_dim=8, scaling=0, base=10000.0, factor=2.0, low=1.0, high=4.0, context=4096.0)
     o.update(kw)
