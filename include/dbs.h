@@ -497,7 +497,9 @@ typedef enum { DBS_ROPE_HALF = 0, DBS_ROPE_INTERLEAVED = 1 } dbs_rope_layout;
  *   inverse        nonzero: rotate by -p (undoes a rotation; the gradient with respect to x
  *                  is this rotation of the output's gradient)
  *   x, out         device, element (t, h, d) at t * token stride + h * head stride + d;
- *                  `out` may be `x` itself (same type and strides), else they do not overlap
+ *                  `out` may be `x` itself (same type and strides), else they share no element.
+ *                  Strides of x are free; of out, one is at least head_dim and the other leaves
+ *                  room for all that the first one spans (either order, either sign)
  */
 dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, int32_t rot_dim, dbs_rope_layout layout,
                     const int32_t *pos, const double *freq, float scale, int32_t inverse, const void *x,

@@ -117,6 +117,13 @@ dbs_status launch_rope(const rope_args &r, hipStream_t s) {
   return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
 
+// whether rows of `width` elements at i * si + j * sj are disjoint because each i's rows end before the next i's begin
+bool apart(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t width) {
+  typedef __int128 wide;
+  const wide i = si < 0 ? -(wide)si : si, j = sj < 0 ? -(wide)sj : sj;
+  return (nj < 2 || j >= width) && (ni < 2 || i >= (nj - 1) * j + width);
+}
+
 }  // namespace
 
 extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, int32_t rot_dim, dbs_rope_layout layout,
@@ -131,9 +138,8 @@ extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, 
   if (rot_dim > DBS_ROPE_MAX_DIM || (int64_t)heads * head_dim > DBS_ROPE_MAX_ELEMENTS) return DBS_ERR_UNSUPPORTED;
   if (tokens == 0 || heads == 0) return DBS_OK;
   if (!pos || (rot_dim > 0 && !freq) || !x || !out) return DBS_ERR_INVALID_ARG;
-  // rows of one output may not overlap each other, and an in-place call reads what it writes
-  if (heads > 1 && oh < head_dim && oh > -(int64_t)head_dim) return DBS_ERR_INVALID_ARG;
-  if (tokens > 1 && ot < head_dim && ot > -(int64_t)head_dim) return DBS_ERR_INVALID_ARG;
+  // two heads of the output may not share an element, and an in-place call reads what it writes
+  if (!apart(tokens, ot, heads, oh, head_dim) && !apart(heads, oh, tokens, ot, head_dim)) return DBS_ERR_INVALID_ARG;
   if (x == out && (x_dtype != out_dtype || (tokens > 1 && xt != ot) || (heads > 1 && xh != oh)))
     return DBS_ERR_INVALID_ARG;
   const rope_args r = {tokens, heads, head_dim, rot_dim, layout == DBS_ROPE_INTERLEAVED, pos, freq, scale,

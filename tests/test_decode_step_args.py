@@ -82,6 +82,13 @@ def test_rope_limits_and_nothing_to_do():
     assert rope(heads=1 << 20, dim=1 << 11, oh=1 << 11, ot=1 << 31) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("oh,ot", [(8, 8), (8, 16), (8, 23), (8, 31), (15, 8), (-8, 24), (8, -25), (16, 7), (9, 0)])
+def test_rope_refuses_outputs_whose_rows_meet(oh, ot):
+    rows = [{t * ot + h * oh + d for d in range(8)} for t in range(2) for h in range(4)]
+    assert len(set.union(*rows)) < 8 * len(rows)
+    assert rope(tokens=2, heads=4, oh=oh, ot=ot) == INVALID
+
+
 def test_rope_largest_head_that_a_lane_can_count():
     last = b.DBS_ROPE_MAX_ELEMENTS
     assert rope(heads=1, dim=last + 8, oh=last + 8, ot=last + 8) == UNSUPPORTED
