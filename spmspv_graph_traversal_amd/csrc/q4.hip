@@ -104,11 +104,12 @@ dbs_status product(dbs_q4_handle A, dbs_q4_handle U, int act, int32_t tokens, co
   const int64_t ybytes = (last * ldy + A->m) * dbs_vector_size(yd);
   if (dbs_overlap(x, (last * ldx + A->n) * dbs_vector_size(xd), y, ybytes)) return DBS_ERR_INVALID_ARG;
   if (mask && dbs_overlap(mask, (last * ldmask + ((int64_t)A->m + 31) / 32) * 4, y, ybytes)) return DBS_ERR_INVALID_ARG;
-  q4_args q = {{A->codes, U ? U->codes : nullptr}, {A->recs, U ? U->recs : nullptr}, A->m, A->n, A->mt, A->kt, act,
+  q4_args q = {dev, {A->codes, U ? U->codes : nullptr}, {A->recs, U ? U->recs : nullptr}, A->m, A->n, A->mt, A->kt, act,
                tokens, x, ldx, mask, ldmask, fill, yd == DBS_BF16, y, ldy};
   const auto run = xd == DBS_BF16 ? (U ? dbs_q4_launch_bf16_gated : dbs_q4_launch_bf16)
                                   : (U ? dbs_q4_launch_f32_gated : dbs_q4_launch_f32);
-  const hipError_t e = run(q, q4_record_words(A->scale_dtype), A->gpt, pick_shape(A, tokens, xd, U != nullptr, mask != nullptr), (hipStream_t)stream);
+  const q4_shape shape = pick_shape(A, tokens, xd, U != nullptr, mask != nullptr);
+  const hipError_t e = run(q, q4_record_words(A->scale_dtype), A->gpt, shape, (hipStream_t)stream);
   return e == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
 

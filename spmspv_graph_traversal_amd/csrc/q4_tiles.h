@@ -1,12 +1,14 @@
 // The product kernel of 4-bit matrices (q4.h) on the matrix cores.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "q4.h"
 #include "tile_kernels.h"
 
 struct q4_args {
+  int device;  // the current one
   const uint32_t *codes[2], *recs[2];  // [1]: the second matrix of a gated product
   int m, n, mt, kt, act;
   int tokens;
@@ -499,9 +501,14 @@ hipError_t launch_tiles(const q4_args &q, int splits, hipStream_t s) {
   const dim3 grid(8 * wide, (unsigned)((q.tokens + T::kTokens - 1) / T::kTokens), (eights + wide - 1) / wide);
   const size_t parts = (size_t)((splits + 1) / 2) * MATS * rows * Q4_ROWS * T::kTokens * 4;
   const size_t xs = (size_t)splits * T::kLds, lds = parts > xs ? parts : xs;
-  if (lds > 65536) {  // more than a launch gets unasked
-    static const hipError_t asked = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    if (asked != hipSuccess) return DBS_NOTE(asked);
+  if (lds > 65536) {  // more than a launch gets unasked; asked for once on each device
+    static std::atomic<uint64_t> asked{0};
+    const uint64_t bit = q.device < 64 ? 1ull << q.device : 0ull;
+    if (!(asked.load(std::memory_order_acquire) & bit)) {
+      const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+      if (e != hipSuccess) return DBS_NOTE(e);
+      asked.fetch_or(bit, std::memory_order_release);
+    }
   }
   hipLaunchKernelGGL(kernel, grid, dim3(64 * splits * RW), lds, s, q);
   return DBS_NOTE(hipGetLastError());
