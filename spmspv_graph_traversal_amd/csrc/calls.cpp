@@ -31,6 +31,13 @@ int64_t integer(PyObject *o) {
   if (v == -1 && PyErr_Occurred()) throw failed();
   return v;
 }
+// a value of an enum
+template <class E>
+E choice(PyObject *o) {
+  const int64_t v = integer(o);
+  if (v < INT32_MIN || v > INT32_MAX) fail(PyExc_ValueError, "%lld is no choice", (long long)v);
+  return (E)v;
+}
 double number(PyObject *o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw failed();
@@ -143,6 +150,15 @@ PyObject *status(F f) {
   return nullptr;
 }
 
+// the library's call without the interpreter's lock: a launch waits while its queue is full
+template <class F, class... A>
+dbs_status unlocked(F f, A... a) {
+  PyThreadState *const thread = PyEval_SaveThread();
+  const dbs_status st = f(a...);
+  PyEval_RestoreThread(thread);
+  return st;
+}
+
 void need(Py_ssize_t have, Py_ssize_t want) {
   if (have != want) fail(PyExc_TypeError, "%zd arguments, expected %zd", have, want);
   if (!f_product) fail(PyExc_RuntimeError, "not bound to the library");
@@ -159,7 +175,8 @@ PyObject *q4_product(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const call c(a[4], "y", a[5]);
     const rows x(c, a[3], "x", integer(a[2]), "tokens"), y(c, a[4], "y", integer(a[1]), "tokens");
     same_tokens(x, y);
-    return f_product((dbs_q4_handle)pointer(a[0]), (int32_t)x.count, x.p, x.type, x.ld, y.p, y.type, y.ld, c.stream);
+    return unlocked(f_product, (dbs_q4_handle)pointer(a[0]), (int32_t)x.count, x.p, x.type, x.ld, y.p, y.type, y.ld,
+                    c.stream);
   });
 }
 
@@ -171,8 +188,8 @@ PyObject *q4_product_masked(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const rows x(c, a[3], "x", integer(a[2]), "tokens"), y(c, a[6], "y", integer(a[1]), "tokens");
     same_tokens(x, y);
     const mask_rows m(c, a[4], x.count, integer(a[1]));
-    return f_masked((dbs_q4_handle)pointer(a[0]), (int32_t)x.count, x.p, x.type, x.ld, m.p, m.ld, (float)number(a[5]), y.p,
-                    y.type, y.ld, c.stream);
+    return unlocked(f_masked, (dbs_q4_handle)pointer(a[0]), (int32_t)x.count, x.p, x.type, x.ld, m.p, m.ld,
+                    (float)number(a[5]), y.p, y.type, y.ld, c.stream);
   });
 }
 
@@ -183,8 +200,8 @@ PyObject *q4_gated(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const call c(a[6], "y", a[7]);
     const rows x(c, a[4], "x", integer(a[3]), "tokens"), y(c, a[6], "y", integer(a[2]), "tokens");
     same_tokens(x, y);
-    return f_gated((dbs_q4_handle)pointer(a[0]), (dbs_q4_handle)pointer(a[1]), (dbs_activation)integer(a[5]),
-                   (int32_t)x.count, x.p, x.type, x.ld, y.p, y.type, y.ld, c.stream);
+    return unlocked(f_gated, (dbs_q4_handle)pointer(a[0]), (dbs_q4_handle)pointer(a[1]), choice<dbs_activation>(a[5]),
+                    (int32_t)x.count, x.p, x.type, x.ld, y.p, y.type, y.ld, c.stream);
   });
 }
 
@@ -217,7 +234,7 @@ PyObject *logits_adjust(PyObject *, PyObject *const *a, Py_ssize_t n) {
       p.mask = m.p;
       p.ldmask = m.ld;
     }
-    return f_logits((int32_t)l.count, (int32_t)vocab, l.p, l.type, l.ld, &p, o.p, o.type, o.ld, c.stream);
+    return unlocked(f_logits, (int32_t)l.count, (int32_t)vocab, l.p, l.type, l.ld, &p, o.p, o.type, o.ld, c.stream);
   });
 }
 
@@ -240,9 +257,9 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (pairs > INT32_MAX / 2) fail(PyExc_ValueError, "freq is too large");
     const int inverse = PyObject_IsTrue(a[6]);
     if (inverse < 0) throw failed();
-    return f_rope((int32_t)x.size(0), (int32_t)x.size(1), (int32_t)x.size(2), (int32_t)(2 * pairs),
-                  (dbs_rope_layout)integer(a[4]), pos, freq, (float)number(a[5]), inverse, x.data_ptr(), xt, x.stride(0),
-                  x.stride(1), o.data_ptr(), ot, o.stride(0), o.stride(1), c.stream);
+    return unlocked(f_rope, (int32_t)x.size(0), (int32_t)x.size(1), (int32_t)x.size(2), (int32_t)(2 * pairs),
+                    choice<dbs_rope_layout>(a[4]), pos, freq, (float)number(a[5]), inverse, x.data_ptr(), xt, x.stride(0),
+                    x.stride(1), o.data_ptr(), ot, o.stride(0), o.stride(1), c.stream);
   });
 }
 

@@ -539,6 +539,51 @@ def test_decode_step(dbs):
 
 
 # --------------------------------------------------------------------------- refusals by the binding
+def test_choices_past_32_bits_are_refused(dbs):
+    import torch
+
+    A = ref.Q4(np.random.default_rng(81), 20, 64, 32, False).build(dbs)
+    x, y = torch.zeros(3, 64, device="cuda"), torch.full((3, 20), 5.0, device="cuda")
+    pos, freq = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.float64, device="cuda")
+    with pytest.raises(ValueError):
+        dbs.dbs_q4_gated(A, A, x, 1 << 32, y)
+    with pytest.raises(ValueError):
+        dbs.dbs_rope(x[:, None], pos, freq, x[:, None], layout=1 << 32)
+    torch.cuda.synchronize()
+    assert (y == 5).all()
+
+
+def test_calls_of_two_threads_on_their_own_streams(dbs):
+    import threading
+
+    import torch
+
+    rng = np.random.default_rng(82)
+    w = ref.Q4(rng, 500, 700, 64, True)
+    A = w.build(dbs)
+    xs = [integers(rng, t, 700) for t in (1, 20)]
+    ins, outs, errors = [cuda(x) for x in xs], [empty((len(x), 500), "f32") for x in xs], []
+    torch.cuda.synchronize()
+
+    def work(x, y):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    dbs.dbs_q4_product(A, x, y)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(ins, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not errors and not any(t.is_alive() for t in threads)
+    for x, y in zip(xs, outs):
+        np.testing.assert_array_equal(host(y), (x.astype(np.float64) @ w.w.T).astype(np.float32))
+
+
 def test_refusals_of_tensors(dbs):
     import torch
 
