@@ -69,7 +69,10 @@ __global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int
  *   More tokens, 16 at a time.  Up to 512 workgroups of one row block: one row block (4096 x 4096, 16 tokens, 5.1 against 8.2
  *   with four).  Else four row blocks that share x (11008 x 4096, 16 tokens, 8.9 against 9.9; gated 12.6 against 13.0), with
  *   two splits once that fills the chip (64 tokens 17.4); cutting an fp32 x costs more, so eight share it (8640 x 1856, 29
- *   tokens, 12.6 against 14.5).
+ *   tokens, 12.6 against 14.5).  Two token tiles a workgroup (bf16) unpack the codes once for both, in workgroups of twice
+ *   the work: worth it if enough of these remain, none is half empty and there are columns to pay for their longer end
+ *   (28672 x 4096, 64 tokens, 30.6 against 35.4; but 20000 x 4096, 32 tokens, 18.5 against 18.1 and 65536 x 512, 64 tokens,
+ *   26.0 against 19.5; gated 11008 x 4096, 32 tokens, 18.2 against 22.3).
  *   A wave gets two column blocks at least: 42752 x 512, one token, 5.4 against 6.0 with one.
  */
 q4_shape pick_shape(const dbs_q4_matrix *A, int tokens, dbs_dtype xd, bool gated, bool masked) {
@@ -80,7 +83,9 @@ q4_shape pick_shape(const dbs_q4_matrix *A, int tokens, dbs_dtype xd, bool gated
     p.splits = A->mt <= 64 ? 16 : A->mt <= 256 ? 8 : 4;
   } else {
     const int64_t work = A->mt * (int64_t)((tokens + 15) / 16);
-    p.rows = work <= 512 ? 1 : work > 1024 && xd == DBS_F32 && !gated ? 8 : 4;
+    const bool whole_pairs = (tokens + 15) / 16 % 2 == 0;
+    p.tiles = xd == DBS_BF16 && whole_pairs && work > (gated ? 1200 : 3000) && A->kt >= (gated ? 24 : 12) ? 2 : 1;
+    p.rows = work <= 512 ? 1 : !gated && (p.tiles == 2 || (work > 1024 && xd == DBS_F32)) ? 8 : 4;
     p.splits = p.rows == 1 ? (work <= 256 ? 8 : 4) : p.rows == 4 && work <= 2048 ? 4 : 2;
   }
   while (p.splits > 1 && A->kt < 2 * p.splits) p.splits /= 2;

@@ -24,8 +24,9 @@ struct q4_args {
 
 // How a call is cut into workgroups.
 struct q4_shape {
-  bool few;    // one to four tokens, else sixteen a workgroup
-  int rows;    // row blocks a workgroup: 1 or 2 (few), 1, 4 or 8 (fp32, one matrix)
+  bool few;    // one to four tokens
+  int tiles;   // else: token tiles of 16 a workgroup, 1 or 2 (bf16)
+  int rows;    // row blocks a workgroup: 1 or 2 (few), 1, 4 or 8 (one matrix; fp32 or two tiles)
   int splits;  // waves that split the columns
 };
 
@@ -521,6 +522,11 @@ hipError_t launch_shape(const q4_args &q, const q4_shape &p, hipStream_t s) {
       if (p.rows == 2) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 1, true>(q, p.splits, s);
     }
     return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 1, true>(q, p.splits, s);
+  }
+  if (p.tiles == 2) {
+    if constexpr (sizeof(X) == 2 && MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 2, 4, false>(q, p.splits, s);
+    if constexpr (sizeof(X) == 2 && MATS == 2) return launch_tiles<X, WORDS, GPT, MATS, 1, 2, 4, false>(q, p.splits, s);
+    return hipErrorInvalidValue;
   }
   if (p.rows == 1) return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 1, false>(q, p.splits, s);
   if (p.rows == 4) {

@@ -102,6 +102,43 @@ def test_products_of_many_rows_are_exact_on_integers(dbs, m, n, group, zeros, sc
         assert torch.equal(y.double(), torch.where(wanted, g, -np.inf)), f"{t} tokens, masked"
 
 
+@pytest.mark.parametrize("m,n,group,zeros,scales", [(26003, 1590, 32, True, "bf16"), (26003, 1537, 64, False, "f32"),
+                                                    (24100, 3101, 128, True, "bf16")])
+def test_products_of_two_token_tiles_are_exact_on_integers(dbs, m, n, group, zeros, scales):
+    """Matrices of so many rows and columns that workgroups take 32 tokens, with a last tile that is cut, an infinity and
+    rows of x and y with strides."""
+    import torch
+
+    rng = np.random.default_rng(m + n)
+    w, u = ref.Q4(rng, m, n, group, zeros, scales), ref.Q4(rng, m, n, group, zeros, scales)
+    A, U = w.build(dbs), u.build(dbs)
+    w64, u64 = torch.from_numpy(w.w).cuda().t(), torch.from_numpy(u.w).cuda().t()
+    for t in (17, 32, 50, 64, 90):
+        wide = torch.full((t, n + 3), float("nan"), device="cuda", dtype=torch.bfloat16)
+        x = wide[:, 1:n + 1]
+        x.copy_(cuda(integers(rng, t, n)))
+        g, h = x.double() @ w64, x.double() @ u64
+        out = torch.full((t, m + 5), 7.0, device="cuda")
+        y = out[:, 2:m + 2]
+        dbs.dbs_q4_product(A, x, y)
+        assert torch.equal(y.double(), g), f"{t} tokens"
+        dbs.dbs_q4_gated(A, U, x, dbs.DBS_ACT_RELU, y)
+        assert torch.equal(y, (g.clamp_min(0) * h).float()), f"{t} tokens, gated"
+        words = cuda(rng.integers(-2 ** 31, 2 ** 31, (t, (m + 31) // 32)).astype(np.int32))
+        words[:, m // 80: m // 40] = 0
+        row = torch.arange(m, device="cuda")
+        wanted = (words[:, row // 32] >> (row % 32)) & 1 != 0
+        dbs.dbs_q4_product_masked(A, x, words, y)
+        assert torch.equal(y.double(), torch.where(wanted, g, -np.inf)), f"{t} tokens, masked"
+        x[t // 2, 5] = float("inf")
+        dbs.dbs_q4_product(A, x, y)
+        few = [0, t // 2 - 1, t // 2 + 1, t - 1]
+        assert torch.equal(y[few].double(), g[few])
+        spread = torch.where(w64[5] == 0, torch.nan, w64[5] * np.inf)
+        assert torch.equal(y[t // 2].nan_to_num(3.0, 1.0, -1.0).double(), spread.nan_to_num(3.0, 1.0, -1.0))
+        assert (out[:, :2] == 7).all() and (out[:, m + 2:] == 7).all()
+
+
 @pytest.mark.parametrize("x_kind", ["bf16", "f32"])
 @pytest.mark.parametrize("tokens", [1, 3, 8, 30, 64])
 def test_product_of_real_values(dbs, tokens, x_kind):
