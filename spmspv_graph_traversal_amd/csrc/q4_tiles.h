@@ -74,6 +74,22 @@ struct x_piece<bf16_bits> {
     for (int e = 0; e < 8; ++e) h[e] = col + e < n ? h[e] : 0u;
     v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   }
+  // the piece was read `back` columns early, so as to end with its row: what lies past the end becomes zero.  `shift` is
+  // the one value of `back` between 0 and 8 in this wave
+  DBS_DEV void cut(int back, int shift) {
+    const uint32_t w[8] = {v.x, v.y, v.z, v.w, 0u, 0u, 0u, 0u};
+    uint32_t moved[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      moved[i] = w[i];
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s == shift) moved[i] = s & 1 ? __builtin_amdgcn_alignbit(w[min(i + s / 2 + 1, 7)], w[i + s / 2], 16) : w[i + s / 2];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) moved[i] = back == 0 ? w[i] : back < columns ? moved[i] : 0u;
+    v = make_uint4(moved[0], moved[1], moved[2], moved[3]);
+  }
   // place(p): where part p of this piece goes
   template <class F>
   DBS_DEV void put(F place) const { *(uint4 *)place(0) = v; }
@@ -88,6 +104,17 @@ struct x_piece<float> {
     for (int e = 0; e < 4; ++e) v[e] = row[min(col + e, n - 1)];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = col + e < n ? v[e] : 0.0f;
+  }
+  DBS_DEV void cut(int back, int shift) {
+    const float w[8] = {v[0], v[1], v[2], v[3], 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float moved = w[i];
+#pragma unroll
+      for (int s = 1; s < 4; ++s)
+        if (s == shift) moved = w[i + s];
+      v[i] = back == 0 ? w[i] : back < columns ? moved : 0.0f;
+    }
   }
   template <class F>
   DBS_DEV void put(F place) const {
@@ -416,18 +443,25 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k
     multiply(d);
     if (RW == 1) wave_fence();
   };
-  // Row waves meet at barriers, so all splits go the same number of rounds; rounds without a block multiply by zero.
-  const int rounds = RW > 1 ? (whole + splits - 1) / splits : split < whole ? (whole - split + splits - 1) / splits : 0;
-  if (rounds > 0) {
-    int k = split;
+  // All blocks of this wave.  CUT: n ends within the last of the columns' blocks; there, pieces that would pass the end are
+  // read `back` columns early, and cut afterwards.  (One code for both would cost whole columns 3 %.)
+  auto all_blocks = [&](auto cut) {
+    constexpr bool CUT = decltype(cut)::value;
+    const int back = max((whole * Q4_COLS + (piece + 1) * x_piece<X>::columns) - q.n, 0);
+    const int shift = (x_piece<X>::columns - q.n % x_piece<X>::columns) % x_piece<X>::columns;
     auto fetch = [&](int d, int k) {
       __builtin_amdgcn_sched_barrier(0);  // in the order in which they are used
+      const int kx = min(k, q.kt - 1);
+      const int at = kx * Q4_COLS - (CUT && kx == whole ? back : 0);
 #pragma unroll
-      for (int i = 0; i < T::kLoads; ++i) xr[d][i].load(from[i], min(k, whole - 1) * Q4_COLS);
+      for (int i = 0; i < T::kLoads; ++i) xr[d][i].load(from[i], at);
       __builtin_amdgcn_sched_barrier(0);
-      fetch_codes(d, k, whole);
+      fetch_codes(d, k, q.kt);
       __builtin_amdgcn_sched_barrier(0);
     };
+    // Row waves meet at barriers, so all splits go the same number of rounds; rounds without a block multiply by zero.
+    const int rounds = (q.kt - (RW > 1 ? 0 : split) + splits - 1) / splits;
+    int k = split;
 #pragma unroll
     for (int d = 0; d < D; ++d) fetch(d, k + d * splits);
     // one way through each turn: where paths with and without loads met, the compiler would wait for all of them
@@ -440,24 +474,28 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k
         fetch(d, k + (D - 1) * splits);
       }
     }
+    // the last block of the columns is the last of its split
     const int left = rounds - turns * D;
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       if (d == left) break;
+      if (CUT && k + d * splits == whole) {
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) xr[d][i].cut(back, shift);
+      }
       block(d);
     }
-  }
-  if (whole < q.kt) {  // the block that n ends in: the first split's
-    dbs_barrier_lds();
-    if (split == 0) {
-      fetch_codes(0, whole, q.kt);
+  };
+  if (whole == 0) {  // less than a column block: n may be too short for a wide load
+    fetch_codes(0, split, q.kt);
 #pragma unroll
-      for (int i = 0; i < T::kLoads; ++i)
-        xr[0][i].load_cut(from[i] - piece * x_piece<X>::columns, whole * Q4_COLS + piece * x_piece<X>::columns, q.n);
-      put_x(0);
-    }
-    dbs_barrier_lds();
-    if (split == 0) multiply(0);
+    for (int i = 0; i < T::kLoads; ++i)
+      xr[0][i].load_cut(from[i] - piece * x_piece<X>::columns, piece * x_piece<X>::columns, q.n);
+    block(0);
+  } else if (whole == q.kt) {
+    all_blocks(std::false_type());
+  } else {
+    all_blocks(std::true_type());
   }
 
   // part[splits / 2][MATS][kTokens][rows], over the x of before.  Lane (kq, j), register i: token 16 t + 4 kq + i of row
