@@ -11,7 +11,7 @@ namespace {
  * bits (a far position is many turns, of which 32 bits would keep no fraction), the sine of its fraction in 32.
  *
  * One workgroup per token and `per` heads, W pairs or W copied elements to a lane at a time.  W = 8 makes loads and stores of
- * 16 bytes, W = 1 takes any rot_dim and head_dim.  Bound by memory for a prompt; x is loaded before the sines, so that a token's
+ * 16 bytes of bf16, W = 1 takes any rot_dim and head_dim.  Bound by memory for a prompt; x is loaded before the sines, so that a token's
  * chain is not position, frequencies, sines and then x.
  */
 // past the caches: 8192 tokens of 40 heads of 128 bf16 30.4 us against 35.0
@@ -25,14 +25,17 @@ DBS_DEV void write(T *p, const T (&v)[W]) {
 
 template <class X, class Y, int W, bool INTERLEAVED>
 struct rope_unit {
-  X a[W], b[W];  // half layout: first and second elements of W pairs; interleaved: 2 W neighbours
+  // Half layout, or W = 1: W pairs, or W elements from rot_dim on.  Interleaved with W > 1: 2 W neighbours, of which those
+  // from rot_dim on are copied.
+  static constexpr bool kMixed = INTERLEAVED && W > 1;
+  X a[W], b[W];
   int h, i;
 
   DBS_DEV void load(const X *x, int64_t xh, int u, int units, int turned, int half) {
     h = u / units;
     i = u % units;
     const X *p = x + h * xh;
-    if (i < turned) {
+    if (kMixed || i < turned) {
       __builtin_memcpy(a, p + (INTERLEAVED ? 2 * W * i : W * i), sizeof a);
       __builtin_memcpy(b, p + (INTERLEAVED ? 2 * W * i + W : half + W * i), sizeof b);
     } else {
@@ -42,15 +45,20 @@ struct rope_unit {
   DBS_DEV void store(Y *out, int64_t oh, const float2 *turn, int turned, int half) const {
     Y oa[W], ob[W];
     Y *p = out + h * oh;
-    if (i < turned) {
+    if (kMixed || i < turned) {
 #pragma unroll
       for (int e = 0; e < W; ++e) {
-        const float2 w = turn[W * i + e];
         const int ka = INTERLEAVED ? 2 * e : e, kb = INTERLEAVED ? 2 * e + 1 : W + e;  // within a, b
         const float va = dbs_value<X>::load(ka < W ? &a[ka % W] : &b[ka % W]);
         const float vb = dbs_value<X>::load(kb < W ? &a[kb % W] : &b[kb % W]);
-        (ka < W ? oa[ka % W] : ob[ka % W]) = dbs_value<Y>::of(va * w.x - vb * w.y);
-        (kb < W ? oa[kb % W] : ob[kb % W]) = dbs_value<Y>::of(va * w.y + vb * w.x);
+        float ra = va, rb = vb;
+        if (!kMixed || W * i + e < half) {
+          const float2 w = turn[W * i + e];
+          ra = va * w.x - vb * w.y;
+          rb = va * w.y + vb * w.x;
+        }
+        (ka < W ? oa[ka % W] : ob[ka % W]) = dbs_value<Y>::of(ra);
+        (kb < W ? oa[kb % W] : ob[kb % W]) = dbs_value<Y>::of(rb);
       }
       write(p + (INTERLEAVED ? 2 * W * i : W * i), oa);
       write(p + (INTERLEAVED ? 2 * W * i + W : half + W * i), ob);
@@ -61,6 +69,12 @@ struct rope_unit {
     }
   }
 };
+
+// units of a head
+template <int W, bool INTERLEAVED>
+__host__ __device__ inline int rope_units(int head_dim, int rot_dim) {
+  return INTERLEAVED && W > 1 ? head_dim / (2 * W) : rot_dim / 2 / W + (head_dim - rot_dim) / W;
+}
 
 template <class X, class Y, int W, bool INTERLEAVED>
 __global__ __launch_bounds__(512) void k_rope(int heads, int per, int head_dim, int rot_dim,
@@ -74,7 +88,7 @@ __global__ __launch_bounds__(512) void k_rope(int heads, int per, int head_dim, 
   const int half = rot_dim / 2, h0 = blockIdx.y * per, count = min(per, heads - h0);
   x += t * xt + h0 * xh;
   out += t * ot + h0 * oh;
-  const int turned = half / W, units = turned + (head_dim - rot_dim) / W, all = count * units;
+  const int turned = half / W, units = rope_units<W, INTERLEAVED>(head_dim, rot_dim), all = count * units;
   rope_unit<X, Y, W, INTERLEAVED> now;
   int u = threadIdx.x;
   if (u < all) now.load(x, xh, u, units, turned, half);
@@ -104,13 +118,11 @@ struct rope_args {
   int64_t ot, oh;
 };
 
-template <class X, class Y>
+template <class X, class Y, int W, bool INTERLEAVED>
 dbs_status launch_rope(const rope_args &r, hipStream_t s) {
-  // eight elements a lane where rotated and copied parts are made of eights
-  const int w = r.rot_dim % 16 == 0 && (r.head_dim - r.rot_dim) % 8 == 0 ? 8 : 1;
   // All heads of a token share its sines; few tokens are spread over workgroups of 256 lanes by head, or one would do the
   // work of a chip.
-  const int units = (r.rot_dim / 2 + r.head_dim - r.rot_dim) / w;
+  const int units = rope_units<W, INTERLEAVED>(r.head_dim, r.rot_dim);
   int per = r.heads;
   if (r.tokens < 512) per = units >= 256 ? 1 : 256 / units;
   if (per > r.heads) per = r.heads;
@@ -119,11 +131,26 @@ dbs_status launch_rope(const rope_args &r, hipStream_t s) {
   const int64_t all = (int64_t)per * units, rounds = (all + 511) / 512;
   const int threads = (int)((all + rounds * 64 - 1) / (rounds * 64)) * 64;
   const dim3 grid((unsigned)r.tokens, (unsigned)((r.heads + per - 1) / per));
-  const auto kernel = w == 8 ? (r.interleaved ? k_rope<X, Y, 8, true> : k_rope<X, Y, 8, false>)
-                             : (r.interleaved ? k_rope<X, Y, 1, true> : k_rope<X, Y, 1, false>);
-  hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, s, r.heads, per, r.head_dim, r.rot_dim, r.pos, r.freq, r.scale,
-                     r.direction, (const X *)r.x, r.xt, r.xh, (Y *)r.out, r.ot, r.oh);
+  hipLaunchKernelGGL((k_rope<X, Y, W, INTERLEAVED>), grid, dim3(threads), 0, s, r.heads, per, r.head_dim, r.rot_dim, r.pos,
+                     r.freq, r.scale, r.direction, (const X *)r.x, r.xt, r.xh, (Y *)r.out, r.ot, r.oh);
   return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
+}
+
+// The widest units that the sizes are made of, up to 16 bytes a lane: wider ones would leave gaps between the lanes' stores,
+// which past the caches cost whole lines (2000 tokens of 32 heads of 256, 64 rotated, bf16 to fp32: 52 us with 64 bytes).
+template <class X, class Y>
+dbs_status launch_rope(const rope_args &r, hipStream_t s) {
+  constexpr int most = 16 / (sizeof(X) > sizeof(Y) ? sizeof(X) : sizeof(Y));
+  if (r.interleaved) {
+    if (r.head_dim % most == 0) return launch_rope<X, Y, most / 2, true>(r, s);
+    if (most == 8 && r.head_dim % 4 == 0) return launch_rope<X, Y, 2, true>(r, s);
+    return launch_rope<X, Y, 1, true>(r, s);
+  }
+  const int width = r.rot_dim / 2 | (r.head_dim - r.rot_dim);
+  if (width % most == 0) return launch_rope<X, Y, most, false>(r, s);
+  if (most == 8 && width % 4 == 0) return launch_rope<X, Y, 4, false>(r, s);
+  if (width % 2 == 0) return launch_rope<X, Y, 2, false>(r, s);
+  return launch_rope<X, Y, 1, false>(r, s);
 }
 
 // whether rows of `width` elements at i * si + j * sj are disjoint because each i's rows end before the next i's begin

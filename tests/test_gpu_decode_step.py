@@ -421,6 +421,28 @@ def test_rope(dbs, tokens, heads, dim, rot, interleaved, x_kind, y_kind):
         np.testing.assert_array_equal(host(y)[..., rot:], rounded(x[..., rot:], y_kind))
 
 
+@pytest.mark.parametrize("x_kind,y_kind", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens,heads,dim,rot", [(9, 3, 96, 24), (4, 5, 20, 12), (600, 2, 12, 6), (3, 7, 64, 18), (5, 1, 36, 2), (2, 9, 24, 0), (520, 3, 40, 38)])
+def test_rope_widths(dbs, tokens, heads, dim, rot, interleaved, x_kind, y_kind):
+    """Sizes made of units of each width, and units that rot_dim ends in."""
+    test_rope(dbs, tokens, heads, dim, rot, interleaved, x_kind, y_kind)
+
+
+def test_rope_copies_what_stands_beside_infinities(dbs):
+    """The elements from rot_dim on are copied, whatever their neighbours hold."""
+    import torch
+
+    for kind in ("f32", "bf16"):
+        x = torch.full((1, 2, 16), 3.0, device="cuda", dtype=torch.float32 if kind == "f32" else torch.bfloat16)
+        x[0, 0, 7::2] = float("inf")
+        x[0, 1, 6::2] = float("nan")
+        out, want = torch.zeros_like(x), x[..., 6:].clone()
+        freq, _ = dbs.dbs_rope_frequencies(6)
+        dbs.dbs_rope(x, torch.tensor([5], dtype=torch.int32, device="cuda"), freq.cuda(), out, layout=dbs.DBS_ROPE_INTERLEAVED)
+        assert torch.equal(out[..., 6:].nan_to_num(1.0, 2.0), want.nan_to_num(1.0, 2.0)) and torch.isfinite(out[..., :6]).all()
+
+
 def test_rope_strides_in_place_and_padding(dbs):
     import torch
 
