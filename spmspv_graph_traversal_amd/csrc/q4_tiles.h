@@ -295,8 +295,8 @@ struct tiling {
   static constexpr int kBuffers = RW > 1 ? 2 : 1;
   static constexpr int kLds = kBuffers * kOps * kPlane;  // per split
   static constexpr int kDepth = 2;                // column blocks in flight
-  // sixteen waves may use 128 registers each, eight 256
-  static constexpr int kThreads = FEW || MATS * R * TT * kOps <= 2 ? 1024 : 512;
+  // sixteen waves may use 128 registers each, twelve 168, eight 256
+  static constexpr int kThreads = FEW || MATS * R * TT * kOps <= 2 ? 1024 : MATS * R * TT == 1 ? 768 : 512;
   static_assert(kLoads >= 1, "");
 };
 
