@@ -83,7 +83,10 @@ struct id_list {
  * seen.  The bias of an id that comes twice is its last entry's: the slab keeps the highest entry number.
  *
  * Bound by memory, if a workgroup's chain of loads is kept short: first the logits or, with a mask, its words (logits that
- * it closes are not read at all), the row's scalars at once, the lists, and only then the counting.
+ * it closes are not read at all), the row's scalars at once, the lists, and only then the counting.  96 rows of 131072 fp32
+ * logits with 4000 ids, 100 biases and a mask each 24.8 us (114 MB moved, 4.6 TB/s; without lists and mask 20.2, a library
+ * copy of the same rows 20.9); one row of 65536 4.2 us, of which the launch is 1.95.  Rows before slabs in the grid, so that
+ * a row's lists stay on one die, was slower: 33.7 us against 30.8 (both before the stores past the caches).
  */
 template <class X, class Y, int PIECES>
 __global__ __launch_bounds__(512) void k_logits(int vocab, const X *logits, int64_t ld_in, dbs_logits_params q, Y *out,
