@@ -26,7 +26,7 @@ struct q4_args {
 struct q4_shape {
   bool few;    // one to four tokens
   int tiles;   // else: token tiles of 16 a workgroup, 1 or 2 (bf16)
-  int rows;    // row blocks a workgroup: 1 or 2 (few), 1, 4 or 8 (one matrix; fp32 or two tiles)
+  int rows;    // row blocks a workgroup: 1 or 2 (few), 1, 2, 4 or 8 (one matrix; fp32 or two tiles)
   int splits;  // waves that split the columns
 };
 
@@ -575,6 +575,10 @@ hipError_t launch_shape(const q4_args &q, const q4_shape &p, hipStream_t s) {
     return hipErrorInvalidValue;
   }
   if (p.rows == 1) return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 1, false>(q, p.splits, s);
+  if (p.rows == 2) {
+    if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 1, false>(q, p.splits, s);
+    else return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 2, false>(q, p.splits, s);
+  }
   if (p.rows == 4) {
     if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 2, false>(q, p.splits, s);
     else return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 4, false>(q, p.splits, s);

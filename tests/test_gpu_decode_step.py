@@ -102,6 +102,35 @@ def test_products_of_many_rows_are_exact_on_integers(dbs, m, n, group, zeros, sc
         assert torch.equal(y.double(), torch.where(wanted, g, -np.inf)), f"{t} tokens, masked"
 
 
+@pytest.mark.parametrize("x_kind", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,group,zeros,scales", [(4099, 4100, 128, True, "bf16"), (4097, 700, 32, False, "f32"),
+                                                    (7003, 2111, 64, True, "bf16"), (14500, 520, 64, False, "bf16")])
+def test_products_of_two_row_blocks_are_exact_on_integers(dbs, m, n, group, zeros, scales, x_kind):
+    """Matrices whose row blocks, and pairs of row and token blocks, are shared out two to a workgroup (and the counts beside)."""
+    import torch
+
+    rng = np.random.default_rng(m * 3 + n)
+    w, u = ref.Q4(rng, m, n, group, zeros, scales), ref.Q4(rng, m, n, group, zeros, scales)
+    A, U = w.build(dbs), u.build(dbs)
+    w64, u64 = torch.from_numpy(w.w).cuda().t(), torch.from_numpy(u.w).cuda().t()
+    for t in (1, 2, 3, 4, 5, 15, 16, 20, 31, 33):
+        x = cuda(integers(rng, t, n))
+        xx = x.bfloat16() if x_kind == "bf16" else x
+        g, h = x.double() @ w64, x.double() @ u64
+        y = empty((t, m), "f32")
+        dbs.dbs_q4_product(A, xx, y)
+        assert torch.equal(y.double(), g), f"{t} tokens"
+        dbs.dbs_q4_gated(A, U, xx, dbs.DBS_ACT_RELU, y)
+        assert torch.equal(y, (g.clamp_min(0) * h).float()), f"{t} tokens, gated"
+        words = cuda(rng.integers(-2 ** 31, 2 ** 31, (t, (m + 31) // 32)).astype(np.int32))
+        words[:, : m // 80] = 0
+        words[:, -1] = 2 - (1 << 31)
+        row = torch.arange(m, device="cuda")
+        wanted = (words[:, row // 32] >> (row % 32)) & 1 != 0
+        dbs.dbs_q4_product_masked(A, xx, words, y)
+        assert torch.equal(y.double(), torch.where(wanted, g, -np.inf)), f"{t} tokens, masked"
+
+
 @pytest.mark.parametrize("m,n,group,zeros,scales", [(26003, 1590, 32, True, "bf16"), (26003, 1537, 64, False, "f32"),
                                                     (24100, 3101, 128, True, "bf16")])
 def test_products_of_two_token_tiles_are_exact_on_integers(dbs, m, n, group, zeros, scales):
