@@ -9,54 +9,54 @@
 
 namespace {
 
-// one thread per code dword of the layout
+// a code dword of the layout to a thread at a time
 __global__ __launch_bounds__(256) void k_q4_codes(int m, int n, int group, int mt, int kt, const uint8_t *__restrict__ codes,
                                                   const uint8_t *__restrict__ zeros, uint32_t *__restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (int64_t)mt * kt * 256) return;
-  const int64_t tile = i >> 8;
-  const int lane = (int)(i >> 2) & 63, s = (int)i & 3;
-  const int64_t row = tile / kt * Q4_ROWS + (lane & 15);
-  const int64_t col0 = tile % kt * Q4_COLS + 32 * s + 8 * (lane >> 4);
-  const int64_t groups = ((int64_t)n + group - 1) / group;
-  uint32_t w = 0u;
-  for (int e = 0; e < 8; ++e) {
-    uint32_t c = 8u;
-    const int64_t col = col0 + e;
-    if (row < m && col < n) {
-      const uint8_t two = codes[row * (((int64_t)n + 1) / 2) + (col >> 1)];
-      c = (col & 1) ? two >> 4 : two & 15u;
-    } else if (row < m && zeros && col / group < groups) {
-      c = zeros[row * groups + col / group] & 15u;  // the rest of a cut group: weight zero
+  const int64_t all = (int64_t)mt * kt * 256, groups = ((int64_t)n + group - 1) / group;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t tile = i >> 8;
+    const int lane = (int)(i >> 2) & 63, s = (int)i & 3;
+    const int64_t row = tile / kt * Q4_ROWS + (lane & 15);
+    const int64_t col0 = tile % kt * Q4_COLS + 32 * s + 8 * (lane >> 4);
+    uint32_t w = 0u;
+    for (int e = 0; e < 8; ++e) {
+      uint32_t c = 8u;
+      const int64_t col = col0 + e;
+      if (row < m && col < n) {
+        const uint8_t two = codes[row * (((int64_t)n + 1) / 2) + (col >> 1)];
+        c = (col & 1) ? two >> 4 : two & 15u;
+      } else if (row < m && zeros && col / group < groups) {
+        c = zeros[row * groups + col / group] & 15u;  // the rest of a cut group: weight zero
+      }
+      const int b = q4_code_bit(e);
+      w |= c << b;
+      if (b > 28) w |= c >> (32 - b);
     }
-    const int b = q4_code_bit(e);
-    w |= c << b;
-    if (b > 28) w |= c >> (32 - b);
+    out[i] = w;
   }
-  out[i] = w;
 }
 
-// one thread per record; a zero point above 15 sets *bad
+// a record to a thread at a time; a zero point above 15 sets *bad
 template <class S>
 __global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int mt, int kt, const S *__restrict__ scales,
                                                     const uint8_t *__restrict__ zeros, uint32_t *__restrict__ out,
                                                     uint32_t *bad) {
   const int gpt = Q4_COLS / group;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (int64_t)mt * kt * Q4_ROWS * gpt) return;
-  const int64_t tile = i / (Q4_ROWS * gpt);
-  const int64_t row = tile / kt * Q4_ROWS + (i / gpt) % Q4_ROWS, g = tile % kt * gpt + i % gpt;
-  const int64_t groups = ((int64_t)n + group - 1) / group;
-  const bool in = row < m && g < groups;
-  uint32_t z = 8u;
-  if (in && zeros) z = zeros[row * groups + g];
-  if (z > 15u) *bad = 1u;
-  const float off = (float)(16u + z);
-  if (sizeof(S) == 4) {
-    out[2 * i] = in ? __float_as_uint((float)scales[row * groups + g]) : 0u;
-    out[2 * i + 1] = __float_as_uint(off);
-  } else {
-    out[i] = (in ? (uint32_t)scales[row * groups + g] << 16 : 0u) | __float_as_uint(off) >> 16;
+  const int64_t all = (int64_t)mt * kt * Q4_ROWS * gpt, groups = ((int64_t)n + group - 1) / group;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t tile = i / (Q4_ROWS * gpt);
+    const int64_t row = tile / kt * Q4_ROWS + (i / gpt) % Q4_ROWS, g = tile % kt * gpt + i % gpt;
+    const bool in = row < m && g < groups;
+    uint32_t z = 8u;
+    if (in && zeros) z = zeros[row * groups + g];
+    if (z > 15u) *bad = 1u;
+    const float off = (float)(16u + z);
+    if (sizeof(S) == 4) {
+      out[2 * i] = in ? __float_as_uint((float)scales[row * groups + g]) : 0u;
+      out[2 * i + 1] = __float_as_uint(off);
+    } else {
+      out[i] = (in ? (uint32_t)scales[row * groups + g] << 16 : 0u) | __float_as_uint(off) >> 16;
+    }
   }
 }
 
@@ -148,8 +148,8 @@ dbs_status q4_build(dbs_q4_matrix *A, const uint8_t *codes, const void *scales, 
   A->bytes = code_bytes + rec_bytes + 4;
   uint32_t *bad = A->recs + rec_bytes / 4;
   if ((e = DBS_NOTE(hipMemsetAsync(bad, 0, 4, s))) != hipSuccess) return map_err(e);
-  const int64_t g1 = tiles, g2 = (nrec + 255) / 256;
-  if (g1 > 0x7FFFFFFF || g2 > 0x7FFFFFFF) return DBS_ERR_UNSUPPORTED;
+  // a launch's lanes are counted in 32 bits, a large matrix's dwords are not
+  const int64_t most = 16384, g1 = tiles < most ? tiles : most, g2 = (nrec + 255) / 256 < most ? (nrec + 255) / 256 : most;
   hipLaunchKernelGGL(k_q4_codes, dim3((unsigned)g1), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt, codes, zeros, A->codes);
   if (A->scale_dtype == DBS_F32)
     hipLaunchKernelGGL(k_q4_records<float>, dim3((unsigned)g2), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt,

@@ -131,10 +131,17 @@ dbs_status launch_rope(const rope_args &r, hipStream_t s) {
   // rounds of at most 512 lanes, all nearly full
   const int64_t all = (int64_t)per * units, rounds = (all + 511) / 512;
   const int threads = (int)((all + rounds * 64 - 1) / (rounds * 64)) * 64;
-  const dim3 grid((unsigned)r.tokens, (unsigned)((r.heads + per - 1) / per));
-  hipLaunchKernelGGL((k_rope<X, Y, W, INTERLEAVED>), grid, dim3(threads), 0, s, r.heads, per, r.head_dim, r.rot_dim, r.pos,
-                     r.freq, r.scale, r.direction, (const X *)r.x, r.xt, r.xh, (Y *)r.out, r.ot, r.oh);
-  return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
+  // a launch's lanes are counted in 32 bits
+  const int most = (int)(0x7FFFFFFF / threads);
+  for (int t = 0;; t += most) {
+    const int count = r.tokens - t < most ? r.tokens - t : most;
+    const dim3 grid((unsigned)count, (unsigned)((r.heads + per - 1) / per));
+    hipLaunchKernelGGL((k_rope<X, Y, W, INTERLEAVED>), grid, dim3(threads), 0, s, r.heads, per, r.head_dim, r.rot_dim,
+                       r.pos + t, r.freq, r.scale, r.direction, (const X *)r.x + t * r.xt, r.xt, r.xh,
+                       (Y *)r.out + t * r.ot, r.ot, r.oh);
+    if (DBS_NOTE(hipGetLastError()) != hipSuccess) return DBS_ERR_DEVICE;
+    if (count == r.tokens - t) return DBS_OK;
+  }
 }
 
 // The widest units that the sizes are made of, up to 16 bytes a lane: wider ones would leave gaps between the lanes' stores,

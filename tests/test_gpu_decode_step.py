@@ -458,6 +458,22 @@ def test_rope_widths(dbs, tokens, heads, dim, rot, interleaved, x_kind, y_kind):
     test_rope(dbs, tokens, heads, dim, rot, interleaved, x_kind, y_kind)
 
 
+def test_rope_of_more_tokens_than_one_launch_takes(dbs):
+    import torch
+
+    tokens = (1 << 31) // 64 + 1000  # workgroups of one wave
+    pos = torch.full((tokens,), -1, device="cuda", dtype=torch.int32)
+    x = torch.full((tokens, 1, 2), 1.0, device="cuda", dtype=torch.bfloat16)
+    out = torch.full_like(x, 7.0)
+    live = torch.tensor([0, 1, (1 << 31) // 64 - 2, (1 << 31) // 64 - 1, (1 << 31) // 64, tokens - 1], device="cuda")
+    pos[live] = 1
+    freq = torch.tensor([np.pi / 2], device="cuda", dtype=torch.float64)  # (1, 1) becomes (-1, 1)
+    dbs.dbs_rope(x, pos, freq, out)
+    # the sine of half a turn's half in fp32 and two products: far below a step of bf16 at 1
+    assert torch.equal(out[live, 0], torch.tensor([[-1.0, 1.0]], device="cuda", dtype=torch.bfloat16).expand(len(live), 2))
+    assert int((out != 7).any(-1).sum()) == len(live)
+
+
 def test_rope_copies_what_stands_beside_infinities(dbs):
     """The elements from rot_dim on are copied, whatever their neighbours hold."""
     import torch
