@@ -383,6 +383,8 @@ def dbs_q4_build(m, n, group, codes, scales, zeros=None, stream=None) -> Q4Matri
     m, n, group = int(m), int(n), int(group)
     if group not in (32, 64, 128):
         raise ValueError(f"group {group}: 32, 64 or 128 expected")
+    if m > DBS_Q4_MAX_ROWS or n > DBS_Q4_MAX_COLUMNS:  # here, since ctypes keeps the low 32 bits
+        raise ValueError(f"{m} x {n} is too large: at most {DBS_Q4_MAX_ROWS} x {DBS_Q4_MAX_COLUMNS}")
     groups = (n + group - 1) // group
     _need(codes, "codes", (_torch.uint8,), m * ((n + 1) // 2))
     _need(scales, "scales", tuple(_VECTOR), m * groups)

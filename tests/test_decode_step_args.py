@@ -29,6 +29,14 @@ def test_q4_build_limits():
     assert q4_build(n=b.DBS_Q4_MAX_COLUMNS + 1) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("m,n", [((1 << 32) + 4, 8), (4, (1 << 32) + 8), (b.DBS_Q4_MAX_ROWS + 1, 8)])
+def test_q4_sizes_past_32_bits_are_not_cut(m, n):
+    import torch
+
+    with pytest.raises(ValueError, match="too large"):
+        b.dbs_q4_build(m, n, 32, torch.zeros(16, dtype=torch.uint8), torch.ones(4))
+
+
 def test_q4_calls_without_a_handle():
     v = C.c_int64()
     assert _lib.dbs_q4_bytes(None, C.byref(v)) == INVALID
