@@ -70,6 +70,16 @@ struct call {
       stream = PyLong_AsVoidPtr(raw);
       Py_DECREF(raw);
       if (!stream && PyErr_Occurred()) throw failed();
+      PyObject *at = PyObject_GetAttrString(given, "device_index");
+      if (at) {
+        const long index = PyLong_AsLong(at);
+        Py_DECREF(at);
+        if (index == -1 && PyErr_Occurred()) throw failed();
+        if (index != device)
+          fail(PyExc_ValueError, "the stream is on device %ld, the call runs on the current device, %d", index, device);
+      } else {
+        PyErr_Clear();
+      }
     }
   }
   const at::Tensor &tensor(PyObject *o, const char *name) const {

@@ -657,6 +657,25 @@ def test_choices_past_32_bits_are_refused(dbs):
     assert (y == 5).all()
 
 
+def test_streams_of_another_device_are_refused(dbs):
+    import torch
+
+    class Stream:
+        cuda_stream = 0
+
+        def __init__(self, device_index):
+            self.device_index = device_index
+
+    x, y = torch.ones(2, 64, device="cuda"), torch.full((2, 64), 5.0, device="cuda")
+    with pytest.raises(ValueError, match="stream"):
+        dbs.dbs_logits_adjust(x, y, stream=Stream(torch.cuda.current_device() + 1))
+    torch.cuda.synchronize()
+    assert (y == 5).all()
+    dbs.dbs_logits_adjust(x, y, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert (y == 1).all()
+
+
 def test_calls_of_two_threads_on_their_own_streams(dbs):
     import threading
 
