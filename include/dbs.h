@@ -389,7 +389,7 @@ dbs_status dbs_q4_free(dbs_q4_handle A);
  * dbs_q4_product — y_t = W x_t for `tokens` vectors, fp32 accumulation, one
  * rounding to y's type.
  *
- *   tokens   0 <= tokens <= DBS_Q4_MAX_TOKENS; made for one to 64 (16 or 32 at a time, each
+ *   tokens   0 <= tokens <= DBS_Q4_MAX_TOKENS; made for one to 64 (up to 32 at a time, each time
  *            going through the weights, which come from memory once if the tokens are few)
  *   x        device [tokens][n], row stride ldx >= n elements
  *   y        device [tokens][m], row stride ldy >= m elements

@@ -69,8 +69,9 @@ __global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int
  *   blocks fill the chip with four splits, and from 900 on two a wave keep more bytes in flight for the same waves (16000 x
  *   6016 11.1 against 12.6; 11008 x 4096 7.7 against 7.3).  Under a mask one row block is the unit: 256 of 65536 rows wanted
  *   6.6 against 8.1.
- *   More tokens, 16 at a time.  Up to 256 pairs of row and token blocks one each (3000 x 11008, 6 tokens, 8.1 with sixteen
- *   splits against 8.5 with eight; fp32 16.8 with twelve against 18.0), up to 512 two (4096 x 4096, 32 tokens, 6.2 against 8.0
+ *   More tokens, 16 at a time; up to eight fetch and cut half of x (3000 x 11008, 6 tokens, 7.4 against 8.5, fp32 13.5 against
+ *   17.5).  Up to 256 pairs of row and token blocks one each (1152 x 4096, 16 tokens, 4.8 with sixteen
+ *   splits against 5.0 with eight; fp32 8.0 with twelve against 8.7), up to 512 two (4096 x 4096, 32 tokens, 6.2 against 8.0
  *   with one and 8.5 with four; fp32 10.9 against 14.8 and 13.7; gated 9.4 against 10.3 and 11.9).  Then four that share x
  *   (11008 x 4096, 16 tokens, 8.9 against 9.9 with one; gated 12.6 against 13.0), with two splits once that fills the chip (64
  *   tokens 17.4); cutting an fp32 x costs more, so eight share it (8640 x 1856, 29 tokens, 12.6 against 14.5).  Two token tiles
@@ -82,15 +83,16 @@ __global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int
  */
 q4_shape pick_shape(const dbs_q4_matrix *A, int tokens, dbs_dtype xd, bool gated, bool masked) {
   q4_shape p = {};
-  p.few = tokens <= 4;
-  if (p.few) {
+  if (tokens <= 4) {
+    p.tokens = 4;
     p.rows = !gated && !masked && ((A->mt > 256 && A->mt <= 512) || A->mt >= 900) ? 2 : 1;
     p.splits = A->mt <= 256 * p.rows ? 16 : 4;
   } else {
     const int64_t work = A->mt * (int64_t)((tokens + 15) / 16);
     const bool whole_pairs = (tokens + 15) / 16 % 2 == 0;
-    p.tiles = xd == DBS_BF16 && whole_pairs && work > (gated ? 1200 : 3000) && A->kt >= (gated ? 24 : 12) ? 2 : 1;
-    p.rows = work <= 256 ? 1 : work <= 512 ? 2 : !gated && (p.tiles == 2 || (work > 1024 && xd == DBS_F32)) ? 8 : 4;
+    const bool pairs = xd == DBS_BF16 && whole_pairs && work > (gated ? 1200 : 3000) && A->kt >= (gated ? 24 : 12);
+    p.tokens = pairs ? 32 : tokens <= 8 ? 8 : 16;
+    p.rows = work <= 256 ? 1 : work <= 512 ? 2 : !gated && (pairs || (work > 1024 && xd == DBS_F32)) ? 8 : 4;
     if (p.rows == 1) p.splits = xd == DBS_BF16 ? 16 : !gated && A->kt >= 24 ? 12 : 8;
     else if (p.rows == 2) p.splits = xd == DBS_BF16 && !gated ? 16 : 8;
     else p.splits = p.rows == 4 && work <= 2048 ? 4 : 2;

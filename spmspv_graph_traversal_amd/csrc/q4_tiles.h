@@ -24,9 +24,8 @@ struct q4_args {
 
 // How a call is cut into workgroups.
 struct q4_shape {
-  bool few;    // one to four tokens
-  int tiles;   // else: token tiles of 16 a workgroup, 1 or 2 (bf16)
-  int rows;    // row blocks a workgroup: 1 or 2 (few), 1, 2, 4 or 8 (one matrix; fp32 or two tiles)
+  int tokens;  // a workgroup: 4, 8, 16 or 32 (bf16)
+  int rows;    // row blocks a workgroup: 1 or 2 (4 tokens), 1, 2, 4 or 8 (one matrix; fp32 or 32 tokens)
   int splits;  // waves that split the columns
 };
 
@@ -261,7 +260,8 @@ DBS_DEV void finish(const q4_args &q, const float *part, int parts, int stride, 
 }
 
 /*
- * y_t = W x_t for a workgroup's 16 R row_waves rows (of MATS matrices) and 16 TT tokens (FEW: up to four).
+ * y_t = W x_t for a workgroup's 16 R RW rows (of MATS matrices; RW waves share x) and TOKENS tokens: tiles of 16, of which 8
+ * leave the upper half as it is in LDS (its sums are dropped), or up to four (FEW).
  *
  * Mathematics: with off = 16 + zero, a group's part of y is
  *   scale (sum (16 + q) x - off sum x),
@@ -291,13 +291,15 @@ DBS_DEV void finish(const q4_args &q, const float *part, int parts, int stride, 
  * are out of range of the codes' buffer descriptor and read nothing.  Streaming loads of the codes (past the caches) were
  * slower: gated 12.1 us against 11.1.
  */
-template <class X, int MATS, int R, int TT, int RW, bool FEW>
+template <class X, int MATS, int R, int TOKENS, int RW>
 struct tiling {
+  static constexpr bool FEW = TOKENS == 4;
+  static constexpr int TT = TOKENS < 16 ? 1 : TOKENS / 16;
   static constexpr int P = x_piece<X>::parts;
   static constexpr int kOps = FEW ? 1 : P;               // operands of a token tile and step
   static constexpr int kSums = kOps > 1 ? 2 : 1;         // sums: first part, other parts
   static constexpr int kRowsPerLoad = 64 * x_piece<X>::columns / Q4_COLS;
-  static constexpr int kTokens = FEW ? 4 : 16 * TT;
+  static constexpr int kTokens = TOKENS;
   static constexpr int kLoads = kTokens / kRowsPerLoad / RW;  // of a column block's x, per wave
   static constexpr int kPlane = TT * 16 * 256;           // bytes of a part of x
   static constexpr int kBuffers = RW > 1 ? 2 : 1;
@@ -308,10 +310,12 @@ struct tiling {
   static_assert(kLoads >= 1, "");
 };
 
-template <class X, int WORDS, int GPT, int MATS, int R, int TT, int RW, bool FEW>
-__global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k_q4(q4_args q) {
+template <class X, int WORDS, int GPT, int MATS, int R, int TOKENS, int RW>
+__global__ __launch_bounds__((tiling<X, MATS, R, TOKENS, RW>::kThreads)) void k_q4(q4_args q) {
   extern __shared__ uint4 lds[];
-  typedef tiling<X, MATS, R, TT, RW, FEW> T;
+  typedef tiling<X, MATS, R, TOKENS, RW> T;
+  constexpr bool FEW = T::FEW;
+  constexpr int TT = T::TT;
   constexpr int kRec = GPT * WORDS, kTokens = T::kTokens, rows = Q4_ROWS * R * RW;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rw = wave % RW, split = wave / RW, splits = (blockDim.x >> 6) / RW;
@@ -522,6 +526,7 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k
           for (int i = 0; i < 4; ++i) {
             if (FEW && T::P > 1 && i) continue;
             if (FEW && T::P == 1 && kq) continue;
+            if (TOKENS == 8 && kq > 1) continue;
             const int token = FEW ? (T::P > 1 ? kq : i) : 16 * t + 4 * kq + i;
             use((a * kTokens + token) * rows + 16 * (rw * R + r) + j, acc[a][r][t][i]);
           }
@@ -538,12 +543,12 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TT, RW, FEW>::kThreads)) void k
   finish<X, WORDS, GPT, MATS>(q, part, half, kTokens, rows, t0, tokens, row0);
 }
 
-template <class X, int WORDS, int GPT, int MATS, int R, int TT, int RW, bool FEW>
+template <class X, int WORDS, int GPT, int MATS, int R, int TOKENS, int RW>
 hipError_t launch_tiles(const q4_args &q, int splits, hipStream_t s) {
-  typedef tiling<X, MATS, R, TT, RW, FEW> T;
+  typedef tiling<X, MATS, R, TOKENS, RW> T;
   constexpr int rows = R * RW;
   while (splits * T::kLds > 160 * 1024 || 64 * splits * RW > T::kThreads) splits /= 2;
-  const auto kernel = k_q4<X, WORDS, GPT, MATS, R, TT, RW, FEW>;
+  const auto kernel = k_q4<X, WORDS, GPT, MATS, R, TOKENS, RW>;
   const unsigned groups = (unsigned)((q.mt + rows - 1) / rows), eights = (groups + 7) / 8, wide = (eights + 65534) / 65535;
   const dim3 grid(8 * wide, (unsigned)((q.tokens + T::kTokens - 1) / T::kTokens), (eights + wide - 1) / wide);
   const size_t parts = (size_t)((splits + 1) / 2) * MATS * rows * Q4_ROWS * T::kTokens * 4;
@@ -561,32 +566,39 @@ hipError_t launch_tiles(const q4_args &q, int splits, hipStream_t s) {
   return DBS_NOTE(hipGetLastError());
 }
 
-template <class X, int WORDS, int GPT, int MATS>
-hipError_t launch_shape(const q4_args &q, const q4_shape &p, hipStream_t s) {
-  if (p.few) {
-    if constexpr (MATS == 1) {
-      if (p.rows == 2) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 1, true>(q, p.splits, s);
-    }
-    return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 1, true>(q, p.splits, s);
-  }
-  if (p.tiles == 2) {
-    if constexpr (sizeof(X) == 2 && MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 2, 4, false>(q, p.splits, s);
-    if constexpr (sizeof(X) == 2 && MATS == 2) return launch_tiles<X, WORDS, GPT, MATS, 1, 2, 4, false>(q, p.splits, s);
-    return hipErrorInvalidValue;
-  }
-  if (p.rows == 1) return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 1, false>(q, p.splits, s);
+template <class X, int WORDS, int GPT, int MATS, int TOKENS>
+hipError_t launch_rows(const q4_args &q, const q4_shape &p, hipStream_t s) {
+  if (p.rows == 1) return launch_tiles<X, WORDS, GPT, MATS, 1, TOKENS, 1>(q, p.splits, s);
   if (p.rows == 2) {
-    if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 1, false>(q, p.splits, s);
-    else return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 2, false>(q, p.splits, s);
+    if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, TOKENS, 1>(q, p.splits, s);
+    else return launch_tiles<X, WORDS, GPT, MATS, 1, TOKENS, 2>(q, p.splits, s);
   }
   if (p.rows == 4) {
-    if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 2, false>(q, p.splits, s);
-    else return launch_tiles<X, WORDS, GPT, MATS, 1, 1, 4, false>(q, p.splits, s);
+    if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, TOKENS, 2>(q, p.splits, s);
+    // (of eight bf16 tokens, four waves would not have a load each)
+    else return launch_tiles<X, WORDS, GPT, MATS, 1, sizeof(X) == 2 ? 16 : TOKENS, 4>(q, p.splits, s);
   }
   if constexpr (MATS == 1 && sizeof(X) == 4) {
-    if (p.rows == 8) return launch_tiles<X, WORDS, GPT, MATS, 2, 1, 4, false>(q, p.splits, s);
+    if (p.rows == 8) return launch_tiles<X, WORDS, GPT, MATS, 2, TOKENS, 4>(q, p.splits, s);
   }
   return hipErrorInvalidValue;
+}
+
+template <class X, int WORDS, int GPT, int MATS>
+hipError_t launch_shape(const q4_args &q, const q4_shape &p, hipStream_t s) {
+  if (p.tokens == 4) {
+    if constexpr (MATS == 1) {
+      if (p.rows == 2) return launch_tiles<X, WORDS, GPT, MATS, 2, 4, 1>(q, p.splits, s);
+    }
+    return launch_tiles<X, WORDS, GPT, MATS, 1, 4, 1>(q, p.splits, s);
+  }
+  if (p.tokens == 32) {
+    if constexpr (sizeof(X) == 2 && MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 32, 4>(q, p.splits, s);
+    if constexpr (sizeof(X) == 2 && MATS == 2) return launch_tiles<X, WORDS, GPT, MATS, 1, 32, 4>(q, p.splits, s);
+    return hipErrorInvalidValue;
+  }
+  if (p.tokens == 8) return launch_rows<X, WORDS, GPT, MATS, 8>(q, p, s);
+  return launch_rows<X, WORDS, GPT, MATS, 16>(q, p, s);
 }
 
 template <class X, int MATS>
