@@ -275,7 +275,7 @@ DBS_DEV void finish(const q4_args &q, const float *part, int parts, int stride, 
  *   One token, memory and the length of a wave's chain: 4096 x 4096 4.1 us, 11008 x 4096 7.0 us (23.3 MB, 3.3 TB/s; without
  *   the launch 4.6), two of these gated 11.3 us (4.1 TB/s).
  *   Many tokens, instruction issue: a vector instruction takes four cycles of a SIMD, the unpacking of an operand (seven of
- *   them) as long as the products of two token tiles, and the two kinds hardly overlap.  11008 x 4096, 64 tokens, 18.3 us,
+ *   them) as long as the products of two token tiles, and the two kinds hardly overlap.  11008 x 4096, 64 tokens, 18.7 us,
  *   of which vector instructions issue for 7.1 and the matrix cores run for 3.4; 28672 x 8192 58 us, 520 TFLOP/s.
  *   fp32 x, 5461 x 2001 gated, 24 tokens, 14.2 us: three products and the cutting of x in place of one.
  *
