@@ -657,6 +657,58 @@ def test_choices_past_32_bits_are_refused(dbs):
     assert (y == 5).all()
 
 
+@pytest.mark.parametrize("x_kind", ["bf16", "f32"])
+def test_largest_calls(dbs, x_kind):
+    import torch
+
+    rng = np.random.default_rng(83)
+    w = ref.Q4(rng, 20, 130, 64, True)
+    A, w64 = w.build(dbs), torch.from_numpy(w.w).cuda().t()
+    tokens = dbs.DBS_Q4_MAX_TOKENS
+    x = torch.randint(-4, 5, (tokens + 1, 130), device="cuda").to(torch.bfloat16 if x_kind == "bf16" else torch.float32)
+    y = torch.zeros(tokens + 1, 20, device="cuda")
+    dbs.dbs_q4_product(A, x[:tokens], y[:tokens])
+    assert torch.equal(y[:tokens].double(), x[:tokens].double() @ w64) and (y[tokens] == 0).all()
+    with pytest.raises(dbs.DBSError):
+        dbs.dbs_q4_product(A, x, y)
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32"])
+def test_product_of_very_long_rows(dbs, x_kind):
+    """A million columns and some, of which x has a few hundred: the sums stay exact."""
+    import torch
+
+    rng = np.random.default_rng(84)
+    n = (1 << 20) + 77
+    w = ref.Q4(rng, 35, n, 128, True)
+    A, w64 = w.build(dbs), torch.from_numpy(w.w).cuda().t()
+    for t in (1, 6, 20):
+        x = np.zeros((t, n), np.float32)
+        for row in x:
+            row[rng.integers(0, n, 300)] = rng.integers(1, 5, 300)
+            row[-3:] = 2
+        x = cuda(x, x_kind)
+        y = empty((t, 35), "f32")
+        dbs.dbs_q4_product(A, x, y)
+        assert torch.equal(y.double(), x.double() @ w64), f"{t} tokens"
+
+
+def test_logits_of_the_most_rows(dbs):
+    import torch
+
+    rows = dbs.DBS_LOGITS_MAX_ROWS
+    x = torch.zeros(rows + 1, 37, device="cuda")
+    out = torch.full((rows + 1, 37), 5.0, device="cuda")
+    ptr = torch.arange(rows + 1, dtype=torch.int32, device="cuda")
+    ids = (torch.arange(rows, device="cuda") % 37).int()
+    dbs.dbs_logits_adjust(x[:rows], out[:rows], hist_ptr=ptr, hist=ids, frequency=torch.ones(rows, device="cuda"))
+    expect = torch.zeros(rows, 37, device="cuda")
+    expect[torch.arange(rows, device="cuda"), ids.long()] = -1.0
+    assert torch.equal(out[:rows], expect) and (out[rows] == 5).all()
+    with pytest.raises(dbs.DBSError):
+        dbs.dbs_logits_adjust(x, out)
+
+
 def test_streams_of_another_device_are_refused(dbs):
     import torch
 
