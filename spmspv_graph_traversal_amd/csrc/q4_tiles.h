@@ -373,8 +373,7 @@ __global__ __launch_bounds__((tiling<X, MATS, R, TOKENS, RW>::kThreads)) void k_
   uint32_t recs[D][MATS][R][kRec];
   x_piece<X> xr[D][T::kLoads];
   auto fetch_codes = [&](int d, int k, int end) {
-    const uint32_t oc = k < end ? (uint32_t)k * Q4_TILE_BYTES + lane * 16 : OOB_OFF;
-    const uint32_t orec = k < end ? ((uint32_t)k * Q4_ROWS + j) * (kRec * 4) : OOB_OFF;
+    const uint32_t oc = q4_code_offset(k, end, lane), orec = q4_record_offset(k, end, j, kRec);
 #pragma unroll
     for (int a = 0; a < MATS; ++a)
 #pragma unroll
