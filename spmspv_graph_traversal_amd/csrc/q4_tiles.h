@@ -4,7 +4,7 @@
 #include <atomic>
 #include <type_traits>
 
-#include "q4.h"
+#include "q4_shape.h"
 #include "tile_kernels.h"
 
 struct q4_args {
@@ -20,13 +20,6 @@ struct q4_args {
   int y_bf16;
   void *y;
   int64_t ldy;
-};
-
-// How a call is cut into workgroups.
-struct q4_shape {
-  int tokens;  // a workgroup: 4, 8, 16 or 32 (bf16)
-  int rows;    // row blocks a workgroup: 1 or 2 (4 tokens), 1, 2, 4 or 8 (one matrix; fp32 or 32 tokens)
-  int splits;  // waves that split the columns
 };
 
 namespace q4 {
@@ -308,6 +301,11 @@ struct tiling {
   // sixteen waves may use 128 registers each, twelve 168, eight 256
   static constexpr int kThreads = FEW || MATS * R * TT * kOps <= 2 ? 1024 : MATS * R * TT == 1 ? 768 : 512;
   static_assert(kLoads >= 1, "");
+  // as many of the splits as registers and LDS allow
+  static int fitting(int splits) {
+    while (splits * kLds > 160 * 1024 || 64 * splits * RW > kThreads) splits /= 2;
+    return splits;
+  }
 };
 
 template <class X, int WORDS, int GPT, int MATS, int R, int TOKENS, int RW>
@@ -546,7 +544,7 @@ template <class X, int WORDS, int GPT, int MATS, int R, int TOKENS, int RW>
 hipError_t launch_tiles(const q4_args &q, int splits, hipStream_t s) {
   typedef tiling<X, MATS, R, TOKENS, RW> T;
   constexpr int rows = R * RW;
-  while (splits * T::kLds > 160 * 1024 || 64 * splits * RW > T::kThreads) splits /= 2;
+  splits = T::fitting(splits);
   const auto kernel = k_q4<X, WORDS, GPT, MATS, R, TOKENS, RW>;
   const unsigned groups = (unsigned)((q.mt + rows - 1) / rows), eights = (groups + 7) / 8, wide = (eights + 65534) / 65535;
   const dim3 grid(8 * wide, (unsigned)((q.tokens + T::kTokens - 1) / T::kTokens), (eights + wide - 1) / wide);
@@ -565,51 +563,64 @@ hipError_t launch_tiles(const q4_args &q, int splits, hipStream_t s) {
   return DBS_NOTE(hipGetLastError());
 }
 
-template <class X, int WORDS, int GPT, int MATS, int TOKENS>
-hipError_t launch_rows(const q4_args &q, const q4_shape &p, hipStream_t s) {
-  if (p.rows == 1) return launch_tiles<X, WORDS, GPT, MATS, 1, TOKENS, 1>(q, p.splits, s);
+// a kernel's parameters
+template <class X, int WORDS, int GPT, int MATS, int R, int TOKENS, int RW>
+struct form {
+  static hipError_t launch(const q4_args &q, int splits, hipStream_t s) {
+    return launch_tiles<X, WORDS, GPT, MATS, R, TOKENS, RW>(q, splits, s);
+  }
+};
+
+// use() of the kernel of a shape
+template <class X, int WORDS, int GPT, int MATS, int TOKENS, class F>
+hipError_t with_rows(const q4_shape &p, const F &use) {
+  if (p.rows == 1) return use(form<X, WORDS, GPT, MATS, 1, TOKENS, 1>());
   if (p.rows == 2) {
-    if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, TOKENS, 1>(q, p.splits, s);
-    else return launch_tiles<X, WORDS, GPT, MATS, 1, TOKENS, 2>(q, p.splits, s);
+    if constexpr (MATS == 1) return use(form<X, WORDS, GPT, MATS, 2, TOKENS, 1>());
+    else return use(form<X, WORDS, GPT, MATS, 1, TOKENS, 2>());
   }
   if (p.rows == 4) {
-    if constexpr (MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, TOKENS, 2>(q, p.splits, s);
+    if constexpr (MATS == 1) return use(form<X, WORDS, GPT, MATS, 2, TOKENS, 2>());
     // (of eight bf16 tokens, four waves would not have a load each)
-    else return launch_tiles<X, WORDS, GPT, MATS, 1, sizeof(X) == 2 ? 16 : TOKENS, 4>(q, p.splits, s);
+    else return use(form<X, WORDS, GPT, MATS, 1, sizeof(X) == 2 ? 16 : TOKENS, 4>());
   }
   if constexpr (MATS == 1 && sizeof(X) == 4) {
-    if (p.rows == 8) return launch_tiles<X, WORDS, GPT, MATS, 2, TOKENS, 4>(q, p.splits, s);
+    if (p.rows == 8) return use(form<X, WORDS, GPT, MATS, 2, TOKENS, 4>());
   }
   return hipErrorInvalidValue;
 }
 
-template <class X, int WORDS, int GPT, int MATS>
-hipError_t launch_shape(const q4_args &q, const q4_shape &p, hipStream_t s) {
+template <class X, int WORDS, int GPT, int MATS, class F>
+hipError_t with_shape(const q4_shape &p, const F &use) {
   if (p.tokens == 4) {
     if constexpr (MATS == 1) {
-      if (p.rows == 2) return launch_tiles<X, WORDS, GPT, MATS, 2, 4, 1>(q, p.splits, s);
+      if (p.rows == 2) return use(form<X, WORDS, GPT, MATS, 2, 4, 1>());
     }
-    return launch_tiles<X, WORDS, GPT, MATS, 1, 4, 1>(q, p.splits, s);
+    return use(form<X, WORDS, GPT, MATS, 1, 4, 1>());
   }
   if (p.tokens == 32) {
-    if constexpr (sizeof(X) == 2 && MATS == 1) return launch_tiles<X, WORDS, GPT, MATS, 2, 32, 4>(q, p.splits, s);
-    if constexpr (sizeof(X) == 2 && MATS == 2) return launch_tiles<X, WORDS, GPT, MATS, 1, 32, 4>(q, p.splits, s);
+    if constexpr (sizeof(X) == 2) return use(form<X, WORDS, GPT, MATS, MATS == 1 ? 2 : 1, 32, 4>());
     return hipErrorInvalidValue;
   }
-  if (p.tokens == 8) return launch_rows<X, WORDS, GPT, MATS, 8>(q, p, s);
-  return launch_rows<X, WORDS, GPT, MATS, 16>(q, p, s);
+  if (p.tokens == 8) return with_rows<X, WORDS, GPT, MATS, 8>(p, use);
+  return with_rows<X, WORDS, GPT, MATS, 16>(p, use);
+}
+
+template <class X, int MATS, class F>
+hipError_t with_form(int words, int gpt, const q4_shape &p, const F &use) {
+  if (words == 1) {
+    if (gpt == 1) return with_shape<X, 1, 1, MATS>(p, use);
+    if (gpt == 2) return with_shape<X, 1, 2, MATS>(p, use);
+    return with_shape<X, 1, 4, MATS>(p, use);
+  }
+  if (gpt == 1) return with_shape<X, 2, 1, MATS>(p, use);
+  if (gpt == 2) return with_shape<X, 2, 2, MATS>(p, use);
+  return with_shape<X, 2, 4, MATS>(p, use);
 }
 
 template <class X, int MATS>
 hipError_t launch(const q4_args &q, int words, int gpt, const q4_shape &p, hipStream_t s) {
-  if (words == 1) {
-    if (gpt == 1) return launch_shape<X, 1, 1, MATS>(q, p, s);
-    if (gpt == 2) return launch_shape<X, 1, 2, MATS>(q, p, s);
-    return launch_shape<X, 1, 4, MATS>(q, p, s);
-  }
-  if (gpt == 1) return launch_shape<X, 2, 1, MATS>(q, p, s);
-  if (gpt == 2) return launch_shape<X, 2, 2, MATS>(q, p, s);
-  return launch_shape<X, 2, 4, MATS>(q, p, s);
+  return with_form<X, MATS>(words, gpt, p, [&](auto kernel) { return kernel.launch(q, p.splits, s); });
 }
 
 }  // namespace q4

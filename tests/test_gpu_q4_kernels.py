@@ -1,6 +1,8 @@
 """Each kernel of the 4-bit products, chosen by sizes and types, on inputs whose results are exact."""
 import pytest
 
+from q4_forms import CALLS, SCALES
+
 pytestmark = pytest.mark.gpu
 
 
@@ -25,3 +27,35 @@ def test_rounds_without_a_column_block_add_nothing(dbs, kind, gated, m, n, token
     from q4_device import check_products, small
 
     check_products(dbs, m + n + tokens, m, n, tokens, 32, True, "f32", gated, small(n, tokens, n, kind))
+
+
+@pytest.mark.parametrize("scales,group", SCALES)
+@pytest.mark.parametrize("kind,gated,m,tokens,columns", CALLS)
+def test_every_kernel_is_exact_on_integers(dbs, kind, gated, m, tokens, columns, scales, group):
+    from q4_device import check_products, small
+
+    for n in columns:
+        check_products(dbs, m + n + tokens, m, n, tokens, group, group != 64, scales, gated, small(n, tokens, n, kind))
+
+
+def test_row_groups_of_more_than_one_grid_row(dbs):
+    """More row groups than eight grid rows of 65535 hold: the grid folds them."""
+    import torch
+
+    from q4_device import Q4, small
+
+    m, n = 16 * 8 * 65535 + 5000, 9
+    w = Q4(5, m, n, 32, True, "bf16")
+    A, w64 = w.build(dbs), w.w.t()
+    for tokens, kind in ((1, "bf16"), (3, "f32"), (6, "bf16")):
+        x = small(tokens, tokens, n, kind)
+        y = torch.full((tokens, m), 7.0, device="cuda")
+        words = torch.full((tokens, (m + 31) // 32), -1, device="cuda", dtype=torch.int32)
+        words[:, 100:-200] = 0
+        dbs.dbs_q4_product_masked(A, x, words, y)  # sixteen rows a workgroup, up to four tokens
+        expect = x.double() @ w64
+        inside = slice(3200, (words.shape[1] - 200) * 32)
+        assert torch.equal(y[:, :3200].double(), expect[:, :3200]) and (y[:, inside] == -torch.inf).all()
+        assert torch.equal(y[:, inside.stop:].double(), expect[:, inside.stop:])
+        dbs.dbs_q4_product(A, x, y)
+        assert torch.equal(y.double(), expect)
