@@ -33,6 +33,18 @@ def small(seed, tokens, n, kind):
     return x.to(torch.bfloat16 if kind == "bf16" else torch.float32)
 
 
+def wide(seed, tokens, n):
+    """fp32 vectors of four odd integers of 17 bits and zeros.  Bits 16, 8 and 0 are set, so that each of the three bf16 parts of
+    eight bits that the kernels cut them into holds something.  Their products with |q - z| <= 15 and scales of 1 and 1/2 have a sum of at most 24 bits (4 * 15 * 2^17 * 2 < 2^24), as
+    have the sums with 16 + q of the first parts (multiples of 2^9) and of the others (below 2^9)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    at = torch.rand(tokens, n, device="cuda", generator=g).topk(min(4, n)).indices
+    at[:, 0] = torch.arange(tokens, device="cuda") * 37 % n  # tokens together all over the columns
+    value = torch.randint(1 << 16, 1 << 17, at.shape, device="cuda", generator=g) | 257
+    value *= 2 * torch.randint(0, 2, at.shape, device="cuda", generator=g) - 1
+    return torch.zeros(tokens, n, device="cuda").scatter_(1, at, value.float())
+
+
 def open_rows(words, m):
     row = torch.arange(m, device=words.device)
     return (words[:, row // 32] >> (row % 32)) & 1 != 0

@@ -38,6 +38,15 @@ def test_every_kernel_is_exact_on_integers(dbs, kind, gated, m, tokens, columns,
         check_products(dbs, m + n + tokens, m, n, tokens, group, group != 64, scales, gated, small(n, tokens, n, kind))
 
 
+@pytest.mark.parametrize("scales,group", SCALES)
+@pytest.mark.parametrize("kind,gated,m,tokens,columns", [c for c in CALLS if c[0] == "f32"])
+def test_every_fp32_kernel_keeps_the_low_parts_of_x(dbs, kind, gated, m, tokens, columns, scales, group):
+    from q4_device import check_products, wide
+
+    for n in columns:
+        check_products(dbs, 1 + m + n + tokens, m, n, tokens, group, group != 64, scales, gated, wide(n, tokens, n), halvings=1)
+
+
 def test_row_groups_of_more_than_one_grid_row(dbs):
     """More row groups than eight grid rows of 65535 hold: the grid folds them."""
     import torch
