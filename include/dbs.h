@@ -396,6 +396,19 @@ dbs_status dbs_q4_free(dbs_q4_handle A);
  *
  * Infinities and NaN in x or the scales spread as in the formula, to the
  * tokens and rows whose sums hold them.
+ *
+ * A group's part of y is scale (sum (16 + code) x - (16 + zero) sum x), each
+ * sum rounded for itself: before its rounding to y's type, y_ti is off by at
+ * most
+ *
+ *   (387 + groups of a row) 2^-24 sum_j |scale x_j| (32 + code + zero)
+ *
+ * which is relative to these magnitudes, not to |W_ij x_j| (on ordinary data
+ * a few 2^-24 of them, since roundings go either way).  A group of a row whose
+ * codes all equal its zero point adds nothing: a row of such groups (pruned
+ * or padding) is exactly 0 for finite x.  Other results that the formula makes 0 by
+ * cancelling, or by zeros in x under nonzero weights, may come out as such a
+ * small number.
  */
 dbs_status dbs_q4_product(dbs_q4_handle A, int32_t tokens, const void *x, dbs_dtype x_dtype, int64_t ldx,
                           void *y, dbs_dtype y_dtype, int64_t ldy, void *stream);
@@ -415,7 +428,8 @@ dbs_status dbs_q4_product_masked(dbs_q4_handle A, int32_t tokens, const void *x,
                                  dbs_dtype y_dtype, int64_t ldy, void *stream);
 
 /* activations of dbs_q4_gated: g / (1 + exp(-g)); g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)));
- * max(g, 0) (whose zeros a following dbs_spmspv_dense skips) */
+ * max(g, 0) (whose zeros a following dbs_spmspv_dense skips; a gate that the formula makes 0 by cancelling may be within
+ * the product's error above 0 instead, which dbs_spmspv_dense_threshold drops) */
 typedef enum { DBS_ACT_SILU = 0, DBS_ACT_GELU_TANH = 1, DBS_ACT_RELU = 2 } dbs_activation;
 
 /*

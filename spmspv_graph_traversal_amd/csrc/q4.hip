@@ -36,11 +36,20 @@ __global__ __launch_bounds__(256) void k_q4_codes(int m, int n, int group, int m
   }
 }
 
-// a record to a thread at a time; a zero point above 15 sets *bad
+// whether all weights of a row's columns [low, high) are zero: low even, `row` the row's codes
+DBS_DEV bool q4_all_zero(const uint8_t *row, int64_t low, int64_t high, uint32_t zero) {
+  for (int64_t c = low; c < high; c += 2)
+    if ((row[c >> 1] ^ zero * 17u) & (c + 1 < high ? 255u : 15u)) return false;
+  return true;
+}
+
+// A record to a thread at a time; a zero point above 15 sets *bad.  A group whose weights are all zero gets the scale 0: the
+// products subtract sums of (16 + zero) x from sums of (16 + code) x that are rounded apart, and would leave some 2^-24 of these.
+// (An infinite or NaN scale stays, its weights are NaN.)
 template <class S>
-__global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int mt, int kt, const S *__restrict__ scales,
-                                                    const uint8_t *__restrict__ zeros, uint32_t *__restrict__ out,
-                                                    uint32_t *bad) {
+__global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int mt, int kt, const uint8_t *__restrict__ codes,
+                                                    const S *__restrict__ scales, const uint8_t *__restrict__ zeros,
+                                                    uint32_t *__restrict__ out, uint32_t *bad) {
   const int gpt = Q4_COLS / group;
   const int64_t all = (int64_t)mt * kt * Q4_ROWS * gpt, groups = ((int64_t)n + group - 1) / group;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (int64_t)gridDim.x * blockDim.x) {
@@ -51,11 +60,17 @@ __global__ __launch_bounds__(256) void k_q4_records(int m, int n, int group, int
     if (in && zeros) z = zeros[row * groups + g];
     if (z > 15u) *bad = 1u;
     const float off = (float)(16u + z);
+    uint32_t scale = 0u;  // as fp32
+    if (in) {
+      scale = sizeof(S) == 4 ? __float_as_uint((float)scales[row * groups + g]) : (uint32_t)scales[row * groups + g] << 16;
+      const int64_t low = g * group, high = low + group < n ? low + group : n;
+      if ((scale & 0x7F800000u) != 0x7F800000u && q4_all_zero(codes + row * (((int64_t)n + 1) / 2), low, high, z)) scale = 0u;
+    }
     if (sizeof(S) == 4) {
-      out[2 * i] = in ? __float_as_uint((float)scales[row * groups + g]) : 0u;
+      out[2 * i] = scale;
       out[2 * i + 1] = __float_as_uint(off);
     } else {
-      out[i] = (in ? (uint32_t)scales[row * groups + g] << 16 : 0u) | __float_as_uint(off) >> 16;
+      out[i] = scale | __float_as_uint(off) >> 16;
     }
   }
 }
@@ -113,10 +128,10 @@ dbs_status q4_build(dbs_q4_matrix *A, const uint8_t *codes, const void *scales, 
   const int64_t most = 16384, g1 = tiles < most ? tiles : most, g2 = (nrec + 255) / 256 < most ? (nrec + 255) / 256 : most;
   hipLaunchKernelGGL(k_q4_codes, dim3((unsigned)g1), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt, codes, zeros, A->codes);
   if (A->scale_dtype == DBS_F32)
-    hipLaunchKernelGGL(k_q4_records<float>, dim3((unsigned)g2), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt,
+    hipLaunchKernelGGL(k_q4_records<float>, dim3((unsigned)g2), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt, codes,
                        (const float *)scales, zeros, A->recs, bad);
   else
-    hipLaunchKernelGGL(k_q4_records<bf16_bits>, dim3((unsigned)g2), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt,
+    hipLaunchKernelGGL(k_q4_records<bf16_bits>, dim3((unsigned)g2), dim3(256), 0, s, A->m, A->n, A->group, A->mt, A->kt, codes,
                        (const bf16_bits *)scales, zeros, A->recs, bad);
   if ((e = DBS_NOTE(hipGetLastError())) != hipSuccess) return map_err(e);
   uint32_t h = 0;

@@ -47,6 +47,60 @@ def test_every_fp32_kernel_keeps_the_low_parts_of_x(dbs, kind, gated, m, tokens,
         check_products(dbs, 1 + m + n + tokens, m, n, tokens, group, group != 64, scales, gated, wide(n, tokens, n), halvings=1)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,group,zeros,scales", [(48, 1000, 64, True, "bf16"), (70, 333, 32, True, "f32"), (40, 4100, 128, False, "bf16"),
+                                                    (33, 31, 32, True, "bf16"), (5000, 700, 64, True, "f32")])
+def test_weights_of_zero_add_nothing(dbs, kind, m, n, group, zeros, scales):
+    """Rows and groups whose codes all equal their zero point, next to others, under x of real values: those rows are 0, so are
+    ReLU gates of them, and the others' error has no part of such groups."""
+    import numpy as np
+    import torch
+
+    import decode_ref as ref
+
+    rng = np.random.default_rng(m + n)
+    w, u = ref.Q4(rng, m, n, group, zeros, scales, exact=False), ref.Q4(rng, m, n, group, zeros, scales, exact=False)
+    none = rng.random((m, w.s.shape[1])) < 0.5  # groups of weights 0
+    none[::3] = True                            # and whole rows
+    none[1::3, 0] = False
+    w.q = np.where(none[:, w.of], w.offset, w.q).astype(np.uint8)
+    assert (w.w[::3] == 0).all()
+    A, U = w.build(dbs), u.build(dbs)
+    for t in (1, 3, 7, 16, 37):
+        x = rng.standard_normal((t, n)).astype(np.float32)
+        x = ref.bf16(x) if kind == "bf16" else x
+        xs = torch.from_numpy(x).cuda()
+        xs = xs.bfloat16() if kind == "bf16" else xs
+        y = torch.full((t, m), 7.0, device="cuda")
+        dbs.dbs_q4_gated(A, U, xs, dbs.DBS_ACT_RELU, y)
+        assert (y[:, ::3] == 0).all()
+        dbs.dbs_q4_product(A, xs, y)
+        assert (y[:, ::3] == 0).all()
+        held = w.s
+        w.s = np.where(none, 0, held)  # the bound of the other groups alone
+        assert (np.abs(y.cpu().numpy() - x.astype(np.float64) @ w.w.T) <= w.bound(x)).all()
+        w.s = held
+
+
+def test_infinities_times_weights_of_zero(dbs):
+    """An infinite x or scale makes NaN of a weight 0, as in the formula; a scale of 0 otherwise changes nothing."""
+    import torch
+
+    m, n = 20, 200
+    zeros = torch.arange(m * 4, device="cuda").view(m, 4).remainder(16).to(torch.uint8)
+    codes = (zeros * 17).repeat_interleave(32, 1)[:, :100].contiguous()
+    scales = torch.ones(m, 4, device="cuda")
+    scales[3, 1], scales[4, 3] = float("inf"), float("nan")
+    A = dbs.dbs_q4_build(m, n, 64, codes, scales, zeros)
+    x = torch.ones(3, n, device="cuda")
+    x[1, 7], x[2, 150] = float("inf"), 3e38
+    y = torch.full((3, m), 7.0, device="cuda")
+    dbs.dbs_q4_product(A, x, y)
+    expect = torch.zeros(3, m, device="cuda")
+    expect[:, 3], expect[:, 4], expect[1] = torch.nan, torch.nan, torch.nan
+    assert torch.equal(y.nan_to_num(-5.0), expect.nan_to_num(-5.0))
+
+
 def test_row_groups_of_more_than_one_grid_row(dbs):
     """More row groups than eight grid rows of 65535 hold: the grid folds them."""
     import torch
