@@ -132,7 +132,8 @@ DBS_DEV bool is_finite(float v) { return (__float_as_uint(v) & 0x7F800000u) != 0
 
 DBS_DEV float act_apply(int act, float g) {
   if (act == DBS_ACT_SILU) return g / (1.0f + expf(-g));
-  if (act == DBS_ACT_GELU_TANH) return 0.5f * g * (1.0f + tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g)));
+  // (1 + tanh u) / 2 as 1 / (1 + exp(-2u)): next to -1 the tanh has no bits left of the difference
+  if (act == DBS_ACT_GELU_TANH) return g / (1.0f + expf(-1.5957691216057308f * (g + 0.044715f * g * g * g)));
   return g > 0.0f || g != g ? g : 0.0f;
 }
 

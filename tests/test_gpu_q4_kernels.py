@@ -101,6 +101,29 @@ def test_infinities_times_weights_of_zero(dbs):
     assert torch.equal(y.nan_to_num(-5.0), expect.nan_to_num(-5.0))
 
 
+@pytest.mark.parametrize("kind", [0, 1])
+def test_activations_keep_their_precision_for_negative_gates(dbs, kind):
+    """act(g) g for gates g = k / 64, exact in the products, against 64 bits, relative to the result itself."""
+    import numpy as np
+    import torch
+
+    import decode_ref as ref
+
+    g = np.arange(-20 * 64, 20 * 64 + 1) / 64
+    one = torch.ones(1, 1, device="cuda")
+    A = dbs.dbs_q4_build(1, 1, 32, torch.full((1, 1), 9, dtype=torch.uint8, device="cuda"), one)  # W = 9 - 8
+    y = torch.full((len(g), 1), 7.0, device="cuda")
+    dbs.dbs_q4_gated(A, A, torch.from_numpy(g).float().cuda()[:, None], kind, y)
+    u2 = 2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3) if kind == 1 else g
+    with np.errstate(over="ignore"):
+        expect = g / (1 + np.exp(-u2)) * g
+    # in half steps: the argument of exp 8 of itself (five for the cube, one for the sum, two for the factor; SiLU's is exact), exp 4,
+    # the sum 1, the quotient 5, the product 1.  Where exp overflows the result is below 20^2 / 2^128.
+    tol = ((8 * np.abs(u2) if kind == 1 else 0) + 11) * ref.U24 * np.abs(expect) + 400 * 2.0 ** -128
+    error = np.abs(y[:, 0].cpu().numpy().astype(np.float64) - expect)
+    assert (error <= tol).all(), (g[error > tol][:5], (error / tol).max())
+
+
 def test_row_groups_of_more_than_one_grid_row(dbs):
     """More row groups than eight grid rows of 65535 hold: the grid folds them."""
     import torch
