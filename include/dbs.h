@@ -511,7 +511,10 @@ typedef enum { DBS_ROPE_HALF = 0, DBS_ROPE_INTERLEAVED = 1 } dbs_rope_layout;
  *   inverse        nonzero: rotate by -p (undoes a rotation; the gradient with respect to x
  *                  is this rotation of the output's gradient)
  *   x, out         device, element (t, h, d) at t * token stride + h * head stride + d;
- *                  `out` may be `x` itself (same type and strides), else they share no element.
+ *                  `out` may be `x` itself (same type and strides), else they share no element;
+ *                  if one has elements between those of the other, as parts of one buffer, they
+ *                  have the same token or head stride in bytes, and where the other stride differs
+ *                  the rows along it, with what stands between them, are apart.
  *                  Strides of x are free; of out, one is at least head_dim and the other leaves
  *                  room for all that the first one spans (either order, either sign)
  */

@@ -184,8 +184,12 @@ extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, 
   if (!pos || (rot_dim > 0 && !freq) || !x || !out) return DBS_ERR_INVALID_ARG;
   // two heads of the output may not share an element, and an in-place call reads what it writes
   if (!apart(tokens, ot, heads, oh, head_dim) && !apart(heads, oh, tokens, ot, head_dim)) return DBS_ERR_INVALID_ARG;
-  if (x == out && (x_dtype != out_dtype || (tokens > 1 && xt != ot) || (heads > 1 && xh != oh)))
-    return DBS_ERR_INVALID_ARG;
+  const bool in_place = x == out && x_dtype == out_dtype && (tokens < 2 || xt == ot) && (heads < 2 || xh == oh);
+  const __int128 xs = dbs_vector_size(x_dtype), os = dbs_vector_size(out_dtype);
+  const dbs_rows from = {(__int128)(uintptr_t)x, tokens, xt * xs, heads, xh * xs, head_dim * xs};
+  const dbs_rows to = {(__int128)(uintptr_t)out, tokens, ot * os, heads, oh * os, head_dim * os};
+  // else workgroups would read what others write
+  if (!in_place && dbs_rows_meet(from, to)) return DBS_ERR_INVALID_ARG;
   const rope_args r = {tokens, heads, head_dim, rot_dim, layout == DBS_ROPE_INTERLEAVED, pos, freq, scale,
                        inverse ? -1.0f : 1.0f, x, xt, xh, out, ot, oh};
   const bool fx = x_dtype == DBS_F32, fy = out_dtype == DBS_F32;
