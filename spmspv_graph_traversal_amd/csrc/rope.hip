@@ -190,6 +190,10 @@ extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, 
   const dbs_rows to = {(__int128)(uintptr_t)out, tokens, ot * os, heads, oh * os, head_dim * os};
   // else workgroups would read what others write
   if (!in_place && dbs_rows_meet(from, to)) return DBS_ERR_INVALID_ARG;
+  const dbs_rows written = to.span();
+  if (dbs_overlap(pos, (int64_t)tokens * 4, (const void *)(uintptr_t)written.at, (int64_t)written.width) ||
+      dbs_overlap(freq, (int64_t)rot_dim * 4, (const void *)(uintptr_t)written.at, (int64_t)written.width))
+    return DBS_ERR_INVALID_ARG;
   const rope_args r = {tokens, heads, head_dim, rot_dim, layout == DBS_ROPE_INTERLEAVED, pos, freq, scale,
                        inverse ? -1.0f : 1.0f, x, xt, xh, out, ot, oh};
   const bool fx = x_dtype == DBS_F32, fy = out_dtype == DBS_F32;

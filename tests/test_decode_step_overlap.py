@@ -28,3 +28,11 @@ def rope(tokens=4, heads=3, dim=8, rot=8, x=P, xd=0, xt=24, xh=8, out=P, od=0, o
 ])
 def test_rope_refuses_overlapping_outputs(bad):
     assert rope(**bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(pos=P), dict(pos=P - 12), dict(pos=P + 4 * 95), dict(freq=P), dict(freq=P - 28), dict(freq=P + 4 * 94),
+    dict(ot=-24, pos=P - 4 * 72), dict(oh=-8, freq=P - 4 * 16), dict(ot=40, pos=P + 4 * 30),  # between its rows too
+])
+def test_rope_refuses_outputs_over_positions_and_frequencies(bad):
+    assert rope(**{"x": P + (1 << 20), **bad}) == INVALID
