@@ -202,6 +202,14 @@ extern "C" dbs_status dbs_logits_adjust(int32_t rows, int32_t vocab, const void 
                          ((rows - 1) * ld_out + vocab) * dbs_vector_size(out_dtype))) {
     return DBS_ERR_INVALID_ARG;
   }
+  // one workgroup of a row writes while others still read that row's lists
+  const int64_t written = ((int64_t)(rows - 1) * ld_out + vocab) * dbs_vector_size(out_dtype);
+  const auto meets = [&](const void *p, int64_t bytes) { return p && dbs_overlap(p, bytes, out, written); };
+  if (meets(q.hist_ptr, ((int64_t)rows + 1) * 4) || meets(q.hist, q.hist_len * 4) || meets(q.hist_new, (int64_t)rows * 4) ||
+      meets(q.repetition, (int64_t)rows * 4) || meets(q.frequency, (int64_t)rows * 4) || meets(q.presence, (int64_t)rows * 4) ||
+      meets(q.bias_ptr, ((int64_t)rows + 1) * 4) || meets(q.bias_idx, q.bias_len * 4) || meets(q.bias_val, q.bias_len * 4) ||
+      meets(q.mask, ((rows - 1) * q.ldmask + ((int64_t)vocab + 31) / 32) * 4))
+    return DBS_ERR_INVALID_ARG;
   const bool fx = in_dtype == DBS_F32, fy = out_dtype == DBS_F32;
   auto run = fx ? (fy ? launch_logits<float, float> : launch_logits<float, bf16_bits>)
                 : (fy ? launch_logits<bf16_bits, float> : launch_logits<bf16_bits, bf16_bits>);

@@ -36,3 +36,24 @@ def test_rope_refuses_overlapping_outputs(bad):
 ])
 def test_rope_refuses_outputs_over_positions_and_frequencies(bad):
     assert rope(**{"x": P + (1 << 20), **bad}) == INVALID
+
+
+def logits(rows=2, vocab=40, x=P, ldx=40, out=4 * P, ldo=40, **fields):
+    p = b.dbs_logits_params(**fields)
+    return _lib.dbs_logits_adjust(rows, vocab, x, 0, ldx, bytes(p), out, 0, ldo, None)
+
+
+HIST = dict(hist_ptr=P, hist=2 * P, hist_len=7)
+BIAS = dict(bias_ptr=P, bias_idx=2 * P, bias_val=3 * P, bias_len=7)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(HIST, hist_ptr=4 * P), dict(HIST, hist_ptr=4 * P - 8), dict(HIST, hist=4 * P + 316), dict(HIST, hist=4 * P - 24),
+    dict(HIST, hist_new=4 * P - 4), dict(HIST, repetition=4 * P + 316), dict(HIST, frequency=4 * P - 4), dict(HIST, presence=4 * P),
+    dict(BIAS, bias_ptr=4 * P + 316), dict(BIAS, bias_idx=4 * P - 24), dict(BIAS, bias_val=4 * P + 100),
+    dict(mask=4 * P - 12, ldmask=2), dict(mask=4 * P + 316, ldmask=2), dict(mask=4 * P - 100, ldmask=30),
+    dict(ldo=60, mask=4 * P + 200, ldmask=2),  # between the rows
+    dict(HIST, out=P), dict(BIAS, out=P, ldo=40),  # in place, over the pointers
+])
+def test_logits_refuse_outputs_over_their_lists(bad):
+    assert logits(**bad) == INVALID
