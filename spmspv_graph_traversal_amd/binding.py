@@ -3,7 +3,8 @@
 Argument marshalling only (that of the decode-step calls in C++, ``csrc/calls.cpp``): every step of the
 computation runs in the HIP library.  Tensors are torch tensors on the current GPU (torch provides the
 device memory and the stream); the functions carry the C names.  Importing
-this module without the built library raises ``ImportError`` — there is no
+this module without the built library raises ``ImportError``, as does a decode-step call without
+the built ``_calls.so`` (the sparse products do without it) — there is no
 fallback.
 """
 from __future__ import annotations
@@ -347,13 +348,24 @@ def dbs_free(A: Matrix) -> None:
 _VECTOR = {_torch.float32: DBS_F32, _torch.bfloat16: DBS_BF16}
 
 
+class _NoCalls:
+    """In place of ``_calls.so``: a decode-step call says why it cannot run."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(self._why)
+
+
 def _load_calls():
     path = os.path.join(_HERE, "_calls.so")
     if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build the HIP library first "
-                          "(python -c 'import __graft_entry__ as g; g.build()')")
-    from . import _calls
-
+        return _NoCalls(f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+    try:
+        from . import _calls
+    except ImportError as e:  # built for another torch or interpreter
+        return _NoCalls(f"{path} does not load, build it again: {e}")
     _calls.bind(*(C.cast(getattr(_lib, f), C.c_void_p).value for f in (
         "dbs_q4_product", "dbs_q4_product_masked", "dbs_q4_gated", "dbs_logits_adjust", "dbs_rope")))
     return _calls

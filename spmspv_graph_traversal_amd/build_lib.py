@@ -74,13 +74,13 @@ def build(verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
         calls = ex.submit(_compile_calls)
         objs = list(ex.map(_compile, SOURCES))
-        calls.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-mcode-object-version=5", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    calls.result()  # after the library, which works without it but for the decode-step calls
     if verbose:
         print(f"built {LIB} and {CALLS}")
     return LIB

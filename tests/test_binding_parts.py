@@ -1,0 +1,39 @@
+"""The binding without its compiled part (CPU only)."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PACKAGE = os.path.join(ROOT, "spmspv_graph_traversal_amd")
+
+CODE = """
+import torch
+import spmspv_graph_traversal_amd as dbs
+assert dbs.dbs_build and dbs.dbs_spmspv and dbs.dbs_bfs and dbs.binding._lib.dbs_q4_product
+freq, scale = dbs.dbs_rope_frequencies(8)
+x = torch.zeros(1, 1, 8)
+for call in (lambda: dbs.dbs_rope(x, x, freq, x), lambda: dbs.dbs_logits_adjust(x, x)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_calls.so" in str(e)
+    else:
+        raise AssertionError
+"""
+
+
+@pytest.mark.parametrize("broken", [False, True])
+def test_sparse_products_need_no_compiled_binding(tmp_path, broken):
+    """Where only the HIP library was built, or the compiled part for another interpreter, the package loads, and the decode-step
+    calls say what is missing."""
+    package = tmp_path / "spmspv_graph_traversal_amd"
+    package.mkdir()
+    for name in ("__init__.py", "binding.py", "build_lib.py", "libdbs.so"):
+        os.symlink(os.path.join(PACKAGE, name), package / name)
+    if broken:
+        (package / "_calls.so").write_bytes(b"not a library")
+    r = subprocess.run([sys.executable, "-c", CODE], cwd=tmp_path, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": str(tmp_path), "PYTHONDONTWRITEBYTECODE": "1"})
+    assert r.returncode == 0, r.stderr
