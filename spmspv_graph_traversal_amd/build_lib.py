@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shutil
 import subprocess
 import sys
 
@@ -49,18 +50,27 @@ def _compile(src: str) -> str:
     return obj
 
 
+def rocm_include() -> str:
+    """Where HIP's headers are: beside the compiler, which may be named without its folder, or where ROCM_PATH or the usual
+    place has them."""
+    found = shutil.which(HIPCC)
+    for rocm in (os.path.dirname(os.path.dirname(os.path.abspath(found))) if found else None, os.environ.get("ROCM_PATH"), "/opt/rocm"):
+        if rocm and os.path.exists(os.path.join(rocm, "include", "hip", "hip_runtime.h")):
+            return os.path.join(rocm, "include")
+    raise RuntimeError(f"HIP's headers were not found beside {HIPCC}, in ROCM_PATH or in /opt/rocm")
+
+
 def _compile_calls() -> None:
     import sysconfig
 
     import torch
 
     at = os.path.dirname(torch.__file__)
-    rocm = os.path.dirname(os.path.dirname(HIPCC))
     tmp = CALLS + ".tmp"
     # the macros tell torch's headers which device backend it was built with
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
            "-I" + os.path.join(at, "include"), "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"),
-           "-I" + os.path.join(rocm, "include"), "-I" + sysconfig.get_paths()["include"],
+           "-I" + rocm_include(), "-I" + sysconfig.get_paths()["include"],
            os.path.join(CSRC, "calls.cpp"), "-o", tmp, "-L" + os.path.join(at, "lib"),
            "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)

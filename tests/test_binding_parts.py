@@ -37,3 +37,21 @@ def test_sparse_products_need_no_compiled_binding(tmp_path, broken):
     r = subprocess.run([sys.executable, "-c", CODE], cwd=tmp_path, capture_output=True, text=True, timeout=300,
                        env={**os.environ, "PYTHONPATH": str(tmp_path), "PYTHONDONTWRITEBYTECODE": "1"})
     assert r.returncode == 0, r.stderr
+
+
+def test_the_compiler_may_be_named_without_its_folder(tmp_path, monkeypatch):
+    from spmspv_graph_traversal_amd import build_lib
+
+    (tmp_path / "bin").mkdir()
+    (tmp_path / "include" / "hip").mkdir(parents=True)
+    (tmp_path / "include" / "hip" / "hip_runtime.h").write_text("")
+    (tmp_path / "bin" / "hipcc").write_text("#!/bin/sh\n")
+    (tmp_path / "bin" / "hipcc").chmod(0o755)
+    monkeypatch.setattr(build_lib, "HIPCC", str(tmp_path / "bin" / "hipcc"))
+    assert build_lib.rocm_include() == str(tmp_path / "include")
+    monkeypatch.setattr(build_lib, "HIPCC", "hipcc")
+    monkeypatch.setenv("PATH", str(tmp_path / "bin"))
+    assert build_lib.rocm_include() == str(tmp_path / "include")
+    monkeypatch.setenv("PATH", "")  # a wrapper elsewhere
+    monkeypatch.setenv("ROCM_PATH", str(tmp_path))
+    assert build_lib.rocm_include() == str(tmp_path / "include")
