@@ -416,9 +416,11 @@ dbs_status dbs_q4_product(dbs_q4_handle A, int32_t tokens, const void *x, dbs_dt
 /*
  * dbs_q4_product_masked — the same where token t wants only the rows i whose
  * bit i % 32 of row_mask[t][i / 32] is set (a grammar's allowed tokens at the
- * head): y_ti = fill elsewhere, whatever x holds.  16-row blocks that no
- * token of a block of tokens wants are not read.  Bits at m and above are
- * ignored.
+ * head): y_ti = fill elsewhere, whatever x holds.  A workgroup's rows are not
+ * read if none of its tokens wants any of them: 16 rows for up to four
+ * tokens; for more, up to 32 tokens and 16, 32, 64 or 128 rows, the more the
+ * larger the call, so that a few wanted rows of a large matrix may have as
+ * many read for each.  Bits at m and above are ignored.
  *
  *   row_mask   device uint32[tokens][ceil(m/32)], row stride ldmask words
  *   fill       any float, -INFINITY for logits
