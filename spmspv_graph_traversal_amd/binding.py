@@ -207,6 +207,10 @@ class Matrix:
         self.handle = handle
         self.m, self.n, self.dtype = m, n, dtype
 
+    @property
+    def q4_handle(self):
+        raise TypeError("a 4-bit matrix (dbs_q4_build) is expected, not a sparse one")
+
     def __del__(self):
         try:
             dbs_free(self)
@@ -377,9 +381,13 @@ _calls = _load_calls()
 class Q4Matrix:
     """Owner of a dbs_q4_handle; freed with the object or by dbs_q4_free."""
 
-    def __init__(self, handle: C.c_void_p, m: int, n: int, group: int):
-        self.handle = handle
+    def __init__(self, q4_handle: C.c_void_p, m: int, n: int, group: int):
+        self.q4_handle = q4_handle
         self.m, self.n, self.group = m, n, group
+
+    @property
+    def handle(self):
+        raise TypeError("a sparse matrix (dbs_build) is expected, not a 4-bit one")
 
     def __del__(self):
         try:
@@ -413,19 +421,19 @@ def dbs_q4_build(m, n, group, codes, scales, zeros=None, stream=None) -> Q4Matri
 
 def dbs_q4_bytes(A: Q4Matrix) -> int:
     v = C.c_int64()
-    _check(_lib.dbs_q4_bytes(A.handle, C.byref(v)), "dbs_q4_bytes")
+    _check(_lib.dbs_q4_bytes(A.q4_handle, C.byref(v)), "dbs_q4_bytes")
     return int(v.value)
 
 
 def dbs_q4_free(A: Q4Matrix) -> None:
-    if A.handle is not None and A.handle.value:
-        _check(_lib.dbs_q4_free(A.handle), "dbs_q4_free")
-        A.handle = C.c_void_p()
+    if A.q4_handle is not None and A.q4_handle.value:
+        _check(_lib.dbs_q4_free(A.q4_handle), "dbs_q4_free")
+        A.q4_handle = C.c_void_p()
 
 
 def dbs_q4_product(A: Q4Matrix, x, y, stream=None) -> None:
     """y[t] = W x[t]; x [n] or [tokens, n], y [m] or [tokens, m], each float32 or bfloat16."""
-    st = _calls.q4_product(A.handle.value, A.m, A.n, x, y, stream)
+    st = _calls.q4_product(A.q4_handle.value, A.m, A.n, x, y, stream)
     if st:
         raise DBSError(st, "dbs_q4_product")
 
@@ -433,14 +441,14 @@ def dbs_q4_product(A: Q4Matrix, x, y, stream=None) -> None:
 def dbs_q4_product_masked(A: Q4Matrix, x, row_mask, y, fill: float = float("-inf"), stream=None) -> None:
     """dbs_q4_product for the rows whose bit is set in row_mask (int32 words [tokens, ceil(m/32)]), `fill`
     elsewhere."""
-    st = _calls.q4_product_masked(A.handle.value, A.m, A.n, x, row_mask, fill, y, stream)
+    st = _calls.q4_product_masked(A.q4_handle.value, A.m, A.n, x, row_mask, fill, y, stream)
     if st:
         raise DBSError(st, "dbs_q4_product_masked")
 
 
 def dbs_q4_gated(G: Q4Matrix, U: Q4Matrix, x, activation: int, y, stream=None) -> None:
     """y[t] = act(G x[t]) * (U x[t]) for two matrices of one shape, group and scale type."""
-    st = _calls.q4_gated(G.handle.value, U.handle.value, G.m, G.n, x, activation, y, stream)
+    st = _calls.q4_gated(G.q4_handle.value, U.q4_handle.value, G.m, G.n, x, activation, y, stream)
     if st:
         raise DBSError(st, "dbs_q4_gated")
 

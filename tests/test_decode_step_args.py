@@ -161,3 +161,15 @@ def test_cpu_tensors_are_refused():
         b.dbs_q4_build(2, 4, 32, torch.zeros(2, 2, dtype=torch.uint8), torch.ones(2, 1))
     with pytest.raises(ValueError):
         b.dbs_q4_build(2, 4, 48, torch.zeros(2, 2, dtype=torch.uint8), torch.ones(2, 1))
+
+
+def test_matrices_of_the_other_kind_are_refused():
+    """A sparse matrix's handle is never read as a 4-bit one's, nor freed as one, and the other way round."""
+    q4, sparse = b.Q4Matrix(C.c_void_p(), 4, 4, 32), b.Matrix(C.c_void_p(), 4, 4, b.DBS_F32)
+    for call in (lambda: b.dbs_free(q4), lambda: b.dbs_get_stats(q4), lambda: b.dbs_set_option(q4, b.DBS_OPT_PATH, 0),
+                 lambda: b.dbs_copy_array(q4, b.DBS_ARR_RB_PTR), lambda: b.dbs_q4_free(sparse), lambda: b.dbs_q4_bytes(sparse),
+                 lambda: b.dbs_q4_product(sparse, None, None), lambda: b.dbs_q4_product_masked(sparse, None, None, None),
+                 lambda: b.dbs_q4_gated(q4, sparse, None, 0, None), lambda: b.dbs_q4_gated(sparse, q4, None, 0, None)):
+        with pytest.raises(TypeError, match="matrix"):
+            call()
+    assert b.dbs_q4_free(q4) is None and b.dbs_free(sparse) is None
