@@ -413,6 +413,8 @@ def dbs_q4_build(m, n, group, codes, scales, zeros=None, stream=None) -> Q4Matri
     for t, name in ((codes, "codes"), (scales, "scales"), (zeros, "zeros")):
         if t is not None and t.get_device() != _torch.cuda.current_device():
             raise ValueError(f"{name} is not on the current device")
+    if getattr(stream, "device_index", codes.get_device()) != codes.get_device():
+        raise ValueError(f"the stream is on device {stream.device_index}, the call runs on the current device, {codes.get_device()}")
     h = C.c_void_p()
     _check(_lib.dbs_q4_build(m, n, group, _ptr(codes), _ptr(scales), _VECTOR[scales.dtype], _ptr(zeros),
                              _stream(stream, codes.device), C.byref(h)), "dbs_q4_build")

@@ -124,6 +124,26 @@ def test_activations_keep_their_precision_for_negative_gates(dbs, kind):
     assert (error <= tol).all(), (g[error > tol][:5], (error / tol).max())
 
 
+def test_builds_on_a_stream(dbs):
+    """A stream of the current device is used, one of another device refused."""
+    import torch
+
+    from q4_device import Q4, small
+
+    class Stream:
+        cuda_stream = 0
+        device_index = torch.cuda.current_device() + 1
+
+    w = Q4(3, 40, 100, 32, True, "f32")
+    with pytest.raises(ValueError, match="stream"):
+        dbs.dbs_q4_build(40, 100, 32, w.codes, w.scales, w.zeros, stream=Stream())
+    x, y = small(1, 3, 100, "f32"), torch.full((3, 40), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    A = dbs.dbs_q4_build(40, 100, 32, w.codes, w.scales, w.zeros, stream=torch.cuda.Stream())
+    dbs.dbs_q4_product(A, x, y)
+    assert torch.equal(y.double(), x.double() @ w.w.t())
+
+
 def test_row_groups_of_more_than_one_grid_row(dbs):
     """More row groups than eight grid rows of 65535 hold: the grid folds them."""
     import torch
