@@ -533,9 +533,10 @@ typedef enum {
   DBS_ROPE_BANDS = 3,   /* by the turns t = context * f / (2 pi) that pair i makes over the model's own
                            context: t < low: f / factor; t > high: f; between them f ((1 - w) / factor + w),
                            w = (t - low) / (high - low) */
-  DBS_ROPE_RAMP = 4     /* by pair index: f up to pair floor(d(high)), f / factor from pair ceil(d(low)),
-                           a linear ramp between, d(t) = rot_dim ln(context / (2 pi t)) / (2 ln base);
-                           *scale = 0.1 ln(factor) + 1 */
+  DBS_ROPE_RAMP = 4     /* by pair index: f up to pair `first`, f / factor from pair `last`, a linear ramp
+                           between, first = max(floor(d(high)), 0), last = min(ceil(d(low)), rot_dim - 1),
+                           d(t) = rot_dim ln(context / (2 pi t)) / (2 ln base); if last <= first,
+                           f / factor behind pair `first`; *scale = 0.1 ln(factor) + 1 */
 } dbs_rope_scaling;
 
 typedef struct {

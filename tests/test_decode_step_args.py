@@ -173,3 +173,26 @@ def test_matrices_of_the_other_kind_are_refused():
         with pytest.raises(TypeError, match="matrix"):
             call()
     assert b.dbs_q4_free(q4) is None and b.dbs_free(sparse) is None
+
+
+@pytest.mark.parametrize("context,low,high,first,last", [
+    (100, 1.0, 32.0, 0, 20),       # pair 0 turns fewer than `high` times: the ramp starts there
+    (4, 1.0, 32.0, 0, None),       # fewer than `low` times even: f / factor behind pair 0
+    (10 ** 15, 1.0, 32.0, None, None),  # every pair turns more than `high` times: f
+    (10 ** 9, 1.0, 10.0 ** 8, 3, 127),  # the ramp's end is kept at the last element
+])
+def test_ramp_at_the_ends(context, low, high, first, last):
+    plain = 10000.0 ** (-np.arange(64) / 64)
+    at = lambda t: 128 * math.log(context / (2 * math.pi * t)) / (2 * math.log(10000.0))
+    f, _ = b.dbs_rope_frequencies(128, scaling=b.DBS_ROPE_RAMP, factor=8, low=low, high=high, context=context)
+    i = np.arange(64)
+    if first is None:
+        assert math.floor(at(high)) > 127
+        w = np.zeros(64)
+    elif last is None:
+        assert math.ceil(at(low)) <= first
+        w = (i > first).astype(float)
+    else:
+        assert max(math.floor(at(high)), 0) == first and min(math.ceil(at(low)), 127) == last
+        w = np.clip((i - first) / (last - first), 0, 1)
+    np.testing.assert_allclose(f.numpy(), plain * (w / 8 + 1 - w), rtol=1e-13)
