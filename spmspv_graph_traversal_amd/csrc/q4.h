@@ -22,14 +22,16 @@
 __host__ __device__ inline int q4_record_words(dbs_dtype scale_dtype) { return scale_dtype == DBS_F32 ? 2 : 1; }
 
 // Byte offsets in a row of tiles that a lane's 16 bytes of codes and its row's records start at: column block k, if it comes
-// before `end`, else one that is out of range of the row's descriptor, as are the 255 bytes behind it, which no 32-bit sum
-// brings back to 0 (records of eight words take two loads).
-#define Q4_NO_BLOCK 0xFFFFFF00u
+// before `end`, else one from which every load of 16 bytes is out of range of the row's descriptor, with no 32-bit sum that
+// wraps: the last 16 bytes of the range, or, for records of eight words, which take two loads, some before.  (0xFFFFFFF0 fits
+// in an instruction, another value takes a register: one more than the 80 that leave room for six waves in the kernel of one
+// token and many rows.)
+__host__ __device__ inline uint32_t q4_no_block(int words) { return words > 4 ? 0xFFFFFF00u : 0xFFFFFFF0u; }
 __host__ __device__ inline uint32_t q4_code_offset(int k, int end, int lane) {
-  return k < end ? (uint32_t)k * Q4_TILE_BYTES + lane * 16 : Q4_NO_BLOCK;
+  return k < end ? (uint32_t)k * Q4_TILE_BYTES + lane * 16 : q4_no_block(4);
 }
 __host__ __device__ inline uint32_t q4_record_offset(int k, int end, int row, int words) {
-  return k < end ? ((uint32_t)k * Q4_ROWS + row) * (words * 4) : Q4_NO_BLOCK;
+  return k < end ? ((uint32_t)k * Q4_ROWS + row) * (words * 4) : q4_no_block(words);
 }
 
 __host__ __device__ inline int q4_code_bit(int e) { return (4 * (e / 2 + 4 * (e & 1)) + 3) & 31; }
