@@ -78,10 +78,9 @@ inline bool dbs_rows_meet(dbs_rows a, dbs_rows b) {
   if (a.ni < 2) a.si = b.si = 0;
   if (a.nj < 2) a.sj = b.sj = 0;
   if (!dbs_like_rows_meet(a.span(), b.span())) return false;
-  if (a.si == b.si && a.sj == b.sj) return dbs_like_rows_meet(a, b);
-  if (a.si == b.si) return dbs_like_rows_meet(a.joined(), b.joined());
-  if (a.sj == b.sj) return dbs_like_rows_meet(a.turned().joined(), b.turned().joined());
-  return true;
+  if (a.si == b.si && !dbs_like_rows_meet(a.joined(), b.joined())) return false;
+  if (a.sj == b.sj && !dbs_like_rows_meet(a.turned().joined(), b.turned().joined())) return false;
+  return a.si != b.si || a.sj != b.sj || dbs_like_rows_meet(a, b);  // the last, exact, takes longest: in steps over i or j
 }
 
 // a barrier that waits for LDS only, not for loads from memory in flight
