@@ -395,7 +395,10 @@ dbs_status dbs_q4_free(dbs_q4_handle A);
  *   y        device [tokens][m], row stride ldy >= m elements
  *
  * Infinities and NaN in x or the scales spread as in the formula, to the
- * tokens and rows whose sums hold them.
+ * tokens and rows whose sums hold them.  Results that are not finite are
+ * computed a second time, weight by weight, which takes far longer (28672 x
+ * 8192, 64 tokens of bf16: 56 us, 0.96 ms with a NaN in one token, 15 ms with
+ * one in each): what pads a batch is better finite, or fewer tokens.
  *
  * A group's part of y is scale (sum (16 + code) x - (16 + zero) sum x), each
  * sum rounded for itself: before its rounding to y's type, y_ti is off by at

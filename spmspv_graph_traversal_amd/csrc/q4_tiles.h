@@ -265,13 +265,17 @@ DBS_DEV void finish(const q4_args &q, const float *part, int parts, int stride, 
  * what loses bits, and the first part's products have few bits.  A result that is not finite is computed again
  * weight by weight.
  *
- * What bounds it (times of a graph of launches, 1.95 us of each being the launch; a copy reaches 4.9 TB/s here).
- *   One token, memory and the length of a wave's chain: 4096 x 4096 4.1 us, 11008 x 4096 7.0 us (23.3 MB, 3.3 TB/s; without
- *   the launch 4.6), two of these gated 11.3 us (4.1 TB/s).
+ * What bounds it (times of a graph of launches, 1.95 us of each being the launch; a copy reaches 4.9 TB/s here, reads 5.5).
+ *   One token, memory and the length of a wave's chain: 4096 x 4096 4.0 us from the Infinity Cache, 5.0 where every call reads
+ *   other codes, 11008 x 4096 6.5 (23.3 MB), two of these gated 11.2, other codes every time 13.9 (46.6 MB, 3.9 TB/s without the
+ *   launch).
  *   Many tokens, instruction issue: a vector instruction takes four cycles of a SIMD, the unpacking of an operand (seven of
- *   them) as long as the products of two token tiles, and the two kinds hardly overlap.  11008 x 4096, 64 tokens, 18.7 us,
- *   of which vector instructions issue for 7.1 and the matrix cores run for 3.4; 28672 x 8192 58 us, 520 TFLOP/s.
- *   fp32 x, 5461 x 2001 gated, 24 tokens, 14.2 us: three products and the cutting of x in place of one.
+ *   them) as long as the products of two token tiles, and the two kinds hardly overlap.  11008 x 4096, 64 tokens, 17.8 us (other
+ *   codes 19.3), of which vector instructions issue for 7.1, the codes being unpacked again for every 16 tokens, and the matrix
+ *   cores run for 3.4, a third of it for the products with ones, which each wave makes for itself; the rest is the launch, and
+ *   three rounds of workgroups for the work of 2.7.  28672 x 8192 58 us, 520 TFLOP/s.
+ *   fp32 x, 5461 x 2001 gated, 24 tokens, 13.6 us: three products and the cutting of x in place of one, half the time; 172
+ *   workgroups leave a third of the compute units idle.
  *
  * Split: `splits` waves share the rows of a row wave and take every splits-th block of 128 columns; their sums meet in LDS
  * in a fixed order.  Nothing is atomic, so results do not depend on timing.
@@ -280,7 +284,7 @@ DBS_DEV void finish(const q4_args &q, const float *part, int parts, int stride, 
  * rotated by the row (exclusive or) so that neither side meets bank conflicts.  FEW: the parts of an fp32 x are rows of one
  * operand, token t's in rows 4t .. 4t + 2.
  *
- * Loads come back in order, and x (from L2) must not queue behind codes (from HBM) of a later block.  So two blocks are in
+ * Loads come back in order, and x (from L2) must not queue behind codes (from memory) of a later block.  So two blocks are in
  * flight: when block b is used up, its registers take x and codes of block b + 2, in this order.  Blocks past a wave's last
  * are out of range of the codes' buffer descriptor and read nothing.  Streaming loads of the codes (past the caches) were
  * slower: gated 12.1 us against 11.1.
