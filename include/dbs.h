@@ -406,6 +406,7 @@ dbs_status dbs_q4_free(dbs_q4_handle A);
  *
  *   (387 + groups of a row) 2^-24 sum_j |scale x_j| (32 + code + zero)
  *
+ * (and, for fp32 x, by what its bits below 2^-133 stand for, which are left out),
  * which is relative to these magnitudes, not to |W_ij x_j| (on ordinary data
  * a few 2^-24 of them, since roundings go either way).  A group of a row whose
  * codes all equal its zero point adds nothing: a row of such groups (pruned

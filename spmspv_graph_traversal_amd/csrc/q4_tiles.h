@@ -49,7 +49,7 @@ DBS_DEV bf16x8 codes_operand(uint32_t w, const code_masks &m) {
 // x on its way to the operands.  A lane takes 16 bytes of a token's row, so that adjacent lanes read adjacent bytes
 // (one operand's lanes are 16 tokens: read directly, each would be a memory request of its own, 64 cycles a load
 // instead of 16), and puts them into LDS as bf16: bf16 as it is, fp32 cut into three bf16 parts of eight mantissa bits,
-// which sum to it exactly.
+// which sum to it exactly (bits below 2^-133, the least that bf16 holds, are left out).
 template <class X>
 struct x_piece;
 template <>
