@@ -555,6 +555,146 @@ typedef struct {
 /* Fills freq[rot_dim/2] (HOST memory) and *scale (may be NULL; 1 but for RAMP).  Touches no device. */
 dbs_status dbs_rope_frequencies(const dbs_rope_options *opt, double *freq, float *scale);
 
+/* one part of dbs_norm_rope: the query or the key heads of the tokens, as dbs_rope's x and out */
+typedef struct {
+  const void *x;
+  int64_t x_token_stride, x_head_stride;
+  void *out;
+  int64_t out_token_stride, out_head_stride;
+  int32_t heads;        /* >= 0 */
+  const void *weight;   /* device [head_dim], or NULL: ones */
+} dbs_norm_part;
+
+/*
+ * dbs_norm_rope — the root mean square norm of each head, then its rotary
+ * positions, in one pass over one or two parts (queries and keys):
+ *
+ *   y = w * x / sqrt(mean(x^2) + eps),  then y as dbs_rope's x
+ *
+ * in fp32 with one rounding to the output's type; the mean is over the
+ * head's head_dim elements.  A weight that is held as its distance from 1 is
+ * given as 1 + w.  head_dim <= DBS_ROPE_MAX_DIM, eps >= 0 and finite; a
+ * negative position leaves the token's rows as they are.  A part's out may
+ * be its x itself; otherwise, and between the parts, outputs share nothing
+ * with inputs or each other: parts of one buffer, as the queries and keys
+ * of a fused projection's rows, have the same token stride, and what a token
+ * of one spans from its first head to its last lies apart from the other's.
+ */
+dbs_status dbs_norm_rope(int32_t tokens, int32_t head_dim, int32_t rot_dim, dbs_rope_layout layout,
+                         const int32_t *pos, const double *freq, float scale, float eps,
+                         const dbs_norm_part *parts, int32_t count, dbs_dtype x_dtype, dbs_dtype out_dtype,
+                         dbs_dtype weight_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A paged cache of keys and values in 4 bits, and the attention over it.
+ *
+ * A group (32, 64 or 128 channels of a head of a token; the last one may be
+ * cut) is held as codes q, a scale s and an offset b, and stands for
+ *
+ *   x = half(s q + b),  b = half(min), s = half((max - b) (1/15)),
+ *                       q = rint((x - b) (1/s)) within 0 .. 15,  0 where s = 0
+ *
+ * each step in fp32, so that the bytes depend on nothing but x.  Values
+ * above DBS_KV4_MAX_VALUE in size, infinities and NaN make their group NaN.
+ *
+ * The pool is the caller's: `pages` pages of page_tokens tokens each, all
+ * key heads of them, dbs_kv4_page_bytes bytes (one layer's; the layers of a
+ * model are several pools, or one with the layers' pages side by side).
+ * Page p of sequence b is table[b][p]; nobody reads the entries of pages that no
+ * new token sees, so the pages that a window has left may be freed and their
+ * entries hold anything.  An entry outside [0, pages) stands for no page: what a call would
+ * store there is dropped, and its tokens are seen by nobody.
+ *
+ * The new tokens of a call are the last ones of their sequences: row
+ * new_ptr[b] + i of the call is token lens[b] - n + i of sequence b, i < n =
+ * new_ptr[b+1] - new_ptr[b]; without new_ptr, n = tokens / sequences for all.
+ * lens counts the new tokens.  A length is taken as at most what the table
+ * has room for.  Tokens before the first (lens[b] < n) are stored nowhere and see nothing.
+ *
+ * Layout of a page, for each key head in turn (d = head_dim rounded up to
+ * 64, 96, 128, 192 or 256, whose last channels have codes 0; a word has eight
+ * nibbles e, the lowest first):
+ *   key codes      uint32[page_tokens][4 g][d/32 k]     nibble e: channel 32 k + 8 g + e
+ *   key records    half[page_tokens][d/group][2]        s, b
+ *   value codes    uint32[page_tokens/8][16 c][d/16 n]  nibble e: channel 16 n + c of token 8 t + e
+ *   value records  half[page_tokens/8][d/group][2][8]   s, b; of tokens 0 4 1 5 2 6 3 7
+ * ------------------------------------------------------------------------ */
+#define DBS_KV4_MAX_VALUE 65024.0f
+#define DBS_KV4_MAX_DIM 256
+/* tokens that a row of the table has room for, sequences, and tokens * heads of a call at most */
+#define DBS_KV4_MAX_CONTEXT 1073741824
+#define DBS_KV4_MAX_SEQUENCES 1048576
+#define DBS_KV4_MAX_ROWS 16777216
+
+typedef struct {
+  void *pool;              /* device, 16-byte aligned */
+  int64_t page_stride;     /* bytes from page to page, a multiple of 16, >= dbs_kv4_page_bytes */
+  int32_t pages;
+  int32_t page_tokens;     /* 16, 32, 64, 128 or 256 */
+  int32_t key_heads;
+  int32_t head_dim;        /* 8 to DBS_KV4_MAX_DIM, a multiple of 8 */
+  int32_t group;           /* 32, 64 or 128, a divisor of d */
+  int32_t sequences;
+  int32_t table_pages;     /* entries of a row of the table */
+  const int32_t *table;    /* device int32[sequences][table_pages], row stride ldtable */
+  int64_t ldtable;
+  const int32_t *lens;     /* device int32[sequences] */
+  const int32_t *new_ptr;  /* device int32[sequences+1], not decreasing; NULL: as many new tokens each */
+} dbs_kv4_cache;
+
+/* Bytes of a page of one layer.  Touches no device. */
+dbs_status dbs_kv4_page_bytes(int32_t key_heads, int32_t head_dim, int32_t group, int32_t page_tokens,
+                              int64_t *bytes);
+
+/*
+ * dbs_kv4_store — keys and values of the new tokens into their pages, which
+ * must be there.  k and v are [tokens][key_heads][head_dim] with free token
+ * and head strides.  k_out and v_out, if not NULL, receive what the cache
+ * now stands for, rounded to their type (also for what is stored nowhere), so
+ * that a prompt's attention can be computed elsewhere from what later steps
+ * will read; they may be k and v themselves (same type and strides), else they share no element with them.
+ * No page that is written may belong to two sequences of the call.
+ */
+dbs_status dbs_kv4_store(const dbs_kv4_cache *cache, int32_t tokens, const void *k, int64_t k_token_stride,
+                         int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                         dbs_dtype x_dtype, void *k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+                         void *v_out, int64_t v_out_token_stride, int64_t v_out_head_stride,
+                         dbs_dtype out_dtype, void *stream);
+
+/*
+ * dbs_kv4_attention — softmax attention of the new tokens, stored before, over
+ * their sequences:
+ *
+ *   out_ih = sum_j p_ihj v_j,  p_ih. = softmax over the tokens j that i sees of scale q_ih k_j
+ *
+ * where query head h reads key head h / (heads / key_heads) and the token at position i
+ * sees j <= i and, if window > 0, of these j > i - window and j < sinks (a few
+ * first tokens that stay visible).  A row that sees nothing is 0, rows of no sequence
+ * (new_ptr[sequences] and behind) are left as they are.  What a row does not
+ * see takes no part in it, whatever it holds.
+ *
+ *   heads      a multiple of key_heads, tokens * heads <= DBS_KV4_MAX_ROWS
+ *   q, out     device [tokens][heads][head_dim], free token and head strides, apart
+ *   scale      > 0 and finite, usually 1/sqrt(head_dim)
+ *   max_len    the host's bound of lens, or 0: the table's room.  It only tells how the work is cut:
+ *              longer sequences are right, and slower
+ *   workspace  device, 16-byte aligned, of dbs_kv4_attention_workspace bytes for these arguments; with
+ *              fewer (NULL and 0 among them) the work is not cut along the tokens, which is slower for long ones and few
+ *              rows.  Calls that may overlap in time need workspaces of their own.
+ *
+ * Keys and values enter the matrix cores as the halves that the cache stands for, q as a half
+ * with its row's largest element below 2^15 and exponentials as halves, of which both are in
+ * two parts where q or out is fp32.  Sums, maxima and the output are held in fp32.
+ */
+dbs_status dbs_kv4_attention_workspace(const dbs_kv4_cache *cache, int32_t tokens, int32_t heads,
+                                       dbs_dtype q_dtype, dbs_dtype out_dtype, int32_t window, int32_t sinks,
+                                       int32_t max_len, int64_t *bytes);
+dbs_status dbs_kv4_attention(const dbs_kv4_cache *cache, int32_t tokens, int32_t heads, const void *q,
+                             dbs_dtype q_dtype, int64_t q_token_stride, int64_t q_head_stride, void *out,
+                             dbs_dtype out_dtype, int64_t out_token_stride, int64_t out_head_stride, float scale,
+                             int32_t window, int32_t sinks, int32_t max_len, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

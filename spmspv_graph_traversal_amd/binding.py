@@ -35,6 +35,8 @@ DBS_ROPE_HALF, DBS_ROPE_INTERLEAVED = 0, 1
 DBS_ROPE_PLAIN, DBS_ROPE_LINEAR, DBS_ROPE_BASE, DBS_ROPE_BANDS, DBS_ROPE_RAMP = 0, 1, 2, 3, 4
 DBS_Q4_MAX_TOKENS, DBS_Q4_MAX_ROWS, DBS_Q4_MAX_COLUMNS = 524288, 2147483520, 1 << 28
 DBS_LOGITS_MAX_ROWS, DBS_ROPE_MAX_DIM, DBS_ROPE_MAX_ELEMENTS = 65535, 1024, 1 << 30
+DBS_KV4_MAX_VALUE, DBS_KV4_MAX_DIM, DBS_KV4_MAX_CONTEXT = 65024.0, 256, 1 << 30
+DBS_KV4_MAX_SEQUENCES, DBS_KV4_MAX_ROWS = 1 << 20, 1 << 24
 # exported arrays
 (DBS_ARR_RB_PTR, DBS_ARR_T_CB, DBS_ARR_T_META, DBS_ARR_CB_PTR, DBS_ARR_CSC_RB, DBS_ARR_CSC2CSR,
  DBS_ARR_PAYLOAD, DBS_ARR_SEGMENTS, DBS_ARR_XMASK, DBS_ARR_ACTIVE, DBS_ARR_CSC_CM, DBS_ARR_PAT_SEGS,
@@ -82,12 +84,26 @@ class dbs_rope_options(C.Structure):
                 ("low", C.c_double), ("high", C.c_double), ("context", C.c_double)]
 
 
+class dbs_norm_part(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_token_stride", C.c_int64), ("x_head_stride", C.c_int64), ("out", C.c_void_p),
+                ("out_token_stride", C.c_int64), ("out_head_stride", C.c_int64), ("heads", C.c_int32), ("weight", C.c_void_p)]
+
+
+class dbs_kv4_view(C.Structure):
+    """dbs_kv4_cache of the C ABI."""
+    _fields_ = [("pool", C.c_void_p), ("page_stride", C.c_int64), ("pages", C.c_int32), ("page_tokens", C.c_int32),
+                ("key_heads", C.c_int32), ("head_dim", C.c_int32), ("group", C.c_int32), ("sequences", C.c_int32),
+                ("table_pages", C.c_int32), ("table", C.c_void_p), ("ldtable", C.c_int64), ("lens", C.c_void_p),
+                ("new_ptr", C.c_void_p)]
+
+
 EXPORTED = ["dbs_build_options_default", "dbs_build", "dbs_spmspv", "dbs_spmspv_dense",
             "dbs_spmspv_dense_threshold", "dbs_bfs", "dbs_bfs_noalloc",
             "dbs_set_option", "dbs_get_option", "dbs_get_stats", "dbs_copy_array", "dbs_free",
             "dbs_status_string", "dbs_probe_read",
             "dbs_q4_build", "dbs_q4_bytes", "dbs_q4_free", "dbs_q4_product", "dbs_q4_product_masked", "dbs_q4_gated",
-            "dbs_logits_adjust", "dbs_rope", "dbs_rope_frequencies"]
+            "dbs_logits_adjust", "dbs_rope", "dbs_rope_frequencies", "dbs_norm_rope",
+            "dbs_kv4_page_bytes", "dbs_kv4_store", "dbs_kv4_attention_workspace", "dbs_kv4_attention"]
 
 
 def load_library(path: str = LIB_PATH) -> C.CDLL:
@@ -126,6 +142,11 @@ def load_library(path: str = LIB_PATH) -> C.CDLL:
         "dbs_logits_adjust": [i32, i32, vp, C.c_int, i64, C.c_char_p, vp, C.c_int, i64, vp],
         "dbs_rope": [i32, i32, i32, i32, C.c_int, vp, vp, C.c_float, i32, vp, C.c_int, i64, i64, vp, C.c_int, i64,
                      i64, vp],
+        "dbs_norm_rope": [i32, i32, i32, C.c_int, vp, vp, C.c_float, C.c_float, vp, i32, C.c_int, C.c_int, C.c_int, vp],
+        "dbs_kv4_page_bytes": [i32, i32, i32, i32, C.POINTER(i64)],
+        "dbs_kv4_store": [vp, i32, vp, i64, i64, vp, i64, i64, C.c_int, vp, i64, i64, vp, i64, i64, C.c_int, vp],
+        "dbs_kv4_attention_workspace": [vp, i32, i32, C.c_int, C.c_int, i32, i32, i32, C.POINTER(i64)],
+        "dbs_kv4_attention": [vp, i32, i32, vp, C.c_int, i64, i64, vp, C.c_int, i64, i64, C.c_float, i32, i32, i32, vp, i64, vp],
         "dbs_rope_frequencies": [C.POINTER(dbs_rope_options), C.POINTER(C.c_double), C.POINTER(C.c_float)],
     }
     for name, args in sig.items():
@@ -371,7 +392,8 @@ def _load_calls():
     except ImportError as e:  # built for another torch or interpreter
         return _NoCalls(f"{path} does not load, build it again: {e}")
     _calls.bind(*(C.cast(getattr(_lib, f), C.c_void_p).value for f in (
-        "dbs_q4_product", "dbs_q4_product_masked", "dbs_q4_gated", "dbs_logits_adjust", "dbs_rope")))
+        "dbs_q4_product", "dbs_q4_product_masked", "dbs_q4_gated", "dbs_logits_adjust", "dbs_rope", "dbs_norm_rope",
+        "dbs_kv4_page_bytes", "dbs_kv4_store", "dbs_kv4_attention_workspace", "dbs_kv4_attention")))
     return _calls
 
 
@@ -486,3 +508,75 @@ def dbs_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = DBS
     _check(_lib.dbs_rope_frequencies(C.byref(o), C.cast(freq.data_ptr(), C.POINTER(C.c_double)) if freq.numel() else None,
                                      C.byref(scale)), "dbs_rope_frequencies")
     return freq, float(scale.value)
+
+
+def dbs_norm_rope(q, k, q_weight, k_weight, pos, freq, q_out, k_out, eps: float = 1e-6, layout: int = DBS_ROPE_HALF,
+                  scale: float = 1.0, stream=None) -> None:
+    """Root mean square norms of the heads of q and k [tokens, heads, head_dim] with weights [head_dim] (or None: ones),
+    then dbs_rope on them, into q_out and k_out, which may be q and k themselves.  k, k_weight and k_out may be None."""
+    st = _calls.norm_rope(q, k, q_weight, k_weight, pos, freq, q_out, k_out, eps, layout, scale, stream)
+    if st:
+        raise DBSError(st, "dbs_norm_rope")
+
+
+class KV4Cache:
+    """The pages of a cache of 4-bit keys and values, and what they hold: `pool` is uint8 [pages, bytes], the caller's or
+    one of dbs_kv4_cache's; the bytes of a page are those of dbs_kv4_page_bytes or more."""
+
+    def __init__(self, pool, key_heads: int, head_dim: int, group: int, page_tokens: int):
+        self.pool = pool
+        self.key_heads, self.head_dim, self.group, self.page_tokens = key_heads, head_dim, group, page_tokens
+
+
+def dbs_kv4_page_bytes(key_heads: int, head_dim: int, group: int, page_tokens: int) -> int:
+    v = C.c_int64()
+    for x in (key_heads, head_dim, group, page_tokens):  # here, since ctypes keeps the low 32 bits
+        if not 0 <= int(x) < 1 << 31:
+            raise ValueError(f"{x} is out of range")
+    _check(_lib.dbs_kv4_page_bytes(int(key_heads), int(head_dim), int(group), int(page_tokens), C.byref(v)), "dbs_kv4_page_bytes")
+    return int(v.value)
+
+
+def dbs_kv4_cache(pages: int, key_heads: int, head_dim: int, group: int, page_tokens: int, pool=None) -> KV4Cache:
+    """The description of `pages` pages of `page_tokens` tokens (16 to 256, a power of two) of key_heads heads of
+    head_dim (a multiple of 8 up to 256) in groups of 32, 64 or 128 channels.  Without `pool` the pages are allocated on
+    the current device; their tokens are undefined until dbs_kv4_store."""
+    size = dbs_kv4_page_bytes(key_heads, head_dim, group, page_tokens)
+    if pool is None:
+        pool = _torch.empty(int(pages), size, dtype=_torch.uint8, device="cuda")
+    elif not isinstance(pool, _Tensor) or not pool.is_cuda or pool.dtype != _torch.uint8:
+        raise TypeError("pool must be a uint8 CUDA tensor")
+    elif pool.dim() != 2 or pool.size(0) != pages or pool.size(1) < size or (pool.size(1) > 1 and pool.stride(1) != 1):
+        raise ValueError(f"pool must be [{pages}, {size} or more] with contiguous pages")
+    elif pool.size(0) > 1 and pool.stride(0) < pool.size(1):
+        raise ValueError("pages of the pool overlap")
+    return KV4Cache(pool, int(key_heads), int(head_dim), int(group), int(page_tokens))
+
+
+def dbs_kv4_store(cache: KV4Cache, table, lens, k, v, new_ptr=None, k_out=None, v_out=None, stream=None) -> None:
+    """Keys and values [tokens, key_heads, head_dim] of the new tokens into their pages: row new_ptr[b] + i is the i-th of
+    sequence b's new tokens, the last ones of its lens[b] tokens, whose pages are table[b] (int32); without new_ptr every
+    sequence has tokens / sequences new ones.  k_out and v_out receive what the cache now stands for."""
+    st = _calls.kv4_store(cache.pool, cache.key_heads, cache.head_dim, cache.group, cache.page_tokens, table, lens, k, v,
+                          new_ptr, k_out, v_out, stream)
+    if st:
+        raise DBSError(st, "dbs_kv4_store")
+
+
+def dbs_kv4_attention(cache: KV4Cache, table, lens, q, out, new_ptr=None, window: int = 0, sinks: int = 0, scale=None,
+                      max_len: int = 0, workspace=None, stream=None) -> None:
+    """Attention of the new tokens, stored before, over their sequences: q and out [tokens, heads, head_dim].  A token at
+    position i sees tokens j <= i and, with a window, of these j > i - window and j < sinks.  scale: 1/sqrt(head_dim)
+    unless given.  max_len bounds lens (0: the table's room); it and the workspace (uint8, allocated for the call
+    unless given) only tell how the work is cut."""
+    st = _calls.kv4_attention(cache.pool, cache.key_heads, cache.head_dim, cache.group, cache.page_tokens, table, lens, q, out,
+                              new_ptr, window, sinks, scale, max_len, workspace, stream)
+    if st:
+        raise DBSError(st, "dbs_kv4_attention")
+
+
+def dbs_kv4_attention_workspace(cache: KV4Cache, table, lens, q, out, new_ptr=None, window: int = 0, sinks: int = 0,
+                                max_len: int = 0) -> int:
+    """Bytes of the workspace that dbs_kv4_attention takes for these arguments."""
+    return _calls.kv4_workspace(cache.pool, cache.key_heads, cache.head_dim, cache.group, cache.page_tokens, table, lens, q, out,
+                                new_ptr, window, sinks, max_len)

@@ -21,7 +21,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["scan.hip", "build.hip", "spmspv.hip", "bfs.hip", "probe.hip", "q4.hip", "q4_bf16.hip", "q4_bf16_gated.hip",
-           "q4_f32.hip", "q4_f32_gated.hip", "logits.hip", "rope.hip",
+           "q4_f32.hip", "q4_f32_gated.hip", "logits.hip", "rope.hip", "norm_rope.hip",
+           "kv4.hip", "kv4_64.hip", "kv4_96.hip", "kv4_128.hip", "kv4_192.hip", "kv4_256.hip",
            "api.cpp"]
 
 FLAGS = [

@@ -4,6 +4,9 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <cmath>
+
+#include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -17,6 +20,11 @@ decltype(&dbs_q4_product_masked) f_masked;
 decltype(&dbs_q4_gated) f_gated;
 decltype(&dbs_logits_adjust) f_logits;
 decltype(&dbs_rope) f_rope;
+decltype(&dbs_norm_rope) f_norm;
+decltype(&dbs_kv4_page_bytes) f_page_bytes;
+decltype(&dbs_kv4_store) f_store;
+decltype(&dbs_kv4_attention_workspace) f_workspace;
+decltype(&dbs_kv4_attention) f_attention;
 
 // A Python exception is set where a check fails.
 struct failed {};
@@ -152,7 +160,7 @@ const T *list(const call &c, PyObject *o, const char *name, at::ScalarType type,
 template <class F>
 PyObject *status(F f) {
   try {
-    return PyLong_FromLong(f());
+    return PyLong_FromLongLong(f());
   } catch (const failed &) {
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -273,10 +281,193 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// addresses of dbs_q4_product, dbs_q4_product_masked, dbs_q4_gated, dbs_logits_adjust, dbs_rope
+// heads [tokens, heads, head_dim] with contiguous elements and any other strides; None where that is allowed
+struct heads {
+  int64_t tokens = 0, count = 0, dim = 0, st = 0, sh = 0;
+  dbs_dtype type = DBS_F32;
+  void *p = nullptr;
+  heads(const call &c, PyObject *o, const char *name, bool optional = false) {
+    if (optional && o == Py_None) return;
+    const at::Tensor &t = c.tensor(o, name);
+    type = vector_type(t, name);
+    if (t.dim() != 3) fail(PyExc_ValueError, "%s must be [tokens, heads, head_dim]", name);
+    if (t.size(2) > 1 && t.numel() > 0 && t.stride(2) != 1) fail(PyExc_ValueError, "%s must have contiguous heads", name);
+    tokens = t.size(0);
+    count = t.size(1);
+    dim = t.size(2);
+    if (tokens > INT32_MAX || count > INT32_MAX || dim > INT32_MAX) fail(PyExc_ValueError, "%s is too large", name);
+    st = t.stride(0);
+    sh = t.stride(1);
+    p = t.data_ptr();
+  }
+  void like(const heads &x, const char *name, const char *other) const {
+    if (tokens != x.tokens || count != x.count || dim != x.dim) fail(PyExc_ValueError, "%s and %s must be of one shape", name, other);
+  }
+};
+
+int32_t small(PyObject *o, const char *name) {
+  const int64_t v = integer(o);
+  if (v < INT32_MIN || v > INT32_MAX) fail(PyExc_ValueError, "%s is out of range", name);
+  return (int32_t)v;
+}
+
+// q, k, q_weight, k_weight, pos, freq, q_out, k_out, eps, layout, scale, stream
+PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status([&] {
+    need(n, 12);
+    const call c(a[6], "q_out", a[11]);
+    const heads q(c, a[0], "q"), k(c, a[1], "k", true), qo(c, a[6], "q_out"), ko(c, a[7], "k_out", true);
+    const bool two = a[1] != Py_None;
+    if (two != (a[7] != Py_None)) fail(PyExc_ValueError, "k and k_out go together");
+    if (!two && a[3] != Py_None) fail(PyExc_ValueError, "k_weight without k");
+    qo.like(q, "q", "q_out");
+    if (two) {
+      ko.like(k, "k", "k_out");
+      if (k.tokens != q.tokens || k.dim != q.dim) fail(PyExc_ValueError, "q and k have the same tokens and head_dim");
+      if (k.type != q.type || ko.type != qo.type) fail(PyExc_TypeError, "q and k, and their outputs, have the same dtype");
+    }
+    if (a[4] == Py_None || a[5] == Py_None) fail(PyExc_TypeError, "pos and freq must be CUDA tensors");
+    int64_t pairs = 0;
+    const int32_t *pos = list<int32_t>(c, a[4], "pos", at::kInt, q.tokens);
+    const double *freq = list<double>(c, a[5], "freq", at::kDouble, -1, &pairs);
+    if (pairs > INT32_MAX / 2) fail(PyExc_ValueError, "freq is too large");
+    dbs_dtype weight_type = DBS_F32;
+    const void *weight[2] = {nullptr, nullptr};
+    for (int i = 0; i < 2; ++i) {
+      if (a[2 + i] == Py_None) continue;
+      const char *const name = i ? "k_weight" : "q_weight";
+      const at::Tensor &t = c.tensor(a[2 + i], name);
+      const dbs_dtype type = vector_type(t, name);
+      if (!t.is_contiguous() || t.dim() != 1 || t.size(0) != q.dim) fail(PyExc_ValueError, "%s must be [%lld], contiguous", name, (long long)q.dim);
+      if (i && weight[0] && type != weight_type) fail(PyExc_TypeError, "the weights have the same dtype");
+      weight_type = type;
+      weight[i] = t.data_ptr();
+    }
+    const dbs_norm_part parts[2] = {{q.p, q.st, q.sh, qo.p, qo.st, qo.sh, (int32_t)q.count, weight[0]},
+                                    {k.p, k.st, k.sh, ko.p, ko.st, ko.sh, (int32_t)k.count, weight[1]}};
+    return unlocked(f_norm, (int32_t)q.tokens, (int32_t)q.dim, (int32_t)(2 * pairs), choice<dbs_rope_layout>(a[9]), pos, freq,
+                    (float)number(a[10]), (float)number(a[8]), &parts[0], two ? 2 : 1, q.type, qo.type, weight_type, c.stream);
+  });
+}
+
+// pool, key_heads, head_dim, group, page_tokens, table, lens, and new_ptr
+struct cache {
+  dbs_kv4_cache v = {};
+  cache(const call &c, PyObject *const *a, PyObject *new_ptr) {
+    const at::Tensor &pool = c.tensor(a[0], "the pool"), &table = c.tensor(a[5], "table");
+    if (pool.scalar_type() != at::kByte || pool.dim() != 2 || (pool.size(1) > 1 && pool.stride(1) != 1))
+      fail(PyExc_TypeError, "the pool must be uint8 [pages, bytes] with contiguous pages");
+    v.key_heads = small(a[1], "key_heads");
+    v.head_dim = small(a[2], "head_dim");
+    v.group = small(a[3], "group");
+    v.page_tokens = small(a[4], "page_tokens");
+    if (pool.size(0) > INT32_MAX) fail(PyExc_ValueError, "the pool has too many pages");
+    v.pool = pool.data_ptr();
+    v.pages = (int32_t)pool.size(0);
+    int64_t bytes = 0;
+    if (f_page_bytes(v.key_heads, v.head_dim, v.group, v.page_tokens, &bytes) != DBS_OK)
+      fail(PyExc_ValueError, "no cache of %d heads of %d in groups of %d and pages of %d tokens", (int)v.key_heads, (int)v.head_dim,
+           (int)v.group, (int)v.page_tokens);
+    if (pool.size(1) < bytes) fail(PyExc_ValueError, "pages have %lld bytes, %lld are needed", (long long)pool.size(1), (long long)bytes);
+    v.page_stride = v.pages > 1 ? pool.stride(0) : bytes;
+    if (v.page_stride < bytes) fail(PyExc_ValueError, "pages of the pool overlap");
+    if (table.scalar_type() != at::kInt || table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1))
+      fail(PyExc_TypeError, "table must be int32 [sequences, pages] with contiguous rows");
+    if (table.size(0) > INT32_MAX || table.size(1) > INT32_MAX) fail(PyExc_ValueError, "table is too large");
+    v.sequences = (int32_t)table.size(0);
+    v.table_pages = (int32_t)table.size(1);
+    v.ldtable = v.sequences > 1 ? table.stride(0) : v.table_pages;
+    v.table = (const int32_t *)table.data_ptr();
+    if (a[6] == Py_None) fail(PyExc_TypeError, "lens must be a CUDA tensor");
+    v.lens = list<int32_t>(c, a[6], "lens", at::kInt, v.sequences);
+    v.new_ptr = list<int32_t>(c, new_ptr, "new_ptr", at::kInt, (int64_t)v.sequences + 1);
+  }
+  void takes(const heads &x, const char *name) const {
+    if (x.dim != v.head_dim) fail(PyExc_ValueError, "%s has heads of %lld, the cache of %d", name, (long long)x.dim, (int)v.head_dim);
+    if (!v.new_ptr && v.sequences > 0 && x.tokens % v.sequences)
+      fail(PyExc_ValueError, "%lld tokens of %d sequences: new_ptr is needed", (long long)x.tokens, (int)v.sequences);
+  }
+};
+
+// pool, key_heads, head_dim, group, page_tokens, table, lens, k, v, new_ptr, k_out, v_out, stream
+PyObject *kv4_store(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status([&] {
+    need(n, 13);
+    const call c(a[0], "the pool", a[12]);
+    const cache s(c, a, a[9]);
+    const heads k(c, a[7], "k"), v(c, a[8], "v"), ko(c, a[10], "k_out", true), vo(c, a[11], "v_out", true);
+    s.takes(k, "k");
+    v.like(k, "k", "v");
+    if (k.count != s.v.key_heads) fail(PyExc_ValueError, "k has %lld heads, the cache %d", (long long)k.count, (int)s.v.key_heads);
+    if (v.type != k.type) fail(PyExc_TypeError, "k and v have the same dtype");
+    if (ko.p || a[10] != Py_None) ko.like(k, "k", "k_out");
+    if (vo.p || a[11] != Py_None) vo.like(v, "v", "v_out");
+    if (a[10] != Py_None && a[11] != Py_None && ko.type != vo.type) fail(PyExc_TypeError, "k_out and v_out have the same dtype");
+    return unlocked(f_store, &s.v, (int32_t)k.tokens, k.p, k.st, k.sh, v.p, v.st, v.sh, k.type, ko.p, ko.st, ko.sh, vo.p, vo.st, vo.sh,
+                    a[10] != Py_None ? ko.type : vo.type, c.stream);
+  });
+}
+
+// pool, key_heads, head_dim, group, page_tokens, table, lens, q, out, new_ptr, window, sinks, scale, max_len, workspace, stream
+PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status([&]() -> long {
+    need(n, 16);
+    const call c(a[8], "out", a[15]);
+    const cache s(c, a, a[9]);
+    const heads q(c, a[7], "q"), o(c, a[8], "out");
+    s.takes(q, "q");
+    o.like(q, "q", "out");
+    const int32_t window = small(a[10], "window"), sinks = small(a[11], "sinks"), max_len = small(a[13], "max_len");
+    const float scale = a[12] == Py_None ? (float)(1.0 / std::sqrt((double)q.dim)) : (float)number(a[12]);
+    int64_t bytes = 0;
+    void *space = nullptr;
+    void *own = nullptr;
+    if (a[14] == Py_None) {
+      const dbs_status st = f_workspace(&s.v, (int32_t)q.tokens, (int32_t)q.count, q.type, o.type, window, sinks, max_len, &bytes);
+      if (st != DBS_OK) return st;
+      // from the given stream's memory, and given back to it: what it runs later may have it
+      if (bytes > 0) own = c10::hip::HIPCachingAllocator::raw_alloc_with_stream((size_t)bytes, (hipStream_t)c.stream);
+      space = own;
+    } else {
+      const at::Tensor &t = c.tensor(a[14], "workspace");
+      if (t.scalar_type() != at::kByte || !t.is_contiguous()) fail(PyExc_TypeError, "workspace must be contiguous uint8");
+      bytes = t.numel();
+      space = t.data_ptr();
+    }
+    const dbs_status st = unlocked(f_attention, &s.v, (int32_t)q.tokens, (int32_t)q.count, q.p, q.type, q.st, q.sh, o.p, o.type, o.st, o.sh,
+                                   scale, window, sinks, max_len, space, bytes, c.stream);
+    if (own) c10::hip::HIPCachingAllocator::raw_delete(own);
+    return st;
+  });
+}
+
+// pool, key_heads, head_dim, group, page_tokens, table, lens, q, out, new_ptr, window, sinks, max_len
+PyObject *kv4_workspace(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status([&] {
+    need(n, 13);
+    const call c(a[8], "out", Py_None);
+    const cache s(c, a, a[9]);
+    const heads q(c, a[7], "q"), o(c, a[8], "out");
+    s.takes(q, "q");
+    o.like(q, "q", "out");
+    int64_t bytes = 0;
+    const dbs_status st = f_workspace(&s.v, (int32_t)q.tokens, (int32_t)q.count, q.type, o.type, small(a[10], "window"), small(a[11], "sinks"),
+                                      small(a[12], "max_len"), &bytes);
+    if (st != DBS_OK) fail(PyExc_ValueError, "no call of these arguments (status %d)", (int)st);
+    return bytes;
+  });
+}
+
+// addresses of dbs_q4_product, dbs_q4_product_masked, dbs_q4_gated, dbs_logits_adjust, dbs_rope, dbs_norm_rope,
+// dbs_kv4_page_bytes, dbs_kv4_store, dbs_kv4_attention_workspace, dbs_kv4_attention
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   try {
-    if (n != 5) fail(PyExc_TypeError, "%zd arguments, expected 5", n);
+    if (n != 10) fail(PyExc_TypeError, "%zd arguments, expected 10", n);
+    f_norm = (decltype(f_norm))pointer(a[5]);
+    f_page_bytes = (decltype(f_page_bytes))pointer(a[6]);
+    f_store = (decltype(f_store))pointer(a[7]);
+    f_workspace = (decltype(f_workspace))pointer(a[8]);
+    f_attention = (decltype(f_attention))pointer(a[9]);
     f_masked = (decltype(f_masked))pointer(a[1]);
     f_gated = (decltype(f_gated))pointer(a[2]);
     f_logits = (decltype(f_logits))pointer(a[3]);
@@ -290,7 +481,8 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 #define METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind), METHOD(q4_product), METHOD(q4_product_masked), METHOD(q4_gated),
-                         METHOD(logits_adjust), METHOD(rope), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(logits_adjust), METHOD(rope), METHOD(norm_rope),
+                         METHOD(kv4_store), METHOD(kv4_attention), METHOD(kv4_workspace), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,385 @@
+// The paged cache of 4-bit keys and values: new tokens into it (dbs_kv4_store), and the calls of the attention over it
+// (dbs_kv4_attention), whose kernels are in kv4_attention.h.
+#include "kv4.h"
+
+#include <math.h>
+
+namespace {
+
+struct kv4_side {
+  const void *x;
+  int64_t xt, xh;
+  void *y;
+  int64_t yt, yh;
+};
+
+/*
+ * Mathematics: of a group's values x (32, 64 or 128 channels of a head of a token) b = half(min), s = half((max - b) / 15) and
+ * codes rint((x - b) / s) within 0..15, each step in fp32 and with products by reciprocals, so that the codes are
+ * reproducible bit by bit.  A group with a value beyond DBS_KV4_MAX_VALUE is NaN throughout.
+ *
+ * A workgroup takes the new ones of eight tokens that share words of the value codes, for one key head: lanes along the
+ * channels, eight to a lane, keys in the first half of the workgroup and values in the second.  Words of tokens that were
+ * there before are read and kept.  Only this workgroup writes these words, so nothing is atomic.
+ */
+template <class X, class Y>
+__global__ void k_kv4_store(kv4_view c, int dim, int padded, int group, kv4_side key, kv4_side value) {
+  __shared__ uint32_t codes[8][KV4_MAX_DIM / 8 + 1];
+  const int64_t unit = blockIdx.x;
+  const int head = blockIdx.y;
+  int b, nth;
+  if (c.new_ptr) {
+    b = kv4_find(c, unit, 1, 8, 2);
+    nth = (int)(unit - kv4_new_ptr(c, b) / 8 - 2 * b);
+  } else {
+    const int units = (c.each + 6) / 8 + 1;
+    b = (int)(unit / units);
+    nth = (int)(unit % units);
+  }
+  const kv4_rows rows = kv4_rows_of(c, b);
+  if (nth < 0 || rows.count <= 0) return;
+  // slots [from, from + 8) of the cache; before the first slot there is nothing to keep, but rows to return
+  const int from = ((rows.position >> 3) + nth) * 8;
+  if (from >= rows.position + rows.count) return;
+
+  const int lanes = padded / 8, side = threadIdx.x >= 8 * lanes;
+  const int e = threadIdx.x / lanes - 8 * side, l = threadIdx.x % lanes, channel = 8 * l;
+  const int t = from + e - rows.position;  // the token among the new ones
+  const bool is_new = t >= 0 && t < rows.count;
+  const kv4_layout lay(padded, group, 1 << c.page_shift);
+  uint8_t *const page = kv4_page(c, b, from, (int64_t)head * lay.head_bytes);
+  const kv4_side &to = side ? value : key;
+  const int64_t row = rows.first + t;
+
+  float x[8];
+  const bool in = is_new && channel < dim;
+  if (in) {
+    X v[8];
+    __builtin_memcpy(v, (const X *)to.x + row * to.xt + head * to.xh + channel, sizeof v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = dbs_value<X>::load(&v[i]);
+  }
+  float low = INFINITY, high = -INFINITY;
+  bool bad = false;
+  if (in) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      low = fminf(low, x[i]);
+      high = fmaxf(high, x[i]);
+      bad |= !(fabsf(x[i]) <= DBS_KV4_MAX_VALUE);
+    }
+  }
+  for (int o = 1; o < group / 8; o <<= 1) {
+    low = fminf(low, __shfl_xor(low, o));
+    high = fmaxf(high, __shfl_xor(high, o));
+    bad |= __shfl_xor((int)bad, o) != 0;
+  }
+  if (low > high) low = high = 0.0f;  // no channel of the head
+  _Float16 of = (_Float16)low;
+  _Float16 sc = (_Float16)fmaxf((high - (float)of) * (1.0f / 15.0f), 0.0f);
+  if (bad) of = sc = (_Float16)NAN;
+  const float step = (float)sc, base = (float)of, inverse = step > 0.0f ? 1.0f / step : 0.0f;
+  uint32_t word = 0u;
+  if (in) {
+    Y y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = bad ? 0.0f : fminf(fmaxf(rintf((x[i] - base) * inverse), 0.0f), 15.0f);
+      word |= (uint32_t)q << (4 * i);
+      y[i] = dbs_value<Y>::of((float)(_Float16)__builtin_fmaf(step, q, base));
+    }
+    if (to.y) __builtin_memcpy((Y *)to.y + row * to.yt + head * to.yh + channel, y, sizeof y);
+  }
+  const int slot = from & ((1 << c.page_shift) - 1);
+  const bool first = channel % group == 0;
+  uint16_t bits[2];
+  __builtin_memcpy(&bits[0], &sc, 2);
+  __builtin_memcpy(&bits[1], &of, 2);
+  if (page && is_new && !side) {
+    // channels 32 k + 8 g .. + 7 are word g (d / 32) + k
+    ((uint32_t *)(page + (slot + e) * (padded / 2)))[(l & 3) * (padded / 32) + (l >> 2)] = word;
+    if (first) ((uint32_t *)(page + lay.key_records))[(slot + e) * lay.groups + channel / group] = bits[0] | (uint32_t)bits[1] << 16;
+  }
+  if (side) {
+    codes[e][l] = word;
+    if (page && is_new && first) {
+      uint16_t *r = (uint16_t *)(page + lay.value_records) + ((slot >> 3) * lay.groups + channel / group) * 16 + kv4_place(e);
+      r[0] = bits[0];
+      r[8] = bits[1];
+    }
+  }
+  __syncthreads();
+  if (!page) return;
+  // a word of the value codes to a thread: nibble e is token e's
+  uint32_t news = 0u;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (from + k >= rows.position && from + k < rows.position + rows.count) news |= 15u << (4 * k);
+  uint32_t *words = (uint32_t *)(page + lay.value_codes) + (slot >> 3) * padded;
+  for (int i = threadIdx.x; i < padded; i += blockDim.x) {
+    const int ch = 16 * (i % (padded / 16)) + i / (padded / 16);
+    uint32_t w = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w |= (codes[k][ch >> 3] >> (4 * (ch & 7)) & 15u) << (4 * k);
+    words[i] = news == ~0u ? w : (words[i] & ~news) | (w & news);
+  }
+}
+
+/*
+ * Joins the splits of a row: o = sum_z 2^(m_z - m) o_z / sum_z 2^(m_z - m) l_z, in the order of the splits.  A workgroup to a
+ * row, its waves taking every fourth split.
+ */
+template <class Y>
+__global__ __launch_bounds__(256) void k_kv4_combine(kv4_view c, int heads, int dim, int padded, int splits, const float *__restrict__ partial,
+                                                     Y *__restrict__ out, int64_t ot, int64_t oh) {
+  __shared__ float sums[4], parts[4][KV4_MAX_DIM];
+  const int64_t row = blockIdx.x;
+  const int64_t t = row / heads;
+  const int h = (int)(row % heads), wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (c.new_ptr && (t < kv4_new_ptr(c, 0) || t >= kv4_new_ptr(c, c.sequences))) return;  // of no sequence
+  const int64_t stride = (int64_t)c.tokens * heads * (padded + 2);
+  const float *from = partial + row * (padded + 2);
+  float top = -3.402823466e38f;
+  for (int z = lane; z < splits; z += 64) top = fmaxf(top, from[z * stride + padded]);
+  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  float sum = 0.0f, v[KV4_MAX_DIM / 64] = {};
+#pragma unroll 4
+  for (int z = wave; z < splits; z += 4) {
+    const float l = from[z * stride + padded + 1], f = __builtin_amdgcn_exp2f(from[z * stride + padded] - top);
+    if (l == 0.0f) continue;
+    sum += f * l;
+#pragma unroll
+    for (int k = 0; k < KV4_MAX_DIM / 64; ++k)
+      if (64 * k + lane < padded) v[k] += f * from[z * stride + 64 * k + lane];
+  }
+#pragma unroll
+  for (int k = 0; k < KV4_MAX_DIM / 64; ++k) parts[wave][64 * k + lane] = v[k];
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  const float all = sums[0] + sums[1] + sums[2] + sums[3], f = all == 0.0f ? 0.0f : 1.0f / all;
+  const int ch = threadIdx.x;
+  if (ch < dim) out[t * ot + h * oh + ch] = dbs_value<Y>::of((parts[0][ch] + parts[1][ch] + parts[2][ch] + parts[3][ch]) * f);
+}
+
+bool view_of(const dbs_kv4_cache *a, int32_t tokens, kv4_view *c, dbs_status *st) {
+  *st = DBS_ERR_INVALID_ARG;
+  int64_t bytes = 0;
+  if (!a || tokens < 0 || dbs_kv4_page_bytes(a->key_heads, a->head_dim, a->group, a->page_tokens, &bytes) != DBS_OK) return false;
+  if (a->sequences < 0 || a->pages < 0 || a->table_pages < 0 || a->page_stride < bytes || a->page_stride % 16) return false;
+  if (a->sequences > 1 && a->ldtable < a->table_pages) return false;
+  if (!a->new_ptr && a->sequences > 0 && tokens % a->sequences) return false;
+  if (a->sequences == 0 && tokens > 0 && !a->new_ptr) return false;
+  const int64_t slots = (int64_t)a->table_pages * a->page_tokens;
+  if (slots > DBS_KV4_MAX_CONTEXT || a->sequences > DBS_KV4_MAX_SEQUENCES) {
+    *st = DBS_ERR_UNSUPPORTED;
+    return false;
+  }
+  *st = DBS_OK;
+  if (tokens == 0 || a->sequences == 0) return false;
+  if (!a->lens || !a->pool || a->pages < 1 || (a->table_pages > 0 && !a->table) || (uintptr_t)a->pool % 16) {
+    *st = DBS_ERR_INVALID_ARG;
+    return false;
+  }
+  c->pool = (uint8_t *)a->pool;
+  c->page_stride = a->page_stride;
+  c->pages = a->pages;
+  c->page_shift = __builtin_ctz((unsigned)a->page_tokens);
+  c->width = a->table_pages;
+  c->sequences = a->sequences;
+  c->tokens = tokens;
+  c->each = a->new_ptr ? 0 : tokens / a->sequences;
+  c->table = a->table;
+  c->ldtable = a->ldtable;
+  c->lens = a->lens;
+  c->new_ptr = a->new_ptr;
+  return true;
+}
+
+// whether heads [tokens][heads][dim] share an element with each other
+bool heads_meet(int64_t tokens, int64_t st, int64_t heads, int64_t sh, int64_t dim) {
+  return !dbs_rows_apart(tokens, st, heads, sh, dim) && !dbs_rows_apart(heads, sh, tokens, st, dim);
+}
+
+dbs_rows rows_of(const void *p, int64_t tokens, int64_t st, int64_t heads, int64_t sh, int64_t dim, int dtype) {
+  const __int128 size = dbs_vector_size(dtype);
+  return {(__int128)(uintptr_t)p, tokens, st * size, heads, sh * size, dim * size};
+}
+
+bool written_over(const dbs_rows &out, const void *p, int64_t bytes) {
+  const dbs_rows s = out.span();
+  return p && dbs_overlap(p, bytes, (const void *)(uintptr_t)s.at, (int64_t)s.width);
+}
+
+// whether rows that a call writes meet what it reads of the cache
+bool meets_lists(const dbs_rows &out, const dbs_kv4_cache *a) {
+  return written_over(out, a->lens, (int64_t)a->sequences * 4) ||
+         written_over(out, a->new_ptr, ((int64_t)a->sequences + 1) * 4) ||
+         written_over(out, a->table, a->table_pages ? ((a->sequences - 1) * a->ldtable + a->table_pages) * 4 : 0);
+}
+bool meets_pool(const dbs_rows &rows, const dbs_kv4_cache *a) {
+  int64_t bytes = 0;
+  (void)dbs_kv4_page_bytes(a->key_heads, a->head_dim, a->group, a->page_tokens, &bytes);
+  // rows between the pages of a larger buffer are no use of it: the whole span counts
+  return written_over(rows, a->pool, (a->pages - 1) * a->page_stride + bytes);
+}
+
+// How a call is cut: tiles of 16 rows a wave takes, workgroups along the rows, and splits of the tokens.
+struct kv4_plan {
+  int tiles, splits, chunk;
+  int64_t units;
+};
+
+kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wide, int32_t window, int32_t sinks, int32_t max_len) {
+  kv4_plan p;
+  const int rep = heads / a->key_heads;
+  const int64_t rows = (int64_t)tokens * rep, each = (rows + a->sequences - 1) / a->sequences;
+  const int d = kv4_padded(a->head_dim);
+  p.tiles = each <= 16 ? 1 : each <= 32 || wide || d > 128 ? 2 : 4;
+  const int per = 16 * p.tiles * 4;
+  p.units = a->new_ptr ? rows / per + a->sequences : (tokens / a->sequences * (int64_t)rep + per - 1) / per * a->sequences;
+  int64_t slots = (int64_t)a->table_pages * a->page_tokens;
+  if (max_len > 0 && max_len < slots) slots = max_len;
+  int64_t blocks = (slots + KV4_BLOCK - 1) / KV4_BLOCK;
+  if (window) {
+    const int64_t span = (int64_t)window + (each < per ? each : per) / rep + 1;
+    const int64_t seen = (span + KV4_BLOCK - 1) / KV4_BLOCK + 1 + ((int64_t)sinks + KV4_BLOCK - 1) / KV4_BLOCK;
+    if (seen < blocks) blocks = seen;
+  }
+  const int64_t groups = p.units * a->key_heads;
+  const int64_t target = 1024;
+  int64_t splits = groups < target ? (target + groups - 1) / groups : 1;
+  const int64_t most = blocks / 8;  // at least two blocks a wave
+  if (splits > most) splits = most;
+  if (splits < 1) splits = 1;
+  if (splits > 1024) splits = 1024;
+  p.chunk = (int)((blocks + splits - 1) / splits);
+  p.chunk = (p.chunk + 3) / 4 * 4;
+  p.splits = blocks > p.chunk ? (int)((blocks + p.chunk - 1) / p.chunk) : 1;
+  return p;
+}
+
+int64_t partial_bytes(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, int splits) {
+  return splits > 1 ? (int64_t)splits * tokens * heads * (kv4_padded(a->head_dim) + 2) * 4 : 0;
+}
+
+dbs_status check_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, int32_t q_dtype, int32_t out_dtype, int32_t window,
+                           int32_t sinks, int32_t max_len, kv4_view *c, bool *go) {
+  dbs_status st;
+  *go = view_of(a, tokens, c, &st);
+  if (st != DBS_OK) return st;
+  if (heads < 0 || heads % a->key_heads || !dbs_is_vector_dtype(q_dtype) || !dbs_is_vector_dtype(out_dtype) || window < 0 ||
+      sinks < 0 || max_len < 0)
+    return DBS_ERR_INVALID_ARG;
+  if ((int64_t)tokens * heads > DBS_KV4_MAX_ROWS) return DBS_ERR_UNSUPPORTED;
+  if (heads == 0) *go = false;
+  return DBS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dbs_status dbs_kv4_page_bytes(int32_t key_heads, int32_t head_dim, int32_t group, int32_t page_tokens, int64_t *bytes) {
+  if (key_heads < 1 || key_heads > 65535 || head_dim < 8 || head_dim > KV4_MAX_DIM || head_dim % 8 || !bytes) return DBS_ERR_INVALID_ARG;
+  if (page_tokens < 16 || page_tokens > 256 || (page_tokens & (page_tokens - 1))) return DBS_ERR_INVALID_ARG;
+  if ((group != 32 && group != 64 && group != 128) || kv4_padded(head_dim) % group) return DBS_ERR_INVALID_ARG;
+  *bytes = (int64_t)key_heads * kv4_layout(kv4_padded(head_dim), group, page_tokens).head_bytes;
+  return DBS_OK;
+}
+
+dbs_status dbs_kv4_store(const dbs_kv4_cache *a, int32_t tokens, const void *k, int64_t kt, int64_t kh, const void *v, int64_t vt,
+                         int64_t vh, dbs_dtype x_dtype, void *k_out, int64_t kot, int64_t koh, void *v_out, int64_t vot,
+                         int64_t voh, dbs_dtype out_dtype, void *stream) {
+  kv4_view c;
+  dbs_status st;
+  const bool go = view_of(a, tokens, &c, &st);
+  if (st != DBS_OK) return st;
+  if (!dbs_is_vector_dtype(x_dtype) || !dbs_is_vector_dtype(out_dtype)) return DBS_ERR_INVALID_ARG;
+  if ((int64_t)tokens * a->key_heads > DBS_KV4_MAX_ROWS) return DBS_ERR_UNSUPPORTED;
+  if (!go) return DBS_OK;
+  if (!k || !v) return DBS_ERR_INVALID_ARG;
+  const int64_t h = a->key_heads, d = a->head_dim;
+  const dbs_rows in[2] = {rows_of(k, tokens, kt, h, kh, d, x_dtype), rows_of(v, tokens, vt, h, vh, d, x_dtype)};
+  const dbs_rows out[2] = {rows_of(k_out, tokens, kot, h, koh, d, out_dtype), rows_of(v_out, tokens, vot, h, voh, d, out_dtype)};
+  const int64_t ot[2] = {kot, vot}, oh[2] = {koh, voh}, it[2] = {kt, vt}, ih[2] = {kh, vh};
+  const void *const x[2] = {k, v}, *const y[2] = {k_out, v_out};
+  for (int s = 0; s < 2; ++s) {
+    if (meets_pool(in[s], a)) return DBS_ERR_INVALID_ARG;
+    if (!y[s]) continue;
+    if (heads_meet(tokens, ot[s], h, oh[s], d) || meets_pool(out[s], a) || meets_lists(out[s], a)) return DBS_ERR_INVALID_ARG;
+    const bool in_place = x[s] == y[s] && x_dtype == out_dtype && (tokens < 2 || ot[s] == it[s]) && (h < 2 || oh[s] == ih[s]);
+    if (!in_place && dbs_rows_meet(in[s], out[s])) return DBS_ERR_INVALID_ARG;
+    if (dbs_rows_meet(in[1 - s], out[s])) return DBS_ERR_INVALID_ARG;
+  }
+  if (k_out && v_out && dbs_rows_meet(out[0], out[1])) return DBS_ERR_INVALID_ARG;
+  const dbs_rows lists = {(__int128)(uintptr_t)a->pool, 1, 0, 1, 0, (a->pages - 1) * a->page_stride + 1};
+  if (meets_lists(lists, a)) return DBS_ERR_INVALID_ARG;
+  const int padded = kv4_padded(a->head_dim);
+  const int64_t units = a->new_ptr ? (int64_t)tokens / 8 + 2 * (int64_t)a->sequences + 1 : ((int64_t)c.each + 6) / 8 * a->sequences + a->sequences;
+  const kv4_side ks = {k, kt, kh, k_out, kot, koh}, vs = {v, vt, vh, v_out, vot, voh};
+  const auto run = x_dtype == DBS_F32 ? (out_dtype == DBS_F32 ? k_kv4_store<float, float> : k_kv4_store<float, bf16_bits>)
+                                      : (out_dtype == DBS_F32 ? k_kv4_store<bf16_bits, float> : k_kv4_store<bf16_bits, bf16_bits>);
+  hipLaunchKernelGGL(run, dim3((unsigned)units, (unsigned)h), dim3(2 * padded), 0, (hipStream_t)stream, c, a->head_dim, padded, a->group,
+                     ks, vs);
+  return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
+}
+
+dbs_status dbs_kv4_attention_workspace(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, dbs_dtype q_dtype, dbs_dtype out_dtype,
+                                       int32_t window, int32_t sinks, int32_t max_len, int64_t *bytes) {
+  if (!bytes) return DBS_ERR_INVALID_ARG;
+  kv4_view c;
+  bool go;
+  const dbs_status st = check_attention(a, tokens, heads, q_dtype, out_dtype, window, sinks, max_len, &c, &go);
+  if (st != DBS_OK) return st;
+  *bytes = 0;
+  if (go) {
+    const kv4_plan p = plan_of(a, tokens, heads, q_dtype == DBS_F32 || out_dtype == DBS_F32, window, sinks, max_len);
+    *bytes = partial_bytes(a, tokens, heads, p.splits);
+  }
+  return DBS_OK;
+}
+
+dbs_status dbs_kv4_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, const void *q, dbs_dtype q_dtype, int64_t qt,
+                             int64_t qh, void *out, dbs_dtype out_dtype, int64_t ot, int64_t oh, float scale, int32_t window,
+                             int32_t sinks, int32_t max_len, void *workspace, int64_t workspace_bytes, void *stream) {
+  kv4_view c;
+  bool go;
+  const dbs_status st = check_attention(a, tokens, heads, q_dtype, out_dtype, window, sinks, max_len, &c, &go);
+  if (st != DBS_OK) return st;
+  if (!(scale > 0.0f) || !isfinite(scale) || workspace_bytes < 0) return DBS_ERR_INVALID_ARG;
+  if (!go) return DBS_OK;
+  if (!q || !out || (workspace_bytes > 0 && (!workspace || (uintptr_t)workspace % 16))) return DBS_ERR_INVALID_ARG;
+  const dbs_rows in = rows_of(q, tokens, qt, heads, qh, a->head_dim, q_dtype), to = rows_of(out, tokens, ot, heads, oh, a->head_dim, out_dtype);
+  if (heads_meet(tokens, ot, heads, oh, a->head_dim) || dbs_rows_meet(in, to) || meets_pool(to, a) || meets_lists(to, a))
+    return DBS_ERR_INVALID_ARG;
+  const bool wide = q_dtype == DBS_F32 || out_dtype == DBS_F32;
+  kv4_plan p = plan_of(a, tokens, heads, wide, window, sinks, max_len);
+  if (workspace_bytes < partial_bytes(a, tokens, heads, p.splits)) p.splits = 1;  // slower, and right
+  if (p.splits > 1) {
+    const dbs_rows scratch = {(__int128)(uintptr_t)workspace, 1, 0, 1, 0, partial_bytes(a, tokens, heads, p.splits)};
+    if (written_over(in, workspace, (int64_t)scratch.width) || written_over(to, workspace, (int64_t)scratch.width) ||
+        meets_pool(scratch, a) || meets_lists(scratch, a))
+      return DBS_ERR_INVALID_ARG;
+  }
+  if (p.units * a->key_heads > 0x7FFFFF) return DBS_ERR_UNSUPPORTED;  // lanes of a launch stay within 31 bits
+  kv4_attention_args k = {c, heads / a->key_heads, a->key_heads, a->head_dim, a->group, q, q_dtype == DBS_BF16, qt, qh, out,
+                          out_dtype == DBS_BF16, ot, oh, scale * 1.4426950408889634f, window, sinks, p.splits, p.chunk, (float *)workspace};
+  const int padded = kv4_padded(a->head_dim);
+  const auto run = padded == 64 ? kv4_attention_64 : padded == 96 ? kv4_attention_96 : padded == 128 ? kv4_attention_128 :
+                   padded == 192 ? kv4_attention_192 : kv4_attention_256;
+  const dim3 grid((unsigned)(p.units * a->key_heads), (unsigned)p.splits);
+  if (run(k, p.tiles, wide, grid, (hipStream_t)stream) != hipSuccess) return DBS_ERR_DEVICE;
+  if (p.splits > 1) {
+    const dim3 rows((unsigned)(tokens * heads));
+    if (out_dtype == DBS_F32)
+      hipLaunchKernelGGL(k_kv4_combine<float>, rows, dim3(256), 0, (hipStream_t)stream, c, heads, a->head_dim, padded, p.splits,
+                         (const float *)workspace, (float *)out, ot, oh);
+    else
+      hipLaunchKernelGGL(k_kv4_combine<bf16_bits>, rows, dim3(256), 0, (hipStream_t)stream, c, heads, a->head_dim, padded, p.splits,
+                         (const float *)workspace, (bf16_bits *)out, ot, oh);
+    if (DBS_NOTE(hipGetLastError()) != hipSuccess) return DBS_ERR_DEVICE;
+  }
+  return DBS_OK;
+}
+
+}  // extern "C"

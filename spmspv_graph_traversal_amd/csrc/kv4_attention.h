@@ -1,0 +1,506 @@
+// Attention over the cache of 4-bit keys and values (kv4.h) on the matrix cores.
+#pragma once
+
+#include "kv4.h"
+
+namespace kv4 {
+
+typedef kv4_half2 half2_t;
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;
+constexpr float kLow = -3.402823466e38f;  // a maximum before any score
+// Exponentials are 2^(score - base), the base being 6 below the largest score when it was last raised, which is when one is 12 above
+// it: up to 2^12, and 20 bits below the largest one before the half that holds them loses bits.
+constexpr float kBelow = 6.0f, kMost = 12.0f;
+
+DBS_DEV half2_t as_half2(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
+DBS_DEV uint32_t as_bits(half2_t h) { return __builtin_bit_cast(uint32_t, h); }
+
+// constants in registers: from literals the compiler makes two instructions of an "and or"
+struct code_masks {
+  uint32_t low, high, base;
+  DBS_DEV code_masks() : low(0x000F000Fu), high(0x00F000F0u), base(0x64006400u) { asm("" : "+s"(low), "+s"(high), "+v"(base)); }
+};
+
+// The eight codes of a word as s q + b, in pairs of nibbles (0, 4), (1, 5), (2, 6), (3, 7): four bits under the exponent of
+// 1024 are 1024 + q or 1024 + 16 q, exactly, then q, and one rounding of s q + b, which is the definition.  Thirteen
+// instructions.
+DBS_DEV half8_t values_of(uint32_t w, const code_masks &m, const half2_t (&s)[4], const half2_t (&b)[4]) {
+  const uint32_t v = w >> 8;
+  const half2_t lowered = {(_Float16)-1024.0f, (_Float16)-1024.0f}, sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f},
+                lowered16 = {(_Float16)-64.0f, (_Float16)-64.0f};
+  half2_t r[4];
+  r[0] = as_half2((w & m.low) | m.base) + lowered;
+  r[1] = __builtin_elementwise_fma(as_half2((w & m.high) | m.base), sixteenth, lowered16);
+  r[2] = as_half2((v & m.low) | m.base) + lowered;
+  r[3] = __builtin_elementwise_fma(as_half2((v & m.high) | m.base), sixteenth, lowered16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __builtin_elementwise_fma(r[i], s[i], b[i]);
+  half8_t o;
+  __builtin_memcpy(&o, r, 16);
+  return o;
+}
+DBS_DEV half8_t values_of(uint32_t w, const code_masks &m, uint32_t record) {
+  const half2_t sb = as_half2(record), s = {sb.x, sb.x}, b = {sb.y, sb.y};
+  const half2_t ss[4] = {s, s, s, s}, bb[4] = {b, b, b, b};
+  return values_of(w, m, ss, bb);
+}
+
+// Two halves of which either is infinite or NaN.
+DBS_DEV bool not_finite(uint32_t pair) { return (pair & 0x7C00u) == 0x7C00u || (pair & 0x7C000000u) == 0x7C000000u; }
+
+// A block of 32 tokens as a lane holds it.
+template <int NC, int NG>
+struct block {
+  uint32_t k[2][NC], kr[2][NG], v[2 * NC], vr[NG][8];
+};
+
+/*
+ * Mathematics: o_i = sum_j e_ij v_j / sum_j e_ij, e_ij = 2^(scale q_i k_j - m_i), over blocks of 32 tokens with a running
+ * base m_i.  A row is one query head of one token; the rows of a key head (its query heads of all new tokens of a
+ * sequence) read the same keys and values, so they fill the tiles of the matrix instructions together.
+ *
+ * A block's scores are K Q^T, two products of 16 tokens by 16 rows, and its output V^T P^T.  Tokens are dealt to the score
+ * tiles so that the lane which gets the scores of a row's tokens 8 g .. 8 g + 7 is the one that gives them to the second
+ * product: no exchange, no LDS.  Codes become halves in registers (values_of), as exact as the cache's definition.
+ *
+ * The base is raised, and the output scaled, only where a score is 12 above it, so that most blocks need no exchange
+ * between lanes.  Sums of exponentials stay in each lane until the end.
+ *
+ * A workgroup's four waves split rows first (R tiles of 16 each) and, where the rows do not need them all, the tokens; further
+ * splits of the tokens over workgroups are joined by k_kv4_combine.
+ */
+template <int NC, int GC, int R, bool WIDE>
+struct wave_state {
+  static constexpr int NG = NC / GC, NV = 2 * NC, PARTS = WIDE ? 2 : 1, D = 32 * NC;
+  half8_t q[PARTS][R][NC];
+  float scale[R], top[R], sum[R];
+  int position[R];  // of the lane's row, -1 behind the last
+  f32x4 o[R][NV];
+
+  DBS_DEV void scores(const block<NC, NG> &b, const code_masks &m, f32x4 (&s)[2][R]) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[t][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const half8_t k = values_of(b.k[t][c], m, b.kr[t][c / GC]);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) s[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[p][r][c], s[t][r], 0, 0, 0);
+      }
+    }
+  }
+
+  // Scores in units of log2 become exponentials; `seen(r)`: bit e for the lane's token e of eight.
+  template <bool MASKED, class F>
+  DBS_DEV void soften(f32x4 (&s)[2][R], F seen) {
+    bool raise = false;
+    float most[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t see = MASKED ? seen(r) : 0u;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[t][r][e] *= scale[r];
+          if (MASKED && !(see >> (4 * t + e) & 1u)) s[t][r][e] = -INFINITY;
+        }
+      float a = s[0][r][0];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a = fmaxf(a, s[t][r][e]);
+      most[r] = a;
+      raise |= a > top[r] + kMost;
+    }
+    if (__builtin_expect(__any(raise), 0)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float a = fmaxf(most[r] - kBelow, top[r]);
+        a = fmaxf(a, __shfl_xor(a, 16));
+        a = fmaxf(a, __shfl_xor(a, 32));
+        const float f = __builtin_amdgcn_exp2f(top[r] - a);
+        top[r] = a;
+        sum[r] *= f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) o[r][n] *= f;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(s[t][r][e] - top[r]);
+          s[t][r][e] = p;
+          sum[r] += p;
+        }
+    }
+  }
+
+  DBS_DEV void weigh(const block<NC, NG> &b, const code_masks &m, const f32x4 (&s)[2][R]) {
+    half8_t p[PARTS][R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      half2_t h[4], l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[e] = half2_t{(_Float16)s[0][r][e], (_Float16)s[1][r][e]};
+        if (WIDE) l[e] = half2_t{(_Float16)(s[0][r][e] - (float)h[e].x), (_Float16)(s[1][r][e] - (float)h[e].y)};
+      }
+      __builtin_memcpy(&p[0][r], h, 16);
+      if (WIDE) __builtin_memcpy(&p[PARTS - 1][r], l, 16);
+    }
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      half2_t vs[4], vb[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        vs[e] = as_half2(b.vr[n / (2 * GC)][e]);
+        vb[e] = as_half2(b.vr[n / (2 * GC)][4 + e]);
+      }
+      const half8_t v = values_of(b.v[n], m, vs, vb);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) o[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[i][r], o[r][n], 0, 0, 0);
+    }
+  }
+};
+
+template <int NC, int GC, int R, bool WIDE>
+__global__ __launch_bounds__(64 * kWaves, R * NC > 8 ? 1 : 2) void k_kv4_attention(kv4_attention_args a) {
+  typedef wave_state<NC, GC, R, WIDE> state;
+  constexpr int NG = state::NG, NV = state::NV, D = state::D, ROWS = 16 * R * kWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int i = lane & 15, g = lane >> 4;
+  const kv4_view &c = a.cache;
+  const int rep = a.heads_per_key, head = blockIdx.x % a.key_heads;
+  const int64_t unit = blockIdx.x / a.key_heads;
+
+  // the workgroup's rows
+  int b, tile;
+  if (c.new_ptr) {
+    b = kv4_find(c, unit, rep, ROWS, 1);
+    tile = (int)(unit - (int64_t)kv4_new_ptr(c, b) * rep / ROWS - b);
+  } else {
+    const int tiles = (int)(((int64_t)c.each * rep + ROWS - 1) / ROWS);
+    b = (int)(unit / tiles);
+    tile = tiles - 1 - (int)(unit % tiles);  // the longest ones first
+  }
+  const kv4_rows rows = kv4_rows_of(c, b);
+  const int all_rows = rows.count * rep, row0 = tile * ROWS;  // DBS_KV4_MAX_ROWS keeps them within 31 bits
+  if (row0 >= all_rows) return;
+  const int have = min(all_rows - row0, ROWS);
+  const int row_waves = have <= 16 * R ? 1 : have <= 32 * R ? 2 : kWaves;
+  const int token_waves = kWaves / row_waves, part = wave % token_waves;
+  const int wave_row = row0 + wave / token_waves * (16 * R);  // may be behind the last row
+
+  state w;
+  int64_t at_token[R];
+  int at_head[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = wave_row + 16 * r + i;
+    const bool real = row < all_rows;
+    const int t = (real ? row : 0) / rep;
+    w.position[r] = real ? rows.position + t : -1;
+    at_token[r] = rows.first + t;
+    at_head[r] = head * rep + (real ? row : 0) - t * rep;
+    w.top[r] = kLow;
+    w.sum[r] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) w.o[r][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // q as halves, its largest element between 2^14 and 2^15; WIDE: in two parts
+    float x[NC][8], most = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int channel = 32 * k + 8 * g;
+      const bool in = real && channel < a.dim;
+      if (a.q_bf16) {
+        uint16_t h[8] = {};
+        if (in) __builtin_memcpy(h, (const bf16_bits *)a.q + at_token[r] * a.qt + at_head[r] * a.qh + channel, 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] = bf16_to_f32(h[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] = 0.0f;
+        if (in) __builtin_memcpy(x[k], (const float *)a.q + at_token[r] * a.qt + at_head[r] * a.qh + channel, 32);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[k][e]));
+    }
+    most = fmaxf(most, __shfl_xor(most, 16));
+    most = fmaxf(most, __shfl_xor(most, 32));
+    const int up = most > 0.0f && most < INFINITY ? 14 - ilogbf(most) : 0;
+    w.scale[r] = ldexpf(a.scale, -up);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      half8_t h, l;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int from = e / 2 + e % 2 * 4;  // the order of values_of
+        const float v = ldexpf(x[k][from], up);
+        h[e] = (_Float16)v;
+        l[e] = (_Float16)(v - (float)h[e]);
+      }
+      w.q[0][r][k] = h;
+      if (WIDE) w.q[state::PARTS - 1][r][k] = l;
+    }
+  }
+
+  // the tokens that the wave's rows see: those below `end` from `start` on, and of the first ones `sink_blocks` blocks
+  const int first_token = wave_row / rep, last_token = (min(all_rows, wave_row + 16 * R) - 1) / rep;
+  const int low = rows.position + first_token, high = rows.position + last_token;  // positions of the first and last row
+  const int end = wave_row < all_rows ? max(high + 1, 0) : 0;
+  int start = 0, sink_blocks = 0;
+  if (a.window) {
+    start = max(low - a.window + 1, 0) & ~(KV4_BLOCK - 1);
+    sink_blocks = (min(a.sinks, end) + KV4_BLOCK - 1) / KV4_BLOCK;
+    if (sink_blocks * KV4_BLOCK >= start) start = sink_blocks = 0;
+  }
+  const int blocks = sink_blocks + (end > start ? (end - start + KV4_BLOCK - 1) / KV4_BLOCK : 0);
+  int next = part, stop = blocks;
+  if (a.splits > 1) {
+    const int split = blockIdx.y;
+    next = (int)min((int64_t)split * a.chunk, (int64_t)blocks) + part;
+    if (split + 1 < a.splits) stop = (int)min((int64_t)(split + 1) * a.chunk, (int64_t)blocks);
+  }
+
+  const kv4_layout lay(D, 32 * GC, 1 << c.page_shift);
+  const int64_t head_offset = (int64_t)head * lay.head_bytes;
+  const code_masks masks;
+  const int page_mask = (1 << c.page_shift) - 1;
+
+  auto token_of = [&](int n) { return n < sink_blocks ? n * KV4_BLOCK : start + (n - sink_blocks) * KV4_BLOCK; };
+  // the pages of the block's two halves of 16 tokens
+  struct place {
+    const uint8_t *page[2];
+    int token;
+  };
+  auto find = [&](int n) {
+    place p;
+    p.token = token_of(n);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) p.page[h] = p.token + 16 * h < end ? kv4_page(c, b, p.token + 16 * h, head_offset) : nullptr;
+    return p;
+  };
+  auto load = [&](const place &p, block<NC, NG> &x) {
+    // a half without a page reads the pool's first, and nobody sees what it read
+    const uint8_t *lo = p.page[0] ? p.page[0] : c.pool + head_offset, *hi = p.page[1] ? p.page[1] : c.pool + head_offset;
+    const int lo_at = p.token & page_mask, hi_at = (p.token + 16) & page_mask;
+    {
+      const bool up = i >= 8;
+      const uint8_t *base = up ? hi : lo;
+      const int at = (up ? hi_at : lo_at) + 8 * ((i >> 2) & 1) + (i & 3);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        __builtin_memcpy(x.k[t], __builtin_assume_aligned(base + (at + 4 * t) * (D / 2) + g * (4 * NC), NC == 3 ? 4 : NC % 4 ? 8 : 16), 4 * NC);
+        __builtin_memcpy(x.kr[t], __builtin_assume_aligned(base + lay.key_records + (at + 4 * t) * (4 * NG), NG % 4 ? NG % 2 ? 4 : 8 : 16), 4 * NG);
+      }
+    }
+    {
+      const bool up = g >= 2;
+      const uint8_t *base = up ? hi : lo;
+      const int at = ((up ? hi_at : lo_at) >> 3) + (g & 1);
+      __builtin_memcpy(x.v, __builtin_assume_aligned(base + lay.value_codes + at * (4 * D) + i * (8 * NC), NC % 2 ? 8 : 16), 8 * NC);
+      __builtin_memcpy(x.vr, __builtin_assume_aligned(base + lay.value_records + at * (32 * NG), 16), 32 * NG);
+    }
+  };
+
+  auto attend = [&](const place &p, block<NC, NG> &x) {
+    f32x4 s[2][R];
+    w.scores(x, masks, s);
+    const int j = p.token;
+    const bool whole = p.page[0] && p.page[1] && j + KV4_BLOCK - 1 <= low &&
+                       (!a.window || j > high - a.window || j + KV4_BLOCK <= a.sinks);
+    if (__builtin_expect(whole, 1)) {
+      w.template soften<false>(s, [](int) { return 0u; });
+    } else {
+      // bit t: the row at `position` sees token j + t
+      auto seen = [&](int position) {
+        uint32_t see = position < j ? 0u : position - j >= 31 ? ~0u : (2u << (position - j)) - 1u;
+        if (a.window) {
+          const int from = position - a.window + 1 - j, sinks = a.sinks - j;  // from bit `from` on, or below bit `sinks`
+          uint32_t in = from <= 0 ? ~0u : from >= 32 ? 0u : ~((1u << from) - 1u);
+          in |= sinks <= 0 ? 0u : sinks >= 32 ? ~0u : (1u << sinks) - 1u;
+          see &= in;
+        }
+        if (!p.page[0]) see &= 0xFFFF0000u;
+        if (!p.page[1]) see &= 0x0000FFFFu;
+        return see;
+      };
+      uint32_t mine[R], any = 0u;
+#pragma unroll
+      for (int r = 0; r < R; ++r) any |= mine[r] = seen(w.position[r]);
+      for (int o = 1; o < 16; o <<= 1) any |= (uint32_t)__shfl_xor((int)any, o);
+      w.template soften<true>(s, [&](int r) { return mine[r] >> (8 * g); });
+      // Nothing times a value that is not finite would be NaN: values that no row sees become 0, and one that is not finite and
+      // that some rows see is added to those alone.
+      uint32_t bad[NG], some = 0u;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        uint32_t mask = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t &sc = x.vr[n][e], &of = x.vr[n][4 + e];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int bit = 8 * g + e + 4 * h;
+            const uint32_t half = h ? 0xFFFF0000u : 0x0000FFFFu;
+            const bool see = any >> bit & 1u, wrong = not_finite(sc & half) || not_finite(of & half);
+            if (see && wrong) mask |= 1u << bit;
+            if (!see || wrong) sc &= ~half, of &= ~half;
+          }
+        }
+        mask |= (uint32_t)__shfl_xor((int)mask, 16);
+        mask |= (uint32_t)__shfl_xor((int)mask, 32);
+        bad[n] = mask;
+        some |= mask;
+      }
+      if (__any(some != 0u)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+            if (bad[n / (2 * GC)] & mine[r]) w.o[r][n] += NAN;
+      }
+    }
+    w.weigh(x, masks, s);
+  };
+
+  if (next < stop) {
+    block<NC, NG> x, y;
+    place p = find(next), n;
+    load(p, x);
+    for (;;) {
+      next += token_waves;
+      const bool more = next < stop;
+      if (more) {
+        n = find(next);
+        load(n, y);
+      }
+      attend(p, x);
+      if (!more) break;
+      next += token_waves;
+      const bool again = next < stop;
+      if (again) {
+        p = find(next);
+        load(p, x);
+      }
+      attend(n, y);
+      if (!again) break;
+    }
+  }
+
+  // sums over the lanes of a row; then the waves that split its tokens
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    w.sum[r] += __shfl_xor(w.sum[r], 16);
+    w.sum[r] += __shfl_xor(w.sum[r], 32);
+  }
+  if (token_waves > 1) {
+    __shared__ float shared[kWaves - 1][4 * NV + 2][64];
+    // writers, in the order of their waves: three of one row part, or one of each of two
+    const int slot = token_waves == kWaves ? part - 1 : wave >> 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (part) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) shared[slot][4 * n + e][lane] = w.o[r][n][e];
+        shared[slot][4 * NV][lane] = w.top[r];
+        shared[slot][4 * NV + 1][lane] = w.sum[r];
+      }
+      __syncthreads();
+      if (!part) {
+        const int from = token_waves == kWaves ? 0 : wave >> 1, count = token_waves - 1;
+        float top = w.top[r];
+        for (int k = 0; k < count; ++k) top = fmaxf(top, shared[from + k][4 * NV][lane]);
+        const float f = __builtin_amdgcn_exp2f(w.top[r] - top);
+        w.sum[r] *= f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) w.o[r][n] *= f;
+        for (int k = 0; k < count; ++k) {
+          const float h = __builtin_amdgcn_exp2f(shared[from + k][4 * NV][lane] - top);
+          w.sum[r] += h * shared[from + k][4 * NV + 1][lane];
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w.o[r][n][e] += h * shared[from + k][4 * n + e][lane];
+        }
+        w.top[r] = top;
+      }
+      __syncthreads();
+    }
+    if (part) return;
+  }
+
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (wave_row + 16 * r + i >= all_rows) continue;
+    if (a.splits > 1) {
+      const int64_t heads = (int64_t)a.key_heads * rep;
+      float *to = a.partial + ((blockIdx.y * (int64_t)c.tokens + at_token[r]) * heads + at_head[r]) * (D + 2);
+      if (w.sum[r] != 0.0f) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) __builtin_memcpy(to + 16 * n + 4 * g, &w.o[r][n], 16);
+      }
+      if (g == 0) to[D] = w.top[r], to[D + 1] = w.sum[r];
+      continue;
+    }
+    // a row that sees nothing is 0; a sum that is not a number stays one
+    const float f = w.sum[r] == 0.0f ? 0.0f : 1.0f / w.sum[r];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int channel = 16 * n + 4 * g;
+      if (channel >= a.dim) continue;
+      if (a.out_bf16) {
+        bf16_bits v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = dbs_value<bf16_bits>::of(w.o[r][n][e] * f);
+        __builtin_memcpy((bf16_bits *)a.out + at_token[r] * a.ot + at_head[r] * a.oh + channel, v, 8);
+      } else {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = w.o[r][n][e] * f;
+        __builtin_memcpy((float *)a.out + at_token[r] * a.ot + at_head[r] * a.oh + channel, v, 16);
+      }
+    }
+  }
+}
+
+template <int NC, int GC, int R, bool WIDE>
+hipError_t launch(const kv4_attention_args &a, dim3 grid, hipStream_t s) {
+  hipLaunchKernelGGL((k_kv4_attention<NC, GC, R, WIDE>), grid, dim3(64 * kWaves), 0, s, a);
+  return DBS_NOTE(hipGetLastError());
+}
+
+template <int NC, int GC>
+hipError_t launch(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s) {
+  if constexpr (NC % GC == 0) {
+    if (wide) return tiles == 1 ? launch<NC, GC, 1, true>(a, grid, s) : launch<NC, GC, 2, true>(a, grid, s);
+    if (tiles == 1) return launch<NC, GC, 1, false>(a, grid, s);
+    if constexpr (NC <= 4)
+      if (tiles == 4) return launch<NC, GC, 4, false>(a, grid, s);
+    return launch<NC, GC, 2, false>(a, grid, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <int NC>
+hipError_t launch(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s) {
+  if (a.group == 32) return launch<NC, 1>(a, tiles, wide, grid, s);
+  if (a.group == 64) return launch<NC, 2>(a, tiles, wide, grid, s);
+  return launch<NC, 4>(a, tiles, wide, grid, s);
+}
+
+}  // namespace kv4

@@ -1,18 +1,9 @@
 // Rotary positions (dbs_rope) and their frequencies (dbs_rope_frequencies).
 #include <math.h>
 
-#include "values.h"
+#include "rope.h"
 
 namespace {
-
-// past the caches: 8192 tokens of 40 heads of 128 bf16 30.6 us against 35.0
-template <class T, int W>
-DBS_DEV void write(T *p, const T (&v)[W]) {
-  typedef T at_any __attribute__((ext_vector_type(W), aligned(sizeof(T))));
-  at_any w;
-  __builtin_memcpy(&w, v, sizeof v);
-  __builtin_nontemporal_store(w, (at_any *)p);
-}
 
 /*
  * Mathematics: a pair (a, b) of a head turns by p = position * freq[i].  Cosine and sine depend on the token and the pair
@@ -61,21 +52,15 @@ struct rope_unit {
         (ka < W ? oa[ka % W] : ob[ka % W]) = dbs_value<Y>::of(ra);
         (kb < W ? oa[kb % W] : ob[kb % W]) = dbs_value<Y>::of(rb);
       }
-      write(p + (INTERLEAVED ? 2 * W * i : W * i), oa);
-      write(p + (INTERLEAVED ? 2 * W * i + W : half + W * i), ob);
+      rope_write(p + (INTERLEAVED ? 2 * W * i : W * i), oa);
+      rope_write(p + (INTERLEAVED ? 2 * W * i + W : half + W * i), ob);
     } else {
 #pragma unroll
       for (int e = 0; e < W; ++e) oa[e] = dbs_value<Y>::of(dbs_value<X>::load(&a[e]));
-      write(p + 2 * half + W * (i - turned), oa);
+      rope_write(p + 2 * half + W * (i - turned), oa);
     }
   }
 };
-
-// units of a head
-template <int W, bool INTERLEAVED>
-__host__ __device__ inline int rope_units(int head_dim, int rot_dim) {
-  return INTERLEAVED && W > 1 ? head_dim / (2 * W) : rot_dim / 2 / W + (head_dim - rot_dim) / W;
-}
 
 template <class X, class Y, int W, bool INTERLEAVED>
 __global__ __launch_bounds__(512) void k_rope(int heads, int per, int head_dim, int rot_dim,
@@ -93,12 +78,7 @@ __global__ __launch_bounds__(512) void k_rope(int heads, int per, int head_dim, 
   rope_unit<X, Y, W, INTERLEAVED> now;
   int u = threadIdx.x;
   if (u < all) now.load(x, xh, u, units, turned, half);
-  for (int i = threadIdx.x; i < half; i += blockDim.x) {
-    const double turns = (double)p * freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    float s, c;
-    sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-    turn[i] = make_float2(scale * c, scale * direction * s);
-  }
+  for (int i = threadIdx.x; i < half; i += blockDim.x) turn[i] = rope_turn(p, freq[i], scale, direction);
   dbs_barrier_lds();
   if (u < all) now.store(out, oh, turn, turned, half);
   for (u += blockDim.x; u < all; u += blockDim.x) {
@@ -161,13 +141,6 @@ dbs_status launch_rope(const rope_args &r, hipStream_t s) {
   return launch_rope<X, Y, 1, false>(r, s);
 }
 
-// whether rows of `width` elements at i * si + j * sj are disjoint because each i's rows end before the next i's begin
-bool apart(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t width) {
-  typedef __int128 wide;
-  const wide i = si < 0 ? -(wide)si : si, j = sj < 0 ? -(wide)sj : sj;
-  return (nj < 2 || j >= width) && (ni < 2 || i >= (nj - 1) * j + width);
-}
-
 }  // namespace
 
 extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, int32_t rot_dim, dbs_rope_layout layout,
@@ -183,7 +156,7 @@ extern "C" dbs_status dbs_rope(int32_t tokens, int32_t heads, int32_t head_dim, 
   if (tokens == 0 || heads == 0) return DBS_OK;
   if (!pos || (rot_dim > 0 && !freq) || !x || !out) return DBS_ERR_INVALID_ARG;
   // two heads of the output may not share an element, and an in-place call reads what it writes
-  if (!apart(tokens, ot, heads, oh, head_dim) && !apart(heads, oh, tokens, ot, head_dim)) return DBS_ERR_INVALID_ARG;
+  if (!dbs_rows_apart(tokens, ot, heads, oh, head_dim) && !dbs_rows_apart(heads, oh, tokens, ot, head_dim)) return DBS_ERR_INVALID_ARG;
   const bool in_place = x == out && x_dtype == out_dtype && (tokens < 2 || xt == ot) && (heads < 2 || xh == oh);
   const __int128 xs = dbs_vector_size(x_dtype), os = dbs_vector_size(out_dtype);
   const dbs_rows from = {(__int128)(uintptr_t)x, tokens, xt * xs, heads, xh * xs, head_dim * xs};

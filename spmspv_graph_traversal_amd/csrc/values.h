@@ -83,6 +83,13 @@ inline bool dbs_rows_meet(dbs_rows a, dbs_rows b) {
   return a.si != b.si || a.sj != b.sj || dbs_like_rows_meet(a, b);  // the last, exact, takes longest: in steps over i or j
 }
 
+// whether rows of `width` elements at i * si + j * sj are disjoint because each i's rows end before the next i's begin
+inline bool dbs_rows_apart(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t width) {
+  typedef __int128 wide;
+  const wide i = si < 0 ? -(wide)si : si, j = sj < 0 ? -(wide)sj : sj;
+  return (nj < 2 || j >= width) && (ni < 2 || i >= (nj - 1) * j + width);
+}
+
 // a barrier that waits for LDS only, not for loads from memory in flight
 DBS_DEV void dbs_barrier_lds() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
