@@ -90,6 +90,7 @@ DBS_DEV uint8_t *kv4_page(const kv4_view &c, int b, int token, int64_t head_offs
 // the attention kernels (kv4_attention.h), one file for each padded head size
 struct kv4_attention_args {
   kv4_view cache;
+  int device;  // the current one
   int heads_per_key, key_heads, dim, group;
   const void *q;
   int q_bf16;
@@ -103,7 +104,7 @@ struct kv4_attention_args {
   float *partial;     // [splits][tokens][heads][d + 2] where splits > 1: the unnormalised row, its maximum and its sum
 };
 
-// tiles: 16-row tiles of a wave; wide: q and p in two parts
+// tiles: 16-row tiles of a wave, 4: the kernel for many rows (kv4_prompt.h); wide: q and p in two parts
 hipError_t kv4_attention_64(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);
 hipError_t kv4_attention_96(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);
 hipError_t kv4_attention_128(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);

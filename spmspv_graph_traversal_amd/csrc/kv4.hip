@@ -229,13 +229,12 @@ struct kv4_plan {
   int64_t units;
 };
 
-kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wide, int32_t window, int32_t sinks, int32_t max_len) {
+kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, int32_t window, int32_t sinks, int32_t max_len) {
   kv4_plan p;
   const int rep = heads / a->key_heads;
   const int64_t rows = (int64_t)tokens * rep, each = (rows + a->sequences - 1) / a->sequences;
-  const int d = kv4_padded(a->head_dim);
-  p.tiles = each <= 16 ? 1 : each <= 32 || wide || d > 128 ? 2 : 4;
-  const int per = 16 * p.tiles * 4;
+  p.tiles = each <= 16 ? 1 : each <= 32 ? 2 : 4;
+  const int per = p.tiles == 4 ? 128 : 16 * p.tiles * 4;
   p.units = a->new_ptr ? rows / per + a->sequences : (tokens / a->sequences * (int64_t)rep + per - 1) / per * a->sequences;
   int64_t slots = (int64_t)a->table_pages * a->page_tokens;
   if (max_len > 0 && max_len < slots) slots = max_len;
@@ -333,7 +332,7 @@ dbs_status dbs_kv4_attention_workspace(const dbs_kv4_cache *a, int32_t tokens, i
   if (st != DBS_OK) return st;
   *bytes = 0;
   if (go) {
-    const kv4_plan p = plan_of(a, tokens, heads, q_dtype == DBS_F32 || out_dtype == DBS_F32, window, sinks, max_len);
+    const kv4_plan p = plan_of(a, tokens, heads, window, sinks, max_len);
     *bytes = partial_bytes(a, tokens, heads, p.splits);
   }
   return DBS_OK;
@@ -353,7 +352,7 @@ dbs_status dbs_kv4_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t hea
   if (heads_meet(tokens, ot, heads, oh, a->head_dim) || dbs_rows_meet(in, to) || meets_pool(to, a) || meets_lists(to, a))
     return DBS_ERR_INVALID_ARG;
   const bool wide = q_dtype == DBS_F32 || out_dtype == DBS_F32;
-  kv4_plan p = plan_of(a, tokens, heads, wide, window, sinks, max_len);
+  kv4_plan p = plan_of(a, tokens, heads, window, sinks, max_len);
   if (workspace_bytes < partial_bytes(a, tokens, heads, p.splits)) p.splits = 1;  // slower, and right
   if (p.splits > 1) {
     const dbs_rows scratch = {(__int128)(uintptr_t)workspace, 1, 0, 1, 0, partial_bytes(a, tokens, heads, p.splits)};
@@ -362,7 +361,9 @@ dbs_status dbs_kv4_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t hea
       return DBS_ERR_INVALID_ARG;
   }
   if (p.units * a->key_heads > 0x7FFFFF) return DBS_ERR_UNSUPPORTED;  // lanes of a launch stay within 31 bits
-  kv4_attention_args k = {c, heads / a->key_heads, a->key_heads, a->head_dim, a->group, q, q_dtype == DBS_BF16, qt, qh, out,
+  int device = -1;
+  if (DBS_NOTE(hipGetDevice(&device)) != hipSuccess) return DBS_ERR_DEVICE;
+  kv4_attention_args k = {c, device, heads / a->key_heads, a->key_heads, a->head_dim, a->group, q, q_dtype == DBS_BF16, qt, qh, out,
                           out_dtype == DBS_BF16, ot, oh, scale * 1.4426950408889634f, window, sinks, p.splits, p.chunk, (float *)workspace};
   const int padded = kv4_padded(a->head_dim);
   const auto run = padded == 64 ? kv4_attention_64 : padded == 96 ? kv4_attention_96 : padded == 128 ? kv4_attention_128 :

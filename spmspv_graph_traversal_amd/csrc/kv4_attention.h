@@ -48,6 +48,9 @@ DBS_DEV half8_t values_of(uint32_t w, const code_masks &m, uint32_t record) {
   return values_of(w, m, ss, bb);
 }
 
+// sum + h.x + h.y in fp32.  Sums are of the halves that weigh the values, so that their rounding is no error of a row's total.
+DBS_DEV float sum_of(half2_t h, float sum) { return __builtin_amdgcn_fdot2(h, half2_t{(_Float16)1.0f, (_Float16)1.0f}, sum, false); }
+
 // Two halves of which either is infinite or NaN.
 DBS_DEV bool not_finite(uint32_t pair) { return (pair & 0x7C00u) == 0x7C00u || (pair & 0x7C000000u) == 0x7C000000u; }
 
@@ -99,6 +102,7 @@ struct wave_state {
   // Scores in units of log2 become exponentials; `seen(r)`: bit e for the lane's token e of eight.
   template <bool MASKED, class F>
   DBS_DEV void soften(f32x4 (&s)[2][R], F seen) {
+#pragma clang fp contract(off)  // the largest score less the base is 6, exactly
     bool raise = false;
     float most[R];
 #pragma unroll
@@ -137,11 +141,7 @@ struct wave_state {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(s[t][r][e] - top[r]);
-          s[t][r][e] = p;
-          sum[r] += p;
-        }
+        for (int e = 0; e < 4; ++e) s[t][r][e] = __builtin_amdgcn_exp2f(s[t][r][e] - top[r]);
     }
   }
 
@@ -153,7 +153,11 @@ struct wave_state {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         h[e] = half2_t{(_Float16)s[0][r][e], (_Float16)s[1][r][e]};
-        if (WIDE) l[e] = half2_t{(_Float16)(s[0][r][e] - (float)h[e].x), (_Float16)(s[1][r][e] - (float)h[e].y)};
+        sum[r] = sum_of(h[e], sum[r]);
+        if (WIDE) {
+          l[e] = half2_t{(_Float16)(s[0][r][e] - (float)h[e].x), (_Float16)(s[1][r][e] - (float)h[e].y)};
+          sum[r] = sum_of(l[e], sum[r]);
+        }
       }
       __builtin_memcpy(&p[0][r], h, 16);
       if (WIDE) __builtin_memcpy(&p[PARTS - 1][r], l, 16);
@@ -482,25 +486,6 @@ template <int NC, int GC, int R, bool WIDE>
 hipError_t launch(const kv4_attention_args &a, dim3 grid, hipStream_t s) {
   hipLaunchKernelGGL((k_kv4_attention<NC, GC, R, WIDE>), grid, dim3(64 * kWaves), 0, s, a);
   return DBS_NOTE(hipGetLastError());
-}
-
-template <int NC, int GC>
-hipError_t launch(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s) {
-  if constexpr (NC % GC == 0) {
-    if (wide) return tiles == 1 ? launch<NC, GC, 1, true>(a, grid, s) : launch<NC, GC, 2, true>(a, grid, s);
-    if (tiles == 1) return launch<NC, GC, 1, false>(a, grid, s);
-    if constexpr (NC <= 4)
-      if (tiles == 4) return launch<NC, GC, 4, false>(a, grid, s);
-    return launch<NC, GC, 2, false>(a, grid, s);
-  }
-  return hipErrorInvalidValue;
-}
-
-template <int NC>
-hipError_t launch(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s) {
-  if (a.group == 32) return launch<NC, 1>(a, tiles, wide, grid, s);
-  if (a.group == 64) return launch<NC, 2>(a, tiles, wide, grid, s);
-  return launch<NC, 4>(a, tiles, wide, grid, s);
 }
 
 }  // namespace kv4
