@@ -99,29 +99,20 @@ struct wave_state {
     }
   }
 
-  // Scores in units of log2 become exponentials; `seen(r)`: bit e for the lane's token e of eight.
-  template <bool MASKED, class F>
-  DBS_DEV void soften(f32x4 (&s)[2][R], F seen) {
-#pragma clang fp contract(off)  // the largest score less the base is 6, exactly
+  // Scores become exponentials.
+  DBS_DEV void soften(f32x4 (&s)[2][R]) {
+#pragma clang fp contract(off)  // the largest score less the base is 6, exactly, where WIDE
     bool raise = false;
     float most[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint32_t see = MASKED ? seen(r) : 0u;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[t][r][e] *= scale[r];
-          if (MASKED && !(see >> (4 * t + e) & 1u)) s[t][r][e] = -INFINITY;
-        }
       float a = s[0][r][0];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) a = fmaxf(a, s[t][r][e]);
-      most[r] = a;
-      raise |= a > top[r] + kMost;
+      most[r] = a * scale[r];
+      raise |= most[r] > top[r] + kMost;
     }
     if (__builtin_expect(__any(raise), 0)) {
 #pragma unroll
@@ -137,12 +128,14 @@ struct wave_state {
       }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][r][e] = __builtin_amdgcn_exp2f(s[t][r][e] - top[r]);
-    }
+        for (int e = 0; e < 4; ++e) {
+          const float v = s[t][r][e];
+          s[t][r][e] = __builtin_amdgcn_exp2f(WIDE ? v * scale[r] - top[r] : __builtin_fmaf(v, scale[r], -top[r]));
+        }
   }
 
   DBS_DEV void weigh(const block<NC, NG> &b, const code_masks &m, const f32x4 (&s)[2][R]) {
@@ -180,7 +173,7 @@ struct wave_state {
 };
 
 template <int NC, int GC, int R, bool WIDE>
-__global__ __launch_bounds__(64 * kWaves, R * NC > 8 ? 1 : 2) void k_kv4_attention(kv4_attention_args a) {
+__global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R * NC * (WIDE ? 2 : 1) <= 8 ? 2 : 1) void k_kv4_attention(kv4_attention_args a) {
   typedef wave_state<NC, GC, R, WIDE> state;
   constexpr int NG = state::NG, NV = state::NV, D = state::D, ROWS = 16 * R * kWaves;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -284,123 +277,146 @@ __global__ __launch_bounds__(64 * kWaves, R * NC > 8 ? 1 : 2) void k_kv4_attenti
   const int page_mask = (1 << c.page_shift) - 1;
 
   auto token_of = [&](int n) { return n < sink_blocks ? n * KV4_BLOCK : start + (n - sink_blocks) * KV4_BLOCK; };
-  // the pages of the block's two halves of 16 tokens
+  // the pages of the block's two halves of 16 tokens, -1 where there is none
   struct place {
-    const uint8_t *page[2];
-    int token;
+    int token, page[2];
   };
+  const int32_t *const table = c.table + b * c.ldtable;
   auto find = [&](int n) {
     place p;
     p.token = token_of(n);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) p.page[h] = p.token + 16 * h < end ? kv4_page(c, b, p.token + 16 * h, head_offset) : nullptr;
+    for (int h = 0; h < 2; ++h) {
+      const int at = (p.token + 16 * h) >> c.page_shift;
+      const int page = p.token + 16 * h < end && at < c.width ? table[at] : -1;
+      p.page[h] = (unsigned)page < (unsigned)c.pages ? page : -1;
+    }
     return p;
   };
-  auto load = [&](const place &p, block<NC, NG> &x) {
-    // a half without a page reads the pool's first, and nobody sees what it read
-    const uint8_t *lo = p.page[0] ? p.page[0] : c.pool + head_offset, *hi = p.page[1] ? p.page[1] : c.pool + head_offset;
-    const int lo_at = p.token & page_mask, hi_at = (p.token + 16) & page_mask;
-    {
-      const bool up = i >= 8;
-      const uint8_t *base = up ? hi : lo;
-      const int at = (up ? hi_at : lo_at) + 8 * ((i >> 2) & 1) + (i & 3);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        __builtin_memcpy(x.k[t], __builtin_assume_aligned(base + (at + 4 * t) * (D / 2) + g * (4 * NC), NC == 3 ? 4 : NC % 4 ? 8 : 16), 4 * NC);
-        __builtin_memcpy(x.kr[t], __builtin_assume_aligned(base + lay.key_records + (at + 4 * t) * (4 * NG), NG % 4 ? NG % 2 ? 4 : 8 : 16), 4 * NG);
-      }
+  // A half without a page reads the pool's first, and nobody sees what it read.  A lane's rows of a half: of its key tokens (4 apart)
+  // and of its eight value tokens; where pages have 32 tokens and more both halves are of one page, and addresses one base and
+  // a lane's constant.
+  const int k_row = 8 * ((i >> 2) & 1) + (i & 3), k_half = i >> 3, v_half = g >> 1;
+  const bool one_page = c.page_shift >= 5;
+  auto base_of = [&](const place &p, int h) { return c.pool + (int64_t)max(p.page[h], 0) * c.page_stride + head_offset; };
+  auto row_of = [&](const place &p, int h) { return (p.token + 16 * h) & page_mask; };
+  auto load_keys = [&](const place &p, block<NC, NG> &x) {
+    const uint8_t *codes, *records;
+    if (one_page) {
+      const uint8_t *const base = base_of(p, 0);
+      codes = base + row_of(p, 0) * (D / 2) + (uint32_t)((16 * k_half + k_row) * (D / 2) + g * (4 * NC));
+      records = base + lay.key_records + row_of(p, 0) * (4 * NG) + (uint32_t)((16 * k_half + k_row) * (4 * NG));
+    } else {
+      const uint8_t *const base = k_half ? base_of(p, 1) : base_of(p, 0);
+      const int row = (k_half ? row_of(p, 1) : row_of(p, 0)) + k_row;
+      codes = base + row * (D / 2) + g * (4 * NC);
+      records = base + lay.key_records + row * (4 * NG);
     }
-    {
-      const bool up = g >= 2;
-      const uint8_t *base = up ? hi : lo;
-      const int at = ((up ? hi_at : lo_at) >> 3) + (g & 1);
-      __builtin_memcpy(x.v, __builtin_assume_aligned(base + lay.value_codes + at * (4 * D) + i * (8 * NC), NC % 2 ? 8 : 16), 8 * NC);
-      __builtin_memcpy(x.vr, __builtin_assume_aligned(base + lay.value_records + at * (32 * NG), 16), 32 * NG);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      __builtin_memcpy(x.k[t], __builtin_assume_aligned(codes + t * (2 * D), NC == 3 ? 4 : NC % 4 ? 8 : 16), 4 * NC);
+      __builtin_memcpy(x.kr[t], __builtin_assume_aligned(records + t * (16 * NG), NG % 4 ? NG % 2 ? 4 : 8 : 16), 4 * NG);
     }
   };
+  auto load_values = [&](const place &p, block<NC, NG> &x) {
+    const uint8_t *codes, *records;
+    if (one_page) {
+      const uint8_t *const base = base_of(p, 0);
+      codes = base + lay.value_codes + row_of(p, 0) * (D / 2) + (uint32_t)(g * (4 * D) + i * (8 * NC));
+      records = base + lay.value_records + row_of(p, 0) * (4 * NG) + (uint32_t)(g * (32 * NG));
+    } else {
+      const uint8_t *const base = v_half ? base_of(p, 1) : base_of(p, 0);
+      const int eight = ((v_half ? row_of(p, 1) : row_of(p, 0)) >> 3) + (g & 1);
+      codes = base + lay.value_codes + eight * (4 * D) + i * (8 * NC);
+      records = base + lay.value_records + eight * (32 * NG);
+    }
+    __builtin_memcpy(x.v, __builtin_assume_aligned(codes, NC % 2 ? 8 : 16), 8 * NC);
+    __builtin_memcpy(x.vr, __builtin_assume_aligned(records, 16), 32 * NG);
+  };
 
-  auto attend = [&](const place &p, block<NC, NG> &x) {
+  block<NC, NG> x;
+  place p = {}, ahead = {};
+  // a block: its scores, the next one's keys on their way, its weights, its values, and the next one's
+  auto attend = [&](bool more) {
     f32x4 s[2][R];
     w.scores(x, masks, s);
+    if (more) load_keys(ahead, x);
     const int j = p.token;
-    const bool whole = p.page[0] && p.page[1] && j + KV4_BLOCK - 1 <= low &&
+    const bool whole = p.page[0] >= 0 && p.page[1] >= 0 && j + KV4_BLOCK - 1 <= low &&
                        (!a.window || j > high - a.window || j + KV4_BLOCK <= a.sinks);
-    if (__builtin_expect(whole, 1)) {
-      w.template soften<false>(s, [](int) { return 0u; });
-    } else {
-      // bit t: the row at `position` sees token j + t
-      auto seen = [&](int position) {
-        uint32_t see = position < j ? 0u : position - j >= 31 ? ~0u : (2u << (position - j)) - 1u;
-        if (a.window) {
-          const int from = position - a.window + 1 - j, sinks = a.sinks - j;  // from bit `from` on, or below bit `sinks`
-          uint32_t in = from <= 0 ? ~0u : from >= 32 ? 0u : ~((1u << from) - 1u);
-          in |= sinks <= 0 ? 0u : sinks >= 32 ? ~0u : (1u << sinks) - 1u;
-          see &= in;
-        }
-        if (!p.page[0]) see &= 0xFFFF0000u;
-        if (!p.page[1]) see &= 0x0000FFFFu;
-        return see;
-      };
-      uint32_t mine[R], any = 0u;
+    // bit t: the row at `position` sees token j + t
+    auto seen = [&](int position) {
+      uint32_t see = position < j ? 0u : position - j >= 31 ? ~0u : (2u << (position - j)) - 1u;
+      if (a.window) {
+        const int from = position - a.window + 1 - j, sinks = a.sinks - j;  // from bit `from` on, or below bit `sinks`
+        uint32_t in = from <= 0 ? ~0u : from >= 32 ? 0u : ~((1u << from) - 1u);
+        in |= sinks <= 0 ? 0u : sinks >= 32 ? ~0u : (1u << sinks) - 1u;
+        see &= in;
+      }
+      if (p.page[0] < 0) see &= 0xFFFF0000u;
+      if (p.page[1] < 0) see &= 0x0000FFFFu;
+      return see;
+    };
+    uint32_t bad[NG], some = 0u;  // the same in all lanes
+    if (__builtin_expect(!whole, 0)) {
+      uint32_t any = 0u;
 #pragma unroll
-      for (int r = 0; r < R; ++r) any |= mine[r] = seen(w.position[r]);
+      for (int r = 0; r < R; ++r) {
+        const uint32_t see = seen(w.position[r]);
+        any |= see;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(see >> (8 * g) >> (4 * t + e) & 1u)) s[t][r][e] = -INFINITY;
+      }
       for (int o = 1; o < 16; o <<= 1) any |= (uint32_t)__shfl_xor((int)any, o);
-      w.template soften<true>(s, [&](int r) { return mine[r] >> (8 * g); });
       // Nothing times a value that is not finite would be NaN: values that no row sees become 0, and one that is not finite and
       // that some rows see is added to those alone.
-      uint32_t bad[NG], some = 0u;
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         uint32_t mask = 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t &sc = x.vr[n][e], &of = x.vr[n][4 + e];
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            uint32_t &sc = x.vr[n][e], &of = x.vr[n][4 + e];
             const int bit = 8 * g + e + 4 * h;
             const uint32_t half = h ? 0xFFFF0000u : 0x0000FFFFu;
             const bool see = any >> bit & 1u, wrong = not_finite(sc & half) || not_finite(of & half);
             if (see && wrong) mask |= 1u << bit;
             if (!see || wrong) sc &= ~half, of &= ~half;
           }
-        }
         mask |= (uint32_t)__shfl_xor((int)mask, 16);
         mask |= (uint32_t)__shfl_xor((int)mask, 32);
-        bad[n] = mask;
-        some |= mask;
-      }
-      if (__any(some != 0u)) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int n = 0; n < NV; ++n)
-            if (bad[n / (2 * GC)] & mine[r]) w.o[r][n] += NAN;
+        bad[n] = (uint32_t)__builtin_amdgcn_readfirstlane((int)mask);
+        some |= bad[n];
       }
     }
+    w.soften(s);
     w.weigh(x, masks, s);
+    if (__builtin_expect(some != 0u, 0)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+          if (bad[n / (2 * GC)] & seen(w.position[r])) w.o[r][n] += NAN;
+    }
   };
 
   if (next < stop) {
-    block<NC, NG> x, y;
-    place p = find(next), n;
-    load(p, x);
+    p = find(next);
+    load_keys(p, x);
+    load_values(p, x);
+    if (next + token_waves < stop) ahead = find(next + token_waves);
     for (;;) {
       next += token_waves;
       const bool more = next < stop;
-      if (more) {
-        n = find(next);
-        load(n, y);
-      }
-      attend(p, x);
+      attend(more);
       if (!more) break;
-      next += token_waves;
-      const bool again = next < stop;
-      if (again) {
-        p = find(next);
-        load(p, x);
-      }
-      attend(n, y);
-      if (!again) break;
+      load_values(ahead, x);
+      p = ahead;
+      if (next + token_waves < stop) ahead = find(next + token_waves);
     }
   }
 
