@@ -101,8 +101,18 @@ struct kv4_attention_args {
   float scale;  // times log2 e
   int window, sinks;
   int splits, chunk;  // blocks of a split
-  float *partial;     // [splits][tokens][heads][d + 2] where splits > 1: the unnormalised row, its maximum and its sum
+  float *partial;     // where splits > 1: unnormalised rows [splits][tokens][heads][d], then their bases and sums [..][2]
 };
+
+// where a split's row goes, and its base and sum
+DBS_DEV float *kv4_partial(const kv4_attention_args &a, int64_t token, int head, int d) {
+  const int64_t heads = (int64_t)a.key_heads * a.heads_per_key;
+  return a.partial + ((blockIdx.y * (int64_t)a.cache.tokens + token) * heads + head) * d;
+}
+DBS_DEV void kv4_partial_end(const kv4_attention_args &a, int64_t token, int head, int d, float base, float sum) {
+  const int64_t heads = (int64_t)a.key_heads * a.heads_per_key, rows = a.cache.tokens * heads;
+  ((float2 *)(a.partial + a.splits * rows * d))[blockIdx.y * rows + token * heads + head] = make_float2(base, sum);
+}
 
 // tiles: 16-row tiles of a wave, 4: the kernel for many rows (kv4_prompt.h); wide: q and p in two parts
 hipError_t kv4_attention_64(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);

@@ -126,39 +126,71 @@ __global__ void k_kv4_store(kv4_view c, int dim, int padded, int group, kv4_side
 }
 
 /*
- * Joins the splits of a row: o = sum_z 2^(m_z - m) o_z / sum_z 2^(m_z - m) l_z, in the order of the splits.  A workgroup to a
- * row, its waves taking every fourth split.
+ * Joins the splits of a row: o = sum_z 2^(m_z - m) o_z / sum_z 2^(m_z - m) l_z.  `lanes` lanes hold a row of four channels each, and
+ * `parts` such groups of a workgroup take every parts-th split of it and meet in LDS, in a fixed order: all of a workgroup for one
+ * row where rows are few and splits many, one group a row where rows are many.
  */
 template <class Y>
-__global__ __launch_bounds__(256) void k_kv4_combine(kv4_view c, int heads, int dim, int padded, int splits, const float *__restrict__ partial,
-                                                     Y *__restrict__ out, int64_t ot, int64_t oh) {
-  __shared__ float sums[4], parts[4][KV4_MAX_DIM];
-  const int64_t row = blockIdx.x;
+__global__ __launch_bounds__(1024) void k_kv4_combine(kv4_view c, int heads, int dim, int padded, int splits, int lanes, int parts,
+                                                     const float *__restrict__ partial, Y *__restrict__ out, int64_t ot, int64_t oh) {
+  __shared__ float sums[1024], shared[1024][4];
+  const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes, part = group % parts;
+  const int64_t all = (int64_t)c.tokens * heads, row = (int64_t)blockIdx.x * (blockDim.x / (lanes * parts)) + group / parts;
   const int64_t t = row / heads;
-  const int h = (int)(row % heads), wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  if (c.new_ptr && (t < kv4_new_ptr(c, 0) || t >= kv4_new_ptr(c, c.sequences))) return;  // of no sequence
-  const int64_t stride = (int64_t)c.tokens * heads * (padded + 2);
-  const float *from = partial + row * (padded + 2);
-  float top = -3.402823466e38f;
-  for (int z = lane; z < splits; z += 64) top = fmaxf(top, from[z * stride + padded]);
-  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-  float sum = 0.0f, v[KV4_MAX_DIM / 64] = {};
+  const int h = (int)(row % heads);
+  // a row of no sequence was written by nobody
+  const bool real = row < all && !(c.new_ptr && (t < kv4_new_ptr(c, 0) || t >= kv4_new_ptr(c, c.sequences)));
+  const bool in = real && 4 * lane < padded;
+  const float2 *const ends = (const float2 *)(partial + splits * all * padded) + row;
+  const float *const from = partial + row * padded + 4 * lane;
+  float top = -3.402823466e38f, sum = 0.0f, v[4] = {};
+  if (real)
+    for (int z = lane; z < splits; z += lanes) top = fmaxf(top, ends[z * all].x);
+  for (int o = 1; o < lanes; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if (in) {
 #pragma unroll 4
-  for (int z = wave; z < splits; z += 4) {
-    const float l = from[z * stride + padded + 1], f = __builtin_amdgcn_exp2f(from[z * stride + padded] - top);
-    if (l == 0.0f) continue;
-    sum += f * l;
+    for (int z = part; z < splits; z += parts) {
+      const float2 e = ends[z * all];
+      float x[4];
+      __builtin_memcpy(x, from + z * all * padded, 16);
+      const float f = __builtin_amdgcn_exp2f(e.x - top);
+      sum += f * e.y;
 #pragma unroll
-    for (int k = 0; k < KV4_MAX_DIM / 64; ++k)
-      if (64 * k + lane < padded) v[k] += f * from[z * stride + 64 * k + lane];
+      for (int k = 0; k < 4; ++k) v[k] += e.y != 0.0f ? f * x[k] : 0.0f;  // a split that saw nothing left its row as it was
+    }
   }
+  if (parts > 1) {
+    sums[threadIdx.x] = sum;
 #pragma unroll
-  for (int k = 0; k < KV4_MAX_DIM / 64; ++k) parts[wave][64 * k + lane] = v[k];
-  if (lane == 0) sums[wave] = sum;
-  __syncthreads();
-  const float all = sums[0] + sums[1] + sums[2] + sums[3], f = all == 0.0f ? 0.0f : 1.0f / all;
-  const int ch = threadIdx.x;
-  if (ch < dim) out[t * ot + h * oh + ch] = dbs_value<Y>::of((parts[0][ch] + parts[1][ch] + parts[2][ch] + parts[3][ch]) * f);
+    for (int k = 0; k < 4; ++k) shared[threadIdx.x][k] = v[k];
+    __syncthreads();
+    if (part) return;
+    for (int p = 1; p < parts; ++p) {
+      sum += sums[threadIdx.x + p * lanes];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += shared[threadIdx.x + p * lanes][k];
+    }
+  }
+  if (!in || 4 * lane >= dim) return;
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  Y y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] = dbs_value<Y>::of(v[k] * f);
+  __builtin_memcpy(out + t * ot + h * oh + 4 * lane, y, sizeof y);
+}
+
+template <class Y>
+hipError_t combine(const kv4_view &c, int heads, int dim, int splits, const void *partial, void *out, int64_t ot, int64_t oh, hipStream_t s) {
+  const int padded = kv4_padded(dim);
+  int lanes = 16, parts = 1;
+  while (4 * lanes < padded) lanes *= 2;
+  const int64_t rows = (int64_t)c.tokens * heads;
+  // about as many lanes as the card holds at once
+  while (lanes * parts < 1024 && parts < splits && rows * lanes * parts < 256 * 1024) parts *= 2;
+  const int threads = lanes * parts < 256 ? 256 : lanes * parts, per = threads / (lanes * parts);
+  hipLaunchKernelGGL(k_kv4_combine<Y>, dim3((unsigned)((rows + per - 1) / per)), dim3(threads), 0, s, c, heads, dim, padded, splits, lanes, parts,
+                     (const float *)partial, (Y *)out, ot, oh);
+  return DBS_NOTE(hipGetLastError());
 }
 
 bool view_of(const dbs_kv4_cache *a, int32_t tokens, kv4_view *c, dbs_status *st) {
@@ -371,14 +403,8 @@ dbs_status dbs_kv4_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t hea
   const dim3 grid((unsigned)(p.units * a->key_heads), (unsigned)p.splits);
   if (run(k, p.tiles, wide, grid, (hipStream_t)stream) != hipSuccess) return DBS_ERR_DEVICE;
   if (p.splits > 1) {
-    const dim3 rows((unsigned)(tokens * heads));
-    if (out_dtype == DBS_F32)
-      hipLaunchKernelGGL(k_kv4_combine<float>, rows, dim3(256), 0, (hipStream_t)stream, c, heads, a->head_dim, padded, p.splits,
-                         (const float *)workspace, (float *)out, ot, oh);
-    else
-      hipLaunchKernelGGL(k_kv4_combine<bf16_bits>, rows, dim3(256), 0, (hipStream_t)stream, c, heads, a->head_dim, padded, p.splits,
-                         (const float *)workspace, (bf16_bits *)out, ot, oh);
-    if (DBS_NOTE(hipGetLastError()) != hipSuccess) return DBS_ERR_DEVICE;
+    const auto join = out_dtype == DBS_F32 ? combine<float> : combine<bf16_bits>;
+    if (join(c, heads, a->head_dim, p.splits, workspace, out, ot, oh, (hipStream_t)stream) != hipSuccess) return DBS_ERR_DEVICE;
   }
   return DBS_OK;
 }

@@ -468,13 +468,12 @@ __global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R *
   for (int r = 0; r < R; ++r) {
     if (wave_row + 16 * r + i >= all_rows) continue;
     if (a.splits > 1) {
-      const int64_t heads = (int64_t)a.key_heads * rep;
-      float *to = a.partial + ((blockIdx.y * (int64_t)c.tokens + at_token[r]) * heads + at_head[r]) * (D + 2);
+      float *to = kv4_partial(a, at_token[r], at_head[r], D);
       if (w.sum[r] != 0.0f) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) __builtin_memcpy(to + 16 * n + 4 * g, &w.o[r][n], 16);
       }
-      if (g == 0) to[D] = w.top[r], to[D + 1] = w.sum[r];
+      if (g == 0) kv4_partial_end(a, at_token[r], at_head[r], D, w.top[r], w.sum[r]);
       continue;
     }
     // a row that sees nothing is 0; a sum that is not a number stays one

@@ -347,8 +347,7 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
   sum += __shfl_xor(sum, 32);
   if (!real) return;
   if (a.splits > 1) {
-    const int64_t heads = (int64_t)a.key_heads * rep;
-    float *to = a.partial + ((blockIdx.y * (int64_t)c.tokens + at_token) * heads + at_head) * (D + 2);
+    float *to = kv4_partial(a, at_token, at_head, D);
     if (sum != 0.0f) {
 #pragma unroll
       for (int n = 0; n < NC; ++n)
@@ -358,7 +357,7 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
           __builtin_memcpy(to + 32 * n + 8 * r + 4 * h, v, 16);
         }
     }
-    if (h == 0) to[D] = top, to[D + 1] = sum;
+    if (h == 0) kv4_partial_end(a, at_token, at_head, D, top, sum);
     return;
   }
   const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
