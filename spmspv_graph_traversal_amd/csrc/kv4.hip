@@ -265,7 +265,7 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, int32_t 
   kv4_plan p;
   const int rep = heads / a->key_heads;
   const int64_t rows = (int64_t)tokens * rep, each = (rows + a->sequences - 1) / a->sequences;
-  p.tiles = each <= 16 ? 1 : each <= 32 ? 2 : 4;
+  p.tiles = each <= 16 ? 1 : each <= 32 && a->head_dim <= 192 ? 2 : 4;  // two tiles of heads of 256 leave no registers
   const int per = p.tiles == 4 ? 128 : 16 * p.tiles * 4;
   p.units = a->new_ptr ? rows / per + a->sequences : (tokens / a->sequences * (int64_t)rep + per - 1) / per * a->sequences;
   int64_t slots = (int64_t)a->table_pages * a->page_tokens;

@@ -1,6 +1,8 @@
 // Attention over the cache of 4-bit keys and values (kv4.h) on the matrix cores.
 #pragma once
 
+#include <type_traits>
+
 #include "kv4.h"
 
 namespace kv4 {
@@ -53,6 +55,63 @@ DBS_DEV float sum_of(half2_t h, float sum) { return __builtin_amdgcn_fdot2(h, ha
 
 // Two halves of which either is infinite or NaN.
 DBS_DEV bool not_finite(uint32_t pair) { return (pair & 0x7C00u) == 0x7C00u || (pair & 0x7C000000u) == 0x7C000000u; }
+
+/*
+ * A lane's part of a query on its way: N runs of eight channels from `first` on, `step` apart.  All loads are issued together, from
+ * addresses that are there (a run behind the head is the last one again), and nothing is waited for until halves() makes halves of
+ * them in the order of values_of, scaled by a power of two so that the row's largest element is between 2^14 and 2^15;
+ * the lanes of a row are `lanes` apart.
+ */
+template <int N, bool WIDE>
+struct query {
+  uint4 raw[N][2];
+  DBS_DEV void load(const kv4_attention_args &a, int64_t token, int head, int first, int step) {
+    if (a.q_bf16) {
+      const bf16_bits *const p = (const bf16_bits *)a.q + token * a.qt + head * a.qh;
+#pragma unroll
+      for (int n = 0; n < N; ++n) __builtin_memcpy(&raw[n][0], p + min(first + n * step, a.dim - 8), 16);
+    } else {
+      const float *const p = (const float *)a.q + token * a.qt + head * a.qh;
+#pragma unroll
+      for (int n = 0; n < N; ++n) __builtin_memcpy(raw[n], p + min(first + n * step, a.dim - 8), 32);
+    }
+  }
+  // the scores' scale
+  template <int LANES>
+  DBS_DEV float halves(const kv4_attention_args &a, bool real, int first, int step, half8_t (&high)[N], half8_t (&low)[N]) {
+    float x[N][8], most = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const bool in = real && first + n * step < a.dim;
+      uint32_t w[8];
+      __builtin_memcpy(w, raw[n], 32);
+      if (a.q_bf16) {
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          const uint32_t two = w[e];
+          w[2 * e] = two << 16;
+          w[2 * e + 1] = two & 0xFFFF0000u;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[n][e] = in ? __uint_as_float(w[e]) : 0.0f;
+        most = fmaxf(most, fabsf(x[n][e]));
+      }
+    }
+    for (int o = LANES; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o));
+    const int up = most > 0.0f && most < INFINITY ? 14 - ilogbf(most) : 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = ldexpf(x[n][e / 2 + e % 2 * 4], up);
+        high[n][e] = (_Float16)v;
+        if (WIDE) low[n][e] = (_Float16)(v - (float)high[n][e]);
+      }
+    return ldexpf(a.scale, -up);
+  }
+};
 
 // A block of 32 tokens as a lane holds it.
 template <int NC, int NG>
@@ -172,8 +231,15 @@ struct wave_state {
   }
 };
 
+// Waves of a SIMD that the registers are made to hold: as many as spill none, since a spilled register's load waits for all codes
+// that are on their way.
+constexpr int waves_of(int nc, int gc, int r, bool wide) {
+  const int parts = wide ? 2 : 1, need = 8 * nc * r + 4 * nc * r * parts + 4 * nc + 10 * (nc / gc) + 12 * r * parts + 60;
+  return need <= 124 ? 4 : need <= 164 ? 3 : need <= 250 ? 2 : 1;
+}
+
 template <int NC, int GC, int R, bool WIDE>
-__global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R * NC * (WIDE ? 2 : 1) <= 8 ? 2 : 1) void k_kv4_attention(kv4_attention_args a) {
+__global__ __launch_bounds__(64 * kWaves, waves_of(NC, GC, R, WIDE)) void k_kv4_attention(kv4_attention_args a) {
   typedef wave_state<NC, GC, R, WIDE> state;
   constexpr int NG = state::NG, NV = state::NV, D = state::D, ROWS = 16 * R * kWaves;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -200,58 +266,23 @@ __global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R *
   const int token_waves = kWaves / row_waves, part = wave % token_waves;
   const int wave_row = row0 + wave / token_waves * (16 * R);  // may be behind the last row
 
+  // What depends on no length is asked for first: the queries and, without a window, the pages of the first block.
   state w;
-  int64_t at_token[R];
-  int at_head[R];
+  query<NC, WIDE> q[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = wave_row + 16 * r + i;
     const bool real = row < all_rows;
     const int t = (real ? row : 0) / rep;
     w.position[r] = real ? rows.position + t : -1;
-    at_token[r] = rows.first + t;
-    at_head[r] = head * rep + (real ? row : 0) - t * rep;
-    w.top[r] = kLow;
-    w.sum[r] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < NV; ++n) w.o[r][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // q as halves, its largest element between 2^14 and 2^15; WIDE: in two parts
-    float x[NC][8], most = 0.0f;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const int channel = 32 * k + 8 * g;
-      const bool in = real && channel < a.dim;
-      if (a.q_bf16) {
-        uint16_t h[8] = {};
-        if (in) __builtin_memcpy(h, (const bf16_bits *)a.q + at_token[r] * a.qt + at_head[r] * a.qh + channel, 16);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = bf16_to_f32(h[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = 0.0f;
-        if (in) __builtin_memcpy(x[k], (const float *)a.q + at_token[r] * a.qt + at_head[r] * a.qh + channel, 32);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[k][e]));
-    }
-    most = fmaxf(most, __shfl_xor(most, 16));
-    most = fmaxf(most, __shfl_xor(most, 32));
-    const int up = most > 0.0f && most < INFINITY ? 14 - ilogbf(most) : 0;
-    w.scale[r] = ldexpf(a.scale, -up);
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      half8_t h, l;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int from = e / 2 + e % 2 * 4;  // the order of values_of
-        const float v = ldexpf(x[k][from], up);
-        h[e] = (_Float16)v;
-        l[e] = (_Float16)(v - (float)h[e]);
-      }
-      w.q[0][r][k] = h;
-      if (WIDE) w.q[state::PARTS - 1][r][k] = l;
-    }
+    q[r].load(a, rows.first + t, head * rep + (real ? row : 0) - t * rep, 8 * g, 32);
   }
+  const int32_t *const table = c.table + b * c.ldtable;
+  const int block0 = (a.splits > 1 ? blockIdx.y * a.chunk : 0) + part, token0 = min(block0, 1 << 25) * KV4_BLOCK;
+  int early[2] = {-1, -1};
+  if (c.width > 0)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) early[h] = table[min((token0 + 16 * h) >> c.page_shift, c.width - 1)];
 
   // the tokens that the wave's rows see: those below `end` from `start` on, and of the first ones `sink_blocks` blocks
   const int first_token = wave_row / rep, last_token = (min(all_rows, wave_row + 16 * R) - 1) / rep;
@@ -264,12 +295,8 @@ __global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R *
     if (sink_blocks * KV4_BLOCK >= start) start = sink_blocks = 0;
   }
   const int blocks = sink_blocks + (end > start ? (end - start + KV4_BLOCK - 1) / KV4_BLOCK : 0);
-  int next = part, stop = blocks;
-  if (a.splits > 1) {
-    const int split = blockIdx.y;
-    next = (int)min((int64_t)split * a.chunk, (int64_t)blocks) + part;
-    if (split + 1 < a.splits) stop = (int)min((int64_t)(split + 1) * a.chunk, (int64_t)blocks);
-  }
+  int next = block0, stop = blocks;
+  if (a.splits > 1 && blockIdx.y + 1 < a.splits) stop = min((int)(blockIdx.y + 1) * a.chunk, blocks);
 
   const kv4_layout lay(D, 32 * GC, 1 << c.page_shift);
   const int64_t head_offset = (int64_t)head * lay.head_bytes;
@@ -281,15 +308,13 @@ __global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R *
   struct place {
     int token, page[2];
   };
-  const int32_t *const table = c.table + b * c.ldtable;
-  auto find = [&](int n) {
+  auto find = [&](int n) {  // n < stop: the table has entries
     place p;
     p.token = token_of(n);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int at = (p.token + 16 * h) >> c.page_shift;
-      const int page = p.token + 16 * h < end && at < c.width ? table[at] : -1;
-      p.page[h] = (unsigned)page < (unsigned)c.pages ? page : -1;
+      const int page = table[min((p.token + 16 * h) >> c.page_shift, c.width - 1)];
+      p.page[h] = p.token + 16 * h < end && (unsigned)page < (unsigned)c.pages ? page : -1;
     }
     return p;
   };
@@ -337,10 +362,10 @@ __global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R *
   block<NC, NG> x;
   place p = {}, ahead = {};
   // a block: its scores, the next one's keys on their way, its weights, its values, and the next one's
-  auto attend = [&](bool more) {
+  auto attend = [&](auto more) {
     f32x4 s[2][R];
     w.scores(x, masks, s);
-    if (more) load_keys(ahead, x);
+    if constexpr (decltype(more)::value) load_keys(ahead, x);
     const int j = p.token;
     const bool whole = p.page[0] >= 0 && p.page[1] >= 0 && j + KV4_BLOCK - 1 <= low &&
                        (!a.window || j > high - a.window || j + KV4_BLOCK <= a.sinks);
@@ -404,20 +429,39 @@ __global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R *
     }
   };
 
+  auto prepare = [&] {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w.scale[r] = q[r].template halves<16>(a, w.position[r] >= 0, 8 * g, 32, w.q[0][r], w.q[state::PARTS - 1][r]);
+      w.top[r] = kLow;
+      w.sum[r] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NV; ++n) w.o[r][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  };
   if (next < stop) {
-    p = find(next);
+    if (a.window) {
+      p = find(next);
+    } else {
+      p.token = token0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) p.page[h] = token0 + 16 * h < end && (unsigned)early[h] < (unsigned)c.pages ? early[h] : -1;
+    }
     load_keys(p, x);
     load_values(p, x);
-    if (next + token_waves < stop) ahead = find(next + token_waves);
-    for (;;) {
-      next += token_waves;
-      const bool more = next < stop;
-      attend(more);
-      if (!more) break;
+    // pages one block further ahead than codes; the last block's again behind it
+    ahead = find(min(next + token_waves, stop - 1));
+    prepare();
+    // the last block in a copy of its own: a wait for codes has to know what was asked for after them
+    for (next += token_waves; next < stop; next += token_waves) {
+      attend(std::true_type());
       load_values(ahead, x);
       p = ahead;
-      if (next + token_waves < stop) ahead = find(next + token_waves);
+      ahead = find(min(next + token_waves, stop - 1));
     }
+    attend(std::false_type());
+  } else {
+    prepare();
   }
 
   // sums over the lanes of a row; then the waves that split its tokens
@@ -466,14 +510,17 @@ __global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R *
 
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    if (wave_row + 16 * r + i >= all_rows) continue;
+    const int row = wave_row + 16 * r + i;
+    if (row >= all_rows) continue;
+    const int64_t at_token = rows.first + row / rep;
+    const int at_head = head * rep + row % rep;
     if (a.splits > 1) {
-      float *to = kv4_partial(a, at_token[r], at_head[r], D);
+      float *to = kv4_partial(a, at_token, at_head, D);
       if (w.sum[r] != 0.0f) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) __builtin_memcpy(to + 16 * n + 4 * g, &w.o[r][n], 16);
       }
-      if (g == 0) kv4_partial_end(a, at_token[r], at_head[r], D, w.top[r], w.sum[r]);
+      if (g == 0) kv4_partial_end(a, at_token, at_head, D, w.top[r], w.sum[r]);
       continue;
     }
     // a row that sees nothing is 0; a sum that is not a number stays one
@@ -486,12 +533,12 @@ __global__ __launch_bounds__(64 * kWaves, R * NC * (WIDE ? 2 : 1) <= 4 ? 4 : R *
         bf16_bits v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = dbs_value<bf16_bits>::of(w.o[r][n][e] * f);
-        __builtin_memcpy((bf16_bits *)a.out + at_token[r] * a.ot + at_head[r] * a.oh + channel, v, 8);
+        __builtin_memcpy((bf16_bits *)a.out + at_token * a.ot + at_head * a.oh + channel, v, 8);
       } else {
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = w.o[r][n][e] * f;
-        __builtin_memcpy((float *)a.out + at_token[r] * a.ot + at_head[r] * a.oh + channel, v, 16);
+        __builtin_memcpy((float *)a.out + at_token * a.ot + at_head * a.oh + channel, v, 16);
       }
     }
   }

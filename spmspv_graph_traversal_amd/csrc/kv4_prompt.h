@@ -70,52 +70,15 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
   const int64_t at_token = rows.first + t;
   const int at_head = head * rep + (real ? row : 0) - t * rep;
 
+  query<2 * NC, WIDE> raw;
+  raw.load(a, at_token, at_head, 8 * h, 16);
   half8_t q[PARTS][2 * NC];
-  float scale, top = kLow, sum = 0.0f;
+  float top = kLow, sum = 0.0f;
   f32x16 o[NC];
 #pragma unroll
   for (int n = 0; n < NC; ++n)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
-  {
-    float most = 0.0f;
-    auto load = [&](int u, float (&x)[8]) {
-      const int channel = 16 * u + 8 * h;
-      const bool in = real && channel < a.dim;
-      if (a.q_bf16) {
-        uint16_t v[8] = {};
-        if (in) __builtin_memcpy(v, (const bf16_bits *)a.q + at_token * a.qt + at_head * a.qh + channel, 16);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = bf16_to_f32(v[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-        if (in) __builtin_memcpy(x, (const float *)a.q + at_token * a.qt + at_head * a.qh + channel, 32);
-      }
-    };
-    float x[2 * NC][8];
-#pragma unroll
-    for (int u = 0; u < 2 * NC; ++u) {
-      load(u, x[u]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[u][e]));
-    }
-    most = fmaxf(most, __shfl_xor(most, 32));
-    const int up = most > 0.0f && most < INFINITY ? 14 - ilogbf(most) : 0;
-    scale = ldexpf(a.scale, -up);
-#pragma unroll
-    for (int u = 0; u < 2 * NC; ++u) {
-      half8_t high, low;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = ldexpf(x[u][e / 2 + e % 2 * 4], up);  // in the order of values_of
-        high[e] = (_Float16)v;
-        low[e] = (_Float16)(v - (float)high[e]);
-      }
-      q[0][u] = high;
-      if (WIDE) q[PARTS - 1][u] = low;
-    }
-  }
 
   // what the workgroup's rows see, in tiles, and what the wave's do
   const int first_token = row0 / rep, last_token = (min(all_rows, row0 + ROWS) - 1) / rep;
@@ -216,7 +179,7 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
     }
   };
 
-  auto attend = [&](int buffer, int j, uint64_t there) {
+  auto attend = [&](int buffer, int j, uint64_t there, float scale) {
 #pragma clang fp contract(off)  // the largest score less the base is 6, exactly
     const half8_t *const k = operands + buffer * 2 * T::kOperands, *const v = k + T::kOperands;
     f32x16 s[SB];
@@ -313,13 +276,14 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
     }
   };
 
+  typename T::stage s;
   if (next < stop) {
-    typename T::stage s;
     // pages one tile further ahead than codes
     int token = token_of(next), k_page = page_of(token + kt), v_page = page_of(token + 8 * vt);
     load(token, k_page, v_page, s);
     int ahead = next + 1 < stop ? token_of(next + 1) : end, k_ahead = page_of(ahead + kt), v_ahead = page_of(ahead + 8 * vt);
     uint64_t there = __ballot((unsigned)k_page < (unsigned)c.pages);
+    const float scale = raw.template halves<32>(a, real, 8 * h, 16, q[0], q[PARTS - 1]);
     put(0, s);
     __syncthreads();
     for (int buffer = 0;; buffer ^= 1) {
@@ -336,7 +300,7 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
       }
       const bool none = !has_rows || token_now > high ||
                         (a.window && token_now + TOKENS - 1 <= low - a.window && token_now >= a.sinks);  // of its rows
-      if (!none) attend(buffer, token_now, there_now);
+      if (!none) attend(buffer, token_now, there_now, scale);
       if (!more) break;
       put(buffer ^ 1, s);
       __syncthreads();
@@ -402,8 +366,9 @@ template <int NC, int GC>
 hipError_t launch(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s) {
   if constexpr (NC % GC == 0) {
     if (tiles == 4) return wide ? launch_prompt<NC, GC, true>(a, grid, s) : launch_prompt<NC, GC, false>(a, grid, s);
-    if (wide) return tiles == 1 ? launch<NC, GC, 1, true>(a, grid, s) : launch<NC, GC, 2, true>(a, grid, s);
-    return tiles == 1 ? launch<NC, GC, 1, false>(a, grid, s) : launch<NC, GC, 2, false>(a, grid, s);
+    if constexpr (NC <= 6)
+      if (tiles == 2) return wide ? launch<NC, GC, 2, true>(a, grid, s) : launch<NC, GC, 2, false>(a, grid, s);
+    if (tiles == 1) return wide ? launch<NC, GC, 1, true>(a, grid, s) : launch<NC, GC, 1, false>(a, grid, s);
   }
   return hipErrorInvalidValue;
 }
