@@ -31,6 +31,14 @@ struct kv4_layout {
   }
 };
 
+// Waves of a SIMD that the kernel for few rows is made to hold, r tiles of 16 rows a wave, heads of 32 nc channels in groups of
+// 32 gc: as many as spill no register, since a spilled one's load waits for all codes that are on their way.
+constexpr int kv4_waves(int nc, int gc, int r, bool wide) {
+  const int parts = wide ? 2 : 1, blocks = 2 * (4 * nc + 10 * (nc / gc));
+  const int need = 8 * nc * r + 4 * nc * r * parts + blocks + 12 * r * parts + 8 * (r - 1) + 56;
+  return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
+}
+
 // place of token e of eight in a value record
 __host__ __device__ inline int kv4_place(int e) { return (e & 3) * 2 + (e >> 2); }
 
@@ -114,9 +122,10 @@ DBS_DEV void kv4_partial_end(const kv4_attention_args &a, int64_t token, int hea
   ((float2 *)(a.partial + a.splits * rows * d))[blockIdx.y * rows + token * heads + head] = make_float2(base, sum);
 }
 
-// tiles: 16-row tiles of a wave, 4: the kernel for many rows (kv4_prompt.h); wide: q and p in two parts
-hipError_t kv4_attention_64(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);
-hipError_t kv4_attention_96(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);
-hipError_t kv4_attention_128(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);
-hipError_t kv4_attention_192(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);
-hipError_t kv4_attention_256(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s);
+// tiles: 16-row tiles of a wave, 4: the kernel for many rows (kv4_prompt.h); share: workgroups that share a compute unit, 0: as many
+// of four waves as fit; wide: q and p in two parts
+hipError_t kv4_attention_64(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
+hipError_t kv4_attention_96(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
+hipError_t kv4_attention_128(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
+hipError_t kv4_attention_192(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
+hipError_t kv4_attention_256(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);

@@ -133,7 +133,8 @@ __global__ void k_kv4_store(kv4_view c, int dim, int padded, int group, kv4_side
 template <class Y>
 __global__ __launch_bounds__(1024) void k_kv4_combine(kv4_view c, int heads, int dim, int padded, int splits, int lanes, int parts,
                                                      const float *__restrict__ partial, Y *__restrict__ out, int64_t ot, int64_t oh) {
-  __shared__ float sums[1024], shared[1024][4];
+  __shared__ float2 sums[1024];
+  __shared__ float shared[1024][4];
   const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes, part = group % parts;
   const int64_t all = (int64_t)c.tokens * heads, row = (int64_t)blockIdx.x * (blockDim.x / (lanes * parts)) + group / parts;
   const int64_t t = row / heads;
@@ -144,31 +145,54 @@ __global__ __launch_bounds__(1024) void k_kv4_combine(kv4_view c, int heads, int
   const float2 *const ends = (const float2 *)(partial + splits * all * padded) + row;
   const float *const from = partial + row * padded + 4 * lane;
   float top = -3.402823466e38f, sum = 0.0f, v[4] = {};
-  if (real)
-    for (int z = lane; z < splits; z += lanes) top = fmaxf(top, ends[z * all].x);
-  for (int o = 1; o < lanes; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
   if (in) {
-#pragma unroll 4
-    for (int z = part; z < splits; z += parts) {
-      const float2 e = ends[z * all];
-      float x[4];
-      __builtin_memcpy(x, from + z * all * padded, 16);
-      const float f = __builtin_amdgcn_exp2f(e.x - top);
-      sum += f * e.y;
+    for (int z0 = part; z0 < splits; z0 += 4 * parts) {  // four splits on their way
+      float2 e[4];
+      float x[4][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += e.y != 0.0f ? f * x[k] : 0.0f;  // a split that saw nothing left its row as it was
+      for (int k = 0; k < 4; ++k) {
+        const int64_t z = min(z0 + k * parts, splits - 1);
+        e[k] = ends[z * all];
+        __builtin_memcpy(x[k], from + z * all * padded, 16);
+      }
+      float t = top;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (z0 + k * parts >= splits) e[k] = make_float2(-3.402823466e38f, 0.0f);
+        t = fmaxf(t, e[k].x);
+      }
+      const float f = __builtin_amdgcn_exp2f(top - t);
+      top = t;
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] *= f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float g = __builtin_amdgcn_exp2f(e[k].x - top);
+        sum += g * e[k].y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += e[k].y != 0.0f ? g * x[k][i] : 0.0f;  // a split that saw nothing left its row as it was
+      }
     }
   }
   if (parts > 1) {
-    sums[threadIdx.x] = sum;
+    sums[threadIdx.x] = make_float2(top, sum);
 #pragma unroll
     for (int k = 0; k < 4; ++k) shared[threadIdx.x][k] = v[k];
     __syncthreads();
     if (part) return;
-    for (int p = 1; p < parts; ++p) {
-      sum += sums[threadIdx.x + p * lanes];
+    float t = top;
+    for (int p = 1; p < parts; ++p) t = fmaxf(t, sums[threadIdx.x + p * lanes].x);
+    const float f = __builtin_amdgcn_exp2f(top - t);
+    sum *= f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += shared[threadIdx.x + p * lanes][k];
+    for (int k = 0; k < 4; ++k) v[k] *= f;
+    for (int p = 1; p < parts; ++p) {
+      const float2 e = sums[threadIdx.x + p * lanes];
+      const float g = __builtin_amdgcn_exp2f(e.x - t);
+      sum += g * e.y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += g * shared[threadIdx.x + p * lanes][k];
     }
   }
   if (!in || 4 * lane >= dim) return;
@@ -255,34 +279,69 @@ bool meets_pool(const dbs_rows &rows, const dbs_kv4_cache *a) {
   return written_over(rows, a->pool, (a->pages - 1) * a->page_stride + bytes);
 }
 
-// How a call is cut: tiles of 16 rows a wave takes, workgroups along the rows, and splits of the tokens.
+// How a call is cut: tiles of 16 rows a wave takes, workgroups along the rows, waves of a workgroup, and splits of the tokens.
 struct kv4_plan {
-  int tiles, splits, chunk;
+  int tiles, share, splits, chunk;
   int64_t units;
 };
 
-kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, int32_t window, int32_t sinks, int32_t max_len) {
-  kv4_plan p;
-  const int rep = heads / a->key_heads;
+kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wide, int32_t window, int32_t sinks, int32_t max_len) {
+  constexpr int units_of_card = 256;
+  kv4_plan p = {};
+  const int rep = heads / a->key_heads, d = kv4_padded(a->head_dim), nc = d / 32, gc = a->group / 32;
   const int64_t rows = (int64_t)tokens * rep, each = (rows + a->sequences - 1) / a->sequences;
-  p.tiles = each <= 16 ? 1 : each <= 32 && a->head_dim <= 192 ? 2 : 4;  // two tiles of heads of 256 leave no registers
-  const int per = p.tiles == 4 ? 128 : 16 * p.tiles * 4;
-  p.units = a->new_ptr ? rows / per + a->sequences : (tokens / a->sequences * (int64_t)rep + per - 1) / per * a->sequences;
+  // two tiles a wave of larger heads leave no registers
+  p.tiles = each <= 16 ? 1 : each <= 64 && d <= 128 ? 2 : 4;
   int64_t slots = (int64_t)a->table_pages * a->page_tokens;
   if (max_len > 0 && max_len < slots) slots = max_len;
-  int64_t blocks = (slots + KV4_BLOCK - 1) / KV4_BLOCK;
-  if (window) {
-    const int64_t span = (int64_t)window + (each < per ? each : per) / rep + 1;
-    const int64_t seen = (span + KV4_BLOCK - 1) / KV4_BLOCK + 1 + ((int64_t)sinks + KV4_BLOCK - 1) / KV4_BLOCK;
-    if (seen < blocks) blocks = seen;
+  const auto cut = [&](int per) {  // workgroups of `per` rows
+    p.units = a->new_ptr ? rows / per + a->sequences : (tokens / a->sequences * (int64_t)rep + per - 1) / per * a->sequences;
+  };
+  const auto blocks_of = [&](int per) {  // that the rows of a workgroup see at most
+    int64_t blocks = (slots + KV4_BLOCK - 1) / KV4_BLOCK;
+    if (window) {
+      const int64_t span = (int64_t)window + (each < per ? each : per) / rep + 1;
+      const int64_t seen = (span + KV4_BLOCK - 1) / KV4_BLOCK + 1 + ((int64_t)sinks + KV4_BLOCK - 1) / KV4_BLOCK;
+      if (seen < blocks) blocks = seen;
+    }
+    return blocks;
+  };
+  const int waves = p.tiles == 4 ? 2 : kv4_waves(nc, gc, p.tiles, wide);
+  p.splits = 1;
+  if (p.tiles == 1 && waves > 1) {
+    // All waves of a compute unit, or of half of one, for a key head's rows: where few blocks leave less to win by splits
+    // than the launch costs that joins them (about three microseconds, of which a compute unit takes 25 blocks of 128 channels).
+    cut(16);
+    const int64_t groups = p.units * a->key_heads;
+    if (groups <= 2 * units_of_card && blocks_of(16) * nc <= 100) {
+      p.share = groups <= units_of_card ? 1 : 2;
+      return p;
+    }
   }
-  const int64_t groups = p.units * a->key_heads;
-  const int64_t target = 1024;
-  int64_t splits = groups < target ? (target + groups - 1) / groups : 1;
-  const int64_t most = blocks / 8;  // at least two blocks a wave
-  if (splits > most) splits = most;
+  const int per = p.tiles == 4 ? 128 : 64 * p.tiles;
+  cut(per);
+  const int64_t blocks = blocks_of(per), groups = p.units * a->key_heads;
+  int64_t splits = 1;
+  if (p.tiles == 4) {
+    // Splits pay where they fill the card's last round better than the joining of their rows costs: rounds of workgroups in units
+    // of a block's time, 1.3 us, in which joining moves 5 MB.
+    const int64_t at_once = units_of_card * (wide || d > 128 ? 1 : 2);
+    double best = 0.0;
+    for (int64_t s = 1; s <= 64 && s <= (blocks + 7) / 8; ++s) {
+      const int64_t chunk = (blocks + s - 1) / s;
+      const double cost = (double)((groups * s + at_once - 1) / at_once) * (chunk + 4) +
+                          (s > 1 ? 4.0 + (double)s * tokens * heads * d * 8 / 5e6 : 0.0);
+      if (s == 1 || cost < best) best = cost, splits = s;
+    }
+  } else {
+    // as many workgroups as the card holds at once, of two blocks a wave at least; more of them where sequences may differ in length
+    const int64_t once = units_of_card * waves, several = p.units > 1 ? 4 * once : 0;
+    splits = once / groups < blocks / 8 ? once / groups : blocks / 8;
+    const int64_t more = several / groups < blocks / 40 ? several / groups : blocks / 40;
+    if (splits < more) splits = more;
+    if (splits > 1024) splits = 1024;
+  }
   if (splits < 1) splits = 1;
-  if (splits > 1024) splits = 1024;
   p.chunk = (int)((blocks + splits - 1) / splits);
   p.chunk = (p.chunk + 3) / 4 * 4;
   p.splits = blocks > p.chunk ? (int)((blocks + p.chunk - 1) / p.chunk) : 1;
@@ -364,7 +423,7 @@ dbs_status dbs_kv4_attention_workspace(const dbs_kv4_cache *a, int32_t tokens, i
   if (st != DBS_OK) return st;
   *bytes = 0;
   if (go) {
-    const kv4_plan p = plan_of(a, tokens, heads, window, sinks, max_len);
+    const kv4_plan p = plan_of(a, tokens, heads, q_dtype == DBS_F32 || out_dtype == DBS_F32, window, sinks, max_len);
     *bytes = partial_bytes(a, tokens, heads, p.splits);
   }
   return DBS_OK;
@@ -384,7 +443,7 @@ dbs_status dbs_kv4_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t hea
   if (heads_meet(tokens, ot, heads, oh, a->head_dim) || dbs_rows_meet(in, to) || meets_pool(to, a) || meets_lists(to, a))
     return DBS_ERR_INVALID_ARG;
   const bool wide = q_dtype == DBS_F32 || out_dtype == DBS_F32;
-  kv4_plan p = plan_of(a, tokens, heads, window, sinks, max_len);
+  kv4_plan p = plan_of(a, tokens, heads, wide, window, sinks, max_len);
   if (workspace_bytes < partial_bytes(a, tokens, heads, p.splits)) p.splits = 1;  // slower, and right
   if (p.splits > 1) {
     const dbs_rows scratch = {(__int128)(uintptr_t)workspace, 1, 0, 1, 0, partial_bytes(a, tokens, heads, p.splits)};
@@ -401,7 +460,7 @@ dbs_status dbs_kv4_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t hea
   const auto run = padded == 64 ? kv4_attention_64 : padded == 96 ? kv4_attention_96 : padded == 128 ? kv4_attention_128 :
                    padded == 192 ? kv4_attention_192 : kv4_attention_256;
   const dim3 grid((unsigned)(p.units * a->key_heads), (unsigned)p.splits);
-  if (run(k, p.tiles, wide, grid, (hipStream_t)stream) != hipSuccess) return DBS_ERR_DEVICE;
+  if (run(k, p.tiles, p.share, wide, grid, (hipStream_t)stream) != hipSuccess) return DBS_ERR_DEVICE;
   if (p.splits > 1) {
     const auto join = out_dtype == DBS_F32 ? combine<float> : combine<bf16_bits>;
     if (join(c, heads, a->head_dim, p.splits, workspace, out, ot, oh, (hipStream_t)stream) != hipSuccess) return DBS_ERR_DEVICE;

@@ -11,7 +11,6 @@ typedef kv4_half2 half2_t;
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;
 constexpr float kLow = -3.402823466e38f;  // a maximum before any score
 // Exponentials are 2^(score - base), the base being 6 below the largest score when it was last raised, which is when one is 12 above
 // it: up to 2^12, and 20 bits below the largest one before the half that holds them loses bits.
@@ -132,7 +131,8 @@ struct block {
  * between lanes.  Sums of exponentials stay in each lane until the end.
  *
  * A workgroup's four waves split rows first (R tiles of 16 each) and, where the rows do not need them all, the tokens; further
- * splits of the tokens over workgroups are joined by k_kv4_combine.
+ * splits of the tokens over workgroups are joined by k_kv4_combine.  Few rows over few tokens are one workgroup's of as many waves
+ * as a compute unit holds, W, which all split the tokens.
  */
 template <int NC, int GC, int R, bool WIDE>
 struct wave_state {
@@ -231,17 +231,10 @@ struct wave_state {
   }
 };
 
-// Waves of a SIMD that the registers are made to hold: as many as spill none, since a spilled register's load waits for all codes
-// that are on their way.
-constexpr int waves_of(int nc, int gc, int r, bool wide) {
-  const int parts = wide ? 2 : 1, need = 8 * nc * r + 4 * nc * r * parts + 4 * nc + 10 * (nc / gc) + 12 * r * parts + 60;
-  return need <= 124 ? 4 : need <= 164 ? 3 : need <= 250 ? 2 : 1;
-}
-
-template <int NC, int GC, int R, bool WIDE>
-__global__ __launch_bounds__(64 * kWaves, waves_of(NC, GC, R, WIDE)) void k_kv4_attention(kv4_attention_args a) {
+template <int NC, int GC, int R, bool WIDE, int W>
+__global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_attention(kv4_attention_args a) {
   typedef wave_state<NC, GC, R, WIDE> state;
-  constexpr int NG = state::NG, NV = state::NV, D = state::D, ROWS = 16 * R * kWaves;
+  constexpr int NG = state::NG, NV = state::NV, D = state::D, ROWS = W > 4 ? 16 * R : 64 * R;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i = lane & 15, g = lane >> 4;
   const kv4_view &c = a.cache;
@@ -262,8 +255,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(NC, GC, R, WIDE)) void k_kv4_
   const int all_rows = rows.count * rep, row0 = tile * ROWS;  // DBS_KV4_MAX_ROWS keeps them within 31 bits
   if (row0 >= all_rows) return;
   const int have = min(all_rows - row0, ROWS);
-  const int row_waves = have <= 16 * R ? 1 : have <= 32 * R ? 2 : kWaves;
-  const int token_waves = kWaves / row_waves, part = wave % token_waves;
+  const int row_waves = have <= 16 * R ? 1 : have <= 32 * R ? 2 : 4;
+  const int token_waves = W / row_waves, part = wave % token_waves;
   const int wave_row = row0 + wave / token_waves * (16 * R);  // may be behind the last row
 
   // What depends on no length is asked for first: the queries and, without a window, the pages of the first block.
@@ -359,10 +352,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(NC, GC, R, WIDE)) void k_kv4_
     __builtin_memcpy(x.vr, __builtin_assume_aligned(records, 16), 32 * NG);
   };
 
-  block<NC, NG> x;
-  place p = {}, ahead = {};
-  // a block: its scores, the next one's keys on their way, its weights, its values, and the next one's
-  auto attend = [&](auto more) {
+  // A block: its scores, its weights, its values; the codes of the one after the next on their way as registers fall free.
+  auto attend = [&](block<NC, NG> &x, place &p, place &ahead, auto more) {
     f32x4 s[2][R];
     w.scores(x, masks, s);
     if constexpr (decltype(more)::value) load_keys(ahead, x);
@@ -420,6 +411,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(NC, GC, R, WIDE)) void k_kv4_
     }
     w.soften(s);
     w.weigh(x, masks, s);
+    if constexpr (decltype(more)::value) load_values(ahead, x);
     if (__builtin_expect(some != 0u, 0)) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
@@ -440,6 +432,12 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(NC, GC, R, WIDE)) void k_kv4_
     }
   };
   if (next < stop) {
+    // Two blocks on their way, and pages two further ahead.  Behind the last block it is asked for again: a branch there would have
+    // every wait be for all codes that may be on their way.
+    block<NC, NG> x, y;
+    place p, n, p_ahead, n_ahead;
+    const int step = token_waves, last = stop - 1;
+    int count = (stop - next + step - 1) / step;
     if (a.window) {
       p = find(next);
     } else {
@@ -449,17 +447,22 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(NC, GC, R, WIDE)) void k_kv4_
     }
     load_keys(p, x);
     load_values(p, x);
-    // pages one block further ahead than codes; the last block's again behind it
-    ahead = find(min(next + token_waves, stop - 1));
+    n = find(min(next + step, last));
+    load_keys(n, y);
+    load_values(n, y);
+    p_ahead = find(min(next + 2 * step, last));
+    n_ahead = find(min(next + 3 * step, last));
     prepare();
-    // the last block in a copy of its own: a wait for codes has to know what was asked for after them
-    for (next += token_waves; next < stop; next += token_waves) {
-      attend(std::true_type());
-      load_values(ahead, x);
-      p = ahead;
-      ahead = find(min(next + token_waves, stop - 1));
+    for (; count > 1; count -= 2) {
+      attend(x, p, p_ahead, std::true_type());
+      p = p_ahead;
+      attend(y, n, n_ahead, std::true_type());
+      n = n_ahead;
+      next += 2 * step;
+      p_ahead = find(min(next + 2 * step, last));
+      n_ahead = find(min(next + 3 * step, last));
     }
-    attend(std::false_type());
+    if (count) attend(x, p, p_ahead, std::false_type());
   } else {
     prepare();
   }
@@ -470,83 +473,80 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(NC, GC, R, WIDE)) void k_kv4_
     w.sum[r] += __shfl_xor(w.sum[r], 16);
     w.sum[r] += __shfl_xor(w.sum[r], 32);
   }
-  if (token_waves > 1) {
-    __shared__ float shared[kWaves - 1][4 * NV + 2][64];
-    // writers, in the order of their waves: three of one row part, or one of each of two
-    const int slot = token_waves == kWaves ? part - 1 : wave >> 1;
+  // four channels of a row, from 16 n + 4 g on
+  auto write = [&](int r, int n, const f32x4 &o, float sum) {
+    const int row = wave_row + 16 * r + i;
+    if (row >= all_rows) return;
+    const int64_t at_token = rows.first + row / rep;
+    const int at_head = head * rep + row % rep, channel = 16 * n + 4 * g;
+    if (a.splits > 1) {
+      if (sum != 0.0f) __builtin_memcpy(kv4_partial(a, at_token, at_head, D) + channel, &o, 16);
+      return;
+    }
+    if (channel >= a.dim) return;
+    // a row that sees nothing is 0; a sum that is not a number stays one
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (a.out_bf16) {
+      bf16_bits v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = dbs_value<bf16_bits>::of(o[e] * f);
+      __builtin_memcpy((bf16_bits *)a.out + at_token * a.ot + at_head * a.oh + channel, v, 8);
+    } else {
+      const f32x4 v = o * f;
+      __builtin_memcpy((float *)a.out + at_token * a.ot + at_head * a.oh + channel, &v, 16);
+    }
+  };
+  auto write_end = [&](int r, float top, float sum) {
+    const int row = wave_row + 16 * r + i;
+    if (a.splits > 1 && row < all_rows && g == 0) kv4_partial_end(a, rows.first + row / rep, head * rep + row % rep, D, top, sum);
+  };
+  if (token_waves == 1) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (part) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) shared[slot][4 * n + e][lane] = w.o[r][n][e];
-        shared[slot][4 * NV][lane] = w.top[r];
-        shared[slot][4 * NV + 1][lane] = w.sum[r];
-      }
-      __syncthreads();
-      if (!part) {
-        const int from = token_waves == kWaves ? 0 : wave >> 1, count = token_waves - 1;
-        float top = w.top[r];
-        for (int k = 0; k < count; ++k) top = fmaxf(top, shared[from + k][4 * NV][lane]);
-        const float f = __builtin_amdgcn_exp2f(w.top[r] - top);
-        w.sum[r] *= f;
-#pragma unroll
-        for (int n = 0; n < NV; ++n) w.o[r][n] *= f;
-        for (int k = 0; k < count; ++k) {
-          const float h = __builtin_amdgcn_exp2f(shared[from + k][4 * NV][lane] - top);
-          w.sum[r] += h * shared[from + k][4 * NV + 1][lane];
-#pragma unroll
-          for (int n = 0; n < NV; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w.o[r][n][e] += h * shared[from + k][4 * n + e][lane];
-        }
-        w.top[r] = top;
-      }
-      __syncthreads();
+      for (int n = 0; n < NV; ++n) write(r, n, w.o[r][n], w.sum[r]);
+      write_end(r, w.top[r], w.sum[r]);
     }
-    if (part) return;
+    return;
   }
-
+  // the waves that split a row's tokens put theirs into LDS, and join and write a share of the channels each
+  constexpr int HALF = W <= 4 ? NV < 8 ? NV : 8 : W <= 12 ? NV < 4 ? NV : 4 : 2;
+  __shared__ f32x4 shared[W][HALF][64];
+  __shared__ float2 ends[W][64];
+  const int first = wave - part;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = wave_row + 16 * r + i;
-    if (row >= all_rows) continue;
-    const int64_t at_token = rows.first + row / rep;
-    const int at_head = head * rep + row % rep;
-    if (a.splits > 1) {
-      float *to = kv4_partial(a, at_token, at_head, D);
-      if (w.sum[r] != 0.0f) {
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int n = 0; n < NV; ++n) __builtin_memcpy(to + 16 * n + 4 * g, &w.o[r][n], 16);
+    for (int half = 0; half < NV; half += HALF) {
+      if (r + half) __syncthreads();
+#pragma unroll
+      for (int n = 0; n < HALF; ++n)
+        if (half + n < NV) shared[wave][n][lane] = w.o[r][half + n];
+      ends[wave][lane] = make_float2(w.top[r], w.sum[r]);
+      __syncthreads();
+      float top = kLow, sum = 0.0f, f[W];
+#pragma unroll
+      for (int k = 0; k < W; ++k) top = fmaxf(top, ends[k < token_waves ? first + k : wave][lane].x);
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float2 e = ends[k < token_waves ? first + k : wave][lane];
+        f[k] = k < token_waves ? __builtin_amdgcn_exp2f(e.x - top) : 0.0f;
+        if (k < token_waves) sum += f[k] * e.y;
       }
-      if (g == 0) kv4_partial_end(a, at_token, at_head, D, w.top[r], w.sum[r]);
-      continue;
-    }
-    // a row that sees nothing is 0; a sum that is not a number stays one
-    const float f = w.sum[r] == 0.0f ? 0.0f : 1.0f / w.sum[r];
+      for (int n = part; n < HALF && half + n < NV; n += token_waves) {
+        f32x4 o = f[0] * shared[first][n][lane];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int channel = 16 * n + 4 * g;
-      if (channel >= a.dim) continue;
-      if (a.out_bf16) {
-        bf16_bits v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = dbs_value<bf16_bits>::of(w.o[r][n][e] * f);
-        __builtin_memcpy((bf16_bits *)a.out + at_token * a.ot + at_head * a.oh + channel, v, 8);
-      } else {
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = w.o[r][n][e] * f;
-        __builtin_memcpy((float *)a.out + at_token * a.ot + at_head * a.oh + channel, v, 16);
+        for (int k = 1; k < W; ++k)
+          if (k < token_waves) o += f[k] * shared[first + k][n][lane];
+        write(r, half + n, o, sum);
       }
+      if (half == 0 && part == 0) write_end(r, top, sum);
     }
-  }
 }
 
-template <int NC, int GC, int R, bool WIDE>
+template <int NC, int GC, int R, bool WIDE, int W = 4>
 hipError_t launch(const kv4_attention_args &a, dim3 grid, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv4_attention<NC, GC, R, WIDE>), grid, dim3(64 * kWaves), 0, s, a);
+  hipLaunchKernelGGL((k_kv4_attention<NC, GC, R, WIDE, W>), grid, dim3(64 * W), 0, s, a);
   return DBS_NOTE(hipGetLastError());
 }
 

@@ -362,22 +362,32 @@ hipError_t launch_prompt(const kv4_attention_args &a, dim3 grid, hipStream_t s) 
   return DBS_NOTE(hipGetLastError());
 }
 
+template <int NC, int GC, bool WIDE>
+hipError_t launch_few(const kv4_attention_args &a, int tiles, int share, dim3 grid, hipStream_t s) {
+  constexpr int waves = kv4_waves(NC, GC, 1, WIDE);
+  if constexpr (NC <= 4)
+    if (tiles == 2) return launch<NC, GC, 2, WIDE>(a, grid, s);
+  if constexpr (waves > 1) {
+    if (share == 1) return launch<NC, GC, 1, WIDE, 4 * waves>(a, grid, s);
+    if (share == 2 && waves > 2) return launch<NC, GC, 1, WIDE, 2 * waves>(a, grid, s);
+  }
+  return launch<NC, GC, 1, WIDE>(a, grid, s);
+}
+
 template <int NC, int GC>
-hipError_t launch(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s) {
+hipError_t launch(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s) {
   if constexpr (NC % GC == 0) {
     if (tiles == 4) return wide ? launch_prompt<NC, GC, true>(a, grid, s) : launch_prompt<NC, GC, false>(a, grid, s);
-    if constexpr (NC <= 6)
-      if (tiles == 2) return wide ? launch<NC, GC, 2, true>(a, grid, s) : launch<NC, GC, 2, false>(a, grid, s);
-    if (tiles == 1) return wide ? launch<NC, GC, 1, true>(a, grid, s) : launch<NC, GC, 1, false>(a, grid, s);
+    return wide ? launch_few<NC, GC, true>(a, tiles, share, grid, s) : launch_few<NC, GC, false>(a, tiles, share, grid, s);
   }
   return hipErrorInvalidValue;
 }
 
 template <int NC>
-hipError_t launch(const kv4_attention_args &a, int tiles, bool wide, dim3 grid, hipStream_t s) {
-  if (a.group == 32) return launch<NC, 1>(a, tiles, wide, grid, s);
-  if (a.group == 64) return launch<NC, 2>(a, tiles, wide, grid, s);
-  return launch<NC, 4>(a, tiles, wide, grid, s);
+hipError_t launch(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s) {
+  if (a.group == 32) return launch<NC, 1>(a, tiles, share, wide, grid, s);
+  if (a.group == 64) return launch<NC, 2>(a, tiles, share, wide, grid, s);
+  return launch<NC, 4>(a, tiles, share, wide, grid, s);
 }
 
 }  // namespace kv4
