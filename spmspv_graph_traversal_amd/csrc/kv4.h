@@ -34,8 +34,7 @@ struct kv4_layout {
 // Waves of a SIMD that the kernel for few rows is made to hold, r tiles of 16 rows a wave, heads of 32 nc channels in groups of
 // 32 gc: as many as spill no register, since a spilled one's load waits for all codes that are on their way.
 constexpr int kv4_waves(int nc, int gc, int r, bool wide) {
-  const int parts = wide ? 2 : 1, blocks = 2 * (4 * nc + 10 * (nc / gc));
-  const int need = 8 * nc * r + 4 * nc * r * parts + blocks + 12 * r * parts + 8 * (r - 1) + 56;
+  const int need = 8 * nc * r + 4 * nc * r * (wide ? 2 : 1) + 4 * nc + 18 * (nc / gc) + 12 * r + 35;  // output, queries, codes, records, scores
   return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
 }
 

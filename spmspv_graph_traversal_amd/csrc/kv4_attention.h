@@ -352,20 +352,20 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
     __builtin_memcpy(x.vr, __builtin_assume_aligned(records, 16), 32 * NG);
   };
 
-  // A block: its scores, its weights, its values; the codes of the one after the next on their way as registers fall free.
-  auto attend = [&](block<NC, NG> &x, place &p, place &ahead, auto more) {
+  // A block: its scores, its weights, its values; the next one's codes on their way as registers fall free.
+  block<NC, NG> x;
+  place p, ahead;
+  auto attend = [&] {
     f32x4 s[2][R];
     w.scores(x, masks, s);
-    if constexpr (decltype(more)::value) load_keys(ahead, x);
+    load_keys(ahead, x);
     const int j = p.token;
-    const bool whole = p.page[0] >= 0 && p.page[1] >= 0 && j + KV4_BLOCK - 1 <= low &&
-                       (!a.window || j > high - a.window || j + KV4_BLOCK <= a.sinks);
-    // bit t: the row at `position` sees token j + t
-    auto seen = [&](int position) {
+    // bit t: a row at `position` sees token j + t, one whose window begins with that of a row at `from`
+    auto seen = [&](int position, int from) {
       uint32_t see = position < j ? 0u : position - j >= 31 ? ~0u : (2u << (position - j)) - 1u;
       if (a.window) {
-        const int from = position - a.window + 1 - j, sinks = a.sinks - j;  // from bit `from` on, or below bit `sinks`
-        uint32_t in = from <= 0 ? ~0u : from >= 32 ? 0u : ~((1u << from) - 1u);
+        const int begin = from - a.window + 1 - j, sinks = a.sinks - j;
+        uint32_t in = begin <= 0 ? ~0u : begin >= 32 ? 0u : ~((1u << begin) - 1u);
         in |= sinks <= 0 ? 0u : sinks >= 32 ? ~0u : (1u << sinks) - 1u;
         see &= in;
       }
@@ -373,51 +373,60 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
       if (p.page[1] < 0) see &= 0x0000FFFFu;
       return see;
     };
+    const bool whole = p.page[0] >= 0 && p.page[1] >= 0 && j + KV4_BLOCK - 1 <= low &&
+                       (!a.window || j > high - a.window || j + KV4_BLOCK <= a.sinks);
     uint32_t bad[NG], some = 0u;  // the same in all lanes
-    if (__builtin_expect(!whole, 0)) {
-      uint32_t any = 0u;
+    if (!whole) {
+      uint32_t wrong = 0u;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const uint32_t see = seen(w.position[r]);
-        any |= see;
+        const uint32_t see = seen(w.position[r], w.position[r]) >> (8 * g);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!(see >> (8 * g) >> (4 * t + e) & 1u)) s[t][r][e] = -INFINITY;
+            if (!(see >> (4 * t + e) & 1u)) s[t][r][e] = -INFINITY;
       }
-      for (int o = 1; o < 16; o <<= 1) any |= (uint32_t)__shfl_xor((int)any, o);
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wrong |= (x.vr[n][e] & 0x7C007C00u) + 0x04000400u;  // an exponent of ones carries into the sign
       // Nothing times a value that is not finite would be NaN: values that no row sees become 0, and one that is not finite and
       // that some rows see is added to those alone.
+      if (__builtin_expect(__any((wrong & 0x80008000u) != 0u), 0)) {
+        const uint32_t any = seen(high, low);
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        uint32_t mask = 0u;
+        for (int n = 0; n < NG; ++n) {
+          uint32_t mask = 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t &sc = x.vr[n][e], &of = x.vr[n][4 + e];
-            const int bit = 8 * g + e + 4 * h;
-            const uint32_t half = h ? 0xFFFF0000u : 0x0000FFFFu;
-            const bool see = any >> bit & 1u, wrong = not_finite(sc & half) || not_finite(of & half);
-            if (see && wrong) mask |= 1u << bit;
-            if (!see || wrong) sc &= ~half, of &= ~half;
-          }
-        mask |= (uint32_t)__shfl_xor((int)mask, 16);
-        mask |= (uint32_t)__shfl_xor((int)mask, 32);
-        bad[n] = (uint32_t)__builtin_amdgcn_readfirstlane((int)mask);
-        some |= bad[n];
+            for (int h = 0; h < 2; ++h) {
+              uint32_t &sc = x.vr[n][e], &of = x.vr[n][4 + e];
+              const uint32_t bit = 1u << (8 * g + e + 4 * h), half = h ? 0xFFFF0000u : 0x0000FFFFu;
+              if (!not_finite(sc & half) && !not_finite(of & half)) continue;
+              mask |= any & bit;
+              sc &= ~half;
+              of &= ~half;
+            }
+          mask |= (uint32_t)__shfl_xor((int)mask, 16);
+          mask |= (uint32_t)__shfl_xor((int)mask, 32);
+          bad[n] = (uint32_t)__builtin_amdgcn_readfirstlane((int)mask);
+          some |= bad[n];
+        }
       }
     }
     w.soften(s);
     w.weigh(x, masks, s);
-    if constexpr (decltype(more)::value) load_values(ahead, x);
+    load_values(ahead, x);
     if (__builtin_expect(some != 0u, 0)) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
+        const uint32_t see = seen(w.position[r], w.position[r]);
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-          if (bad[n / (2 * GC)] & seen(w.position[r])) w.o[r][n] += NAN;
+          if (bad[n / (2 * GC)] & see) w.o[r][n] += NAN;
+      }
     }
   };
 
@@ -432,12 +441,6 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
     }
   };
   if (next < stop) {
-    // Two blocks on their way, and pages two further ahead.  Behind the last block it is asked for again: a branch there would have
-    // every wait be for all codes that may be on their way.
-    block<NC, NG> x, y;
-    place p, n, p_ahead, n_ahead;
-    const int step = token_waves, last = stop - 1;
-    int count = (stop - next + step - 1) / step;
     if (a.window) {
       p = find(next);
     } else {
@@ -447,22 +450,15 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
     }
     load_keys(p, x);
     load_values(p, x);
-    n = find(min(next + step, last));
-    load_keys(n, y);
-    load_values(n, y);
-    p_ahead = find(min(next + 2 * step, last));
-    n_ahead = find(min(next + 3 * step, last));
+    // Pages one block further ahead than codes.  Behind the last block it is asked for again: a branch there would have every wait be
+    // for all codes that may be on their way, and a copy of the block for the last one would not fit the instruction cache as well.
+    ahead = find(min(next + token_waves, stop - 1));
     prepare();
-    for (; count > 1; count -= 2) {
-      attend(x, p, p_ahead, std::true_type());
-      p = p_ahead;
-      attend(y, n, n_ahead, std::true_type());
-      n = n_ahead;
-      next += 2 * step;
-      p_ahead = find(min(next + 2 * step, last));
-      n_ahead = find(min(next + 3 * step, last));
+    for (; next < stop; next += token_waves) {
+      attend();
+      p = ahead;
+      ahead = find(min(next + 2 * token_waves, stop - 1));
     }
-    if (count) attend(x, p, p_ahead, std::false_type());
   } else {
     prepare();
   }
