@@ -57,7 +57,11 @@ struct kv4_rows {
   int position;                // of the first one, negative where the cache holds fewer tokens than are new
 };
 
-DBS_DEV int kv4_new_ptr(const kv4_view &c, int b) { return min(max(c.new_ptr[b], 0), c.tokens); }
+// Tables and lists, which nothing writes while a kernel runs: read as constants, so that what all lanes read alike is a scalar load
+// behind stores too.
+DBS_DEV int kv4_list(const int32_t *p, int64_t at) { return ((const __attribute__((address_space(4))) int32_t *)(uintptr_t)p)[at]; }
+
+DBS_DEV int kv4_new_ptr(const kv4_view &c, int b) { return min(max(kv4_list(c.new_ptr, b), 0), c.tokens); }
 
 DBS_DEV kv4_rows kv4_rows_of(const kv4_view &c, int b) {
   kv4_rows r;
@@ -65,7 +69,7 @@ DBS_DEV kv4_rows kv4_rows_of(const kv4_view &c, int b) {
   r.first = c.new_ptr ? kv4_new_ptr(c, b) : b * c.each;
   r.count = c.new_ptr ? max(kv4_new_ptr(c, b + 1) - r.first, 0) : c.each;
   const int most = c.width << c.page_shift;
-  r.position = min(max(c.lens[b], 0), most) - r.count;
+  r.position = min(max(kv4_list(c.lens, b), 0), most) - r.count;
   return r;
 }
 
@@ -89,7 +93,7 @@ DBS_DEV int kv4_find(const kv4_view &c, int64_t u, int times, int per, int extra
 DBS_DEV uint8_t *kv4_page(const kv4_view &c, int b, int token, int64_t head_offset) {
   const int at = token >> c.page_shift;
   if (token < 0 || at >= c.width) return nullptr;
-  const int page = c.table[b * c.ldtable + at];
+  const int page = kv4_list(c.table, b * c.ldtable + at);
   if ((unsigned)page >= (unsigned)c.pages) return nullptr;
   return c.pool + page * c.page_stride + head_offset;
 }

@@ -275,7 +275,7 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
   int early[2] = {-1, -1};
   if (c.width > 0)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) early[h] = table[min((token0 + 16 * h) >> c.page_shift, c.width - 1)];
+    for (int h = 0; h < 2; ++h) early[h] = kv4_list(table, min((token0 + 16 * h) >> c.page_shift, c.width - 1));
 
   // the tokens that the wave's rows see: those below `end` from `start` on, and of the first ones `sink_blocks` blocks
   const int first_token = wave_row / rep, last_token = (min(all_rows, wave_row + 16 * R) - 1) / rep;
@@ -306,50 +306,49 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
     p.token = token_of(n);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int page = table[min((p.token + 16 * h) >> c.page_shift, c.width - 1)];
+      const int page = kv4_list(table, min((p.token + 16 * h) >> c.page_shift, c.width - 1));
       p.page[h] = p.token + 16 * h < end && (unsigned)page < (unsigned)c.pages ? page : -1;
     }
     return p;
   };
-  // A half without a page reads the pool's first, and nobody sees what it read.  A lane's rows of a half: of its key tokens (4 apart)
-  // and of its eight value tokens; where pages have 32 tokens and more both halves are of one page, and addresses one base and
-  // a lane's constant.
-  const int k_row = 8 * ((i >> 2) & 1) + (i & 3), k_half = i >> 3, v_half = g >> 1;
+  // A half without a page reads the pool's first, and nobody sees what it read.  Codes of keys and of values have as many bytes a
+  // token, and so have their records: two bases and a lane's constants reach all four.  Where pages have 32 tokens and more both
+  // halves are of one page, and the bases are the same for all lanes.
   const bool one_page = c.page_shift >= 5;
-  auto base_of = [&](const place &p, int h) { return c.pool + (int64_t)max(p.page[h], 0) * c.page_stride + head_offset; };
-  auto row_of = [&](const place &p, int h) { return (p.token + 16 * h) & page_mask; };
-  auto load_keys = [&](const place &p, block<NC, NG> &x) {
+  const int k_half = i >> 3, v_half = g >> 1, k_row = 8 * ((i >> 2) & 1) + (i & 3), v_row = 8 * (g & 1);
+  const int k_from = k_row + (one_page ? 16 * k_half : 0), v_from = v_row + (one_page ? 16 * v_half : 0);  // tokens from the base
+  const uint32_t k_codes = k_from * (D / 2) + g * (4 * NC), k_records = lay.key_records + k_from * (4 * NG);
+  const uint32_t v_codes = lay.value_codes + v_from * (D / 2) + i * (8 * NC), v_records = lay.value_records + v_from * (4 * NG);
+  struct bases {
     const uint8_t *codes, *records;
-    if (one_page) {
-      const uint8_t *const base = base_of(p, 0);
-      codes = base + row_of(p, 0) * (D / 2) + (uint32_t)((16 * k_half + k_row) * (D / 2) + g * (4 * NC));
-      records = base + lay.key_records + row_of(p, 0) * (4 * NG) + (uint32_t)((16 * k_half + k_row) * (4 * NG));
-    } else {
-      const uint8_t *const base = k_half ? base_of(p, 1) : base_of(p, 0);
-      const int row = (k_half ? row_of(p, 1) : row_of(p, 0)) + k_row;
-      codes = base + row * (D / 2) + g * (4 * NC);
-      records = base + lay.key_records + row * (4 * NG);
-    }
+  };
+  auto bases_of = [&](const place &p, int h) {
+    const uint8_t *const page = c.pool + (int64_t)max(p.page[h], 0) * c.page_stride + head_offset;
+    const int row = (p.token + 16 * h) & page_mask;
+    return bases{page + row * (D / 2), page + row * (4 * NG)};
+  };
+  auto lane_bases = [&](const place &p, int half) {
+    const bases lo = bases_of(p, 0), hi = bases_of(p, 1);
+    return bases{half ? hi.codes : lo.codes, half ? hi.records : lo.records};
+  };
+  auto get_keys = [&](const bases &p, block<NC, NG> &x) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      __builtin_memcpy(x.k[t], __builtin_assume_aligned(codes + t * (2 * D), NC == 3 ? 4 : NC % 4 ? 8 : 16), 4 * NC);
-      __builtin_memcpy(x.kr[t], __builtin_assume_aligned(records + t * (16 * NG), NG % 4 ? NG % 2 ? 4 : 8 : 16), 4 * NG);
+      __builtin_memcpy(x.k[t], __builtin_assume_aligned(p.codes + k_codes + t * (2 * D), NC == 3 ? 4 : NC % 4 ? 8 : 16), 4 * NC);
+      __builtin_memcpy(x.kr[t], __builtin_assume_aligned(p.records + k_records + t * (16 * NG), NG % 4 ? NG % 2 ? 4 : 8 : 16), 4 * NG);
     }
   };
+  auto get_values = [&](const bases &p, block<NC, NG> &x) {
+    __builtin_memcpy(x.v, __builtin_assume_aligned(p.codes + v_codes, NC % 2 ? 8 : 16), 8 * NC);
+    __builtin_memcpy(x.vr, __builtin_assume_aligned(p.records + v_records, 16), 32 * NG);
+  };
+  auto load_keys = [&](const place &p, block<NC, NG> &x) {
+    if (one_page) get_keys(bases_of(p, 0), x);
+    else get_keys(lane_bases(p, k_half), x);
+  };
   auto load_values = [&](const place &p, block<NC, NG> &x) {
-    const uint8_t *codes, *records;
-    if (one_page) {
-      const uint8_t *const base = base_of(p, 0);
-      codes = base + lay.value_codes + row_of(p, 0) * (D / 2) + (uint32_t)(g * (4 * D) + i * (8 * NC));
-      records = base + lay.value_records + row_of(p, 0) * (4 * NG) + (uint32_t)(g * (32 * NG));
-    } else {
-      const uint8_t *const base = v_half ? base_of(p, 1) : base_of(p, 0);
-      const int eight = ((v_half ? row_of(p, 1) : row_of(p, 0)) >> 3) + (g & 1);
-      codes = base + lay.value_codes + eight * (4 * D) + i * (8 * NC);
-      records = base + lay.value_records + eight * (32 * NG);
-    }
-    __builtin_memcpy(x.v, __builtin_assume_aligned(codes, NC % 2 ? 8 : 16), 8 * NC);
-    __builtin_memcpy(x.vr, __builtin_assume_aligned(records, 16), 32 * NG);
+    if (one_page) get_values(bases_of(p, 0), x);
+    else get_values(lane_bases(p, v_half), x);
   };
 
   // A block: its scores, its weights, its values; the next one's codes on their way as registers fall free.

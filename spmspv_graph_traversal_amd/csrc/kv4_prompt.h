@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
   const code_masks masks;
   auto page_of = [&](int token) {
     const int at = token >> c.page_shift;
-    return token < end && at < c.width ? c.table[b * c.ldtable + at] : -1;
+    return token < end && at < c.width ? kv4_list(c.table, b * c.ldtable + at) : -1;
   };
   auto page_at = [&](int page) { return c.pool + ((unsigned)page < (unsigned)c.pages ? page : 0) * c.page_stride + head_offset; };
   auto group_of = [&](int e) { return T::kAligned ? e / (2 * GC) : (vj * KW + e) / (2 * GC) - vj * KW / (2 * GC); };
