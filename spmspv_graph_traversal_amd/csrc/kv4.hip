@@ -18,15 +18,15 @@ struct kv4_side {
  * codes rint((x - b) / s) within 0..15, each step in fp32 and with products by reciprocals, so that the codes are
  * reproducible bit by bit.  A group with a value beyond DBS_KV4_MAX_VALUE is NaN throughout.
  *
- * A workgroup takes the new ones of eight tokens that share words of the value codes, for one key head: lanes along the
- * channels, eight to a lane, keys in the first half of the workgroup and values in the second.  Words of tokens that were
- * there before are read and kept.  Only this workgroup writes these words, so nothing is atomic.
+ * A workgroup takes the new ones of eight tokens that share words of the value codes, one key head after the other: lanes along
+ * the channels, eight to a lane, keys in the first half of the workgroup and values in the second; the next head's are on their
+ * way meanwhile.  Words of tokens that were there before are read and kept.  Only this workgroup writes these words, so nothing is
+ * atomic.  Few tokens have a workgroup for each head, many share the chain of list, length and page among `per` heads.
  */
 template <class X, class Y>
-__global__ void k_kv4_store(kv4_view c, int dim, int padded, int group, kv4_side key, kv4_side value) {
-  __shared__ uint32_t codes[8][KV4_MAX_DIM / 8 + 1];
+__global__ __launch_bounds__(512) void k_kv4_store(kv4_view c, int heads, int per, int dim, int padded, int group, kv4_side key, kv4_side value) {
+  __shared__ uint32_t codes[2][8][KV4_MAX_DIM / 8 + 1];
   const int64_t unit = blockIdx.x;
-  const int head = blockIdx.y;
   int b, nth;
   if (c.new_ptr) {
     b = kv4_find(c, unit, 1, 8, 2);
@@ -45,83 +45,92 @@ __global__ void k_kv4_store(kv4_view c, int dim, int padded, int group, kv4_side
   const int lanes = padded / 8, side = threadIdx.x >= 8 * lanes;
   const int e = threadIdx.x / lanes - 8 * side, l = threadIdx.x % lanes, channel = 8 * l;
   const int t = from + e - rows.position;  // the token among the new ones
-  const bool is_new = t >= 0 && t < rows.count;
+  const bool is_new = t >= 0 && t < rows.count, in = is_new && channel < dim;
   const kv4_layout lay(padded, group, 1 << c.page_shift);
-  uint8_t *const page = kv4_page(c, b, from, (int64_t)head * lay.head_bytes);
   const kv4_side &to = side ? value : key;
   const int64_t row = rows.first + t;
-
-  float x[8];
-  const bool in = is_new && channel < dim;
-  if (in) {
-    X v[8];
-    __builtin_memcpy(v, (const X *)to.x + row * to.xt + head * to.xh + channel, sizeof v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = dbs_value<X>::load(&v[i]);
-  }
-  float low = INFINITY, high = -INFINITY;
-  bool bad = false;
-  if (in) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      low = fminf(low, x[i]);
-      high = fmaxf(high, x[i]);
-      bad |= !(fabsf(x[i]) <= DBS_KV4_MAX_VALUE);
-    }
-  }
-  for (int o = 1; o < group / 8; o <<= 1) {
-    low = fminf(low, __shfl_xor(low, o));
-    high = fmaxf(high, __shfl_xor(high, o));
-    bad |= __shfl_xor((int)bad, o) != 0;
-  }
-  if (low > high) low = high = 0.0f;  // no channel of the head
-  _Float16 of = (_Float16)low;
-  _Float16 sc = (_Float16)fmaxf((high - (float)of) * (1.0f / 15.0f), 0.0f);
-  if (bad) of = sc = (_Float16)NAN;
-  const float step = (float)sc, base = (float)of, inverse = step > 0.0f ? 1.0f / step : 0.0f;
-  uint32_t word = 0u;
-  if (in) {
-    Y y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = bad ? 0.0f : fminf(fmaxf(rintf((x[i] - base) * inverse), 0.0f), 15.0f);
-      word |= (uint32_t)q << (4 * i);
-      y[i] = dbs_value<Y>::of((float)(_Float16)__builtin_fmaf(step, q, base));
-    }
-    if (to.y) __builtin_memcpy((Y *)to.y + row * to.yt + head * to.yh + channel, y, sizeof y);
-  }
+  const int head0 = blockIdx.y * per, head1 = min(head0 + per, heads);
+  const auto load = [&](int head, X (&v)[8]) {
+    if (in) __builtin_memcpy(v, (const X *)to.x + row * to.xt + head * to.xh + channel, sizeof v);
+  };
+  X now[8], next[8];
+  load(head0, now);
+  uint8_t *page = kv4_page(c, b, from, (int64_t)head0 * lay.head_bytes);
   const int slot = from & ((1 << c.page_shift) - 1);
   const bool first = channel % group == 0;
-  uint16_t bits[2];
-  __builtin_memcpy(&bits[0], &sc, 2);
-  __builtin_memcpy(&bits[1], &of, 2);
-  if (page && is_new && !side) {
-    // channels 32 k + 8 g .. + 7 are word g (d / 32) + k
-    ((uint32_t *)(page + (slot + e) * (padded / 2)))[(l & 3) * (padded / 32) + (l >> 2)] = word;
-    if (first) ((uint32_t *)(page + lay.key_records))[(slot + e) * lay.groups + channel / group] = bits[0] | (uint32_t)bits[1] << 16;
-  }
-  if (side) {
-    codes[e][l] = word;
-    if (page && is_new && first) {
-      uint16_t *r = (uint16_t *)(page + lay.value_records) + ((slot >> 3) * lay.groups + channel / group) * 16 + kv4_place(e);
-      r[0] = bits[0];
-      r[8] = bits[1];
-    }
-  }
-  __syncthreads();
-  if (!page) return;
-  // a word of the value codes to a thread: nibble e is token e's
+  // nibble e of a word of the value codes is token e's
   uint32_t news = 0u;
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     if (from + k >= rows.position && from + k < rows.position + rows.count) news |= 15u << (4 * k);
-  uint32_t *words = (uint32_t *)(page + lay.value_codes) + (slot >> 3) * padded;
-  for (int i = threadIdx.x; i < padded; i += blockDim.x) {
-    const int ch = 16 * (i % (padded / 16)) + i / (padded / 16);
-    uint32_t w = 0u;
+
+  for (int head = head0; head < head1; ++head) {
+    if (head + 1 < head1) load(head + 1, next);
+    float x[8], low = INFINITY, high = -INFINITY;
+    bool bad = false;
+    if (in) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w |= (codes[k][ch >> 3] >> (4 * (ch & 7)) & 15u) << (4 * k);
-    words[i] = news == ~0u ? w : (words[i] & ~news) | (w & news);
+      for (int i = 0; i < 8; ++i) {
+        x[i] = dbs_value<X>::load(&now[i]);
+        low = fminf(low, x[i]);
+        high = fmaxf(high, x[i]);
+        bad |= !(fabsf(x[i]) <= DBS_KV4_MAX_VALUE);
+      }
+    }
+    for (int o = 1; o < group / 8; o <<= 1) {
+      low = fminf(low, __shfl_xor(low, o));
+      high = fmaxf(high, __shfl_xor(high, o));
+      bad |= __shfl_xor((int)bad, o) != 0;
+    }
+    if (low > high) low = high = 0.0f;  // no channel of the head
+    _Float16 of = (_Float16)low;
+    _Float16 sc = (_Float16)fmaxf((high - (float)of) * (1.0f / 15.0f), 0.0f);
+    if (bad) of = sc = (_Float16)NAN;
+    const float step = (float)sc, base = (float)of, inverse = step > 0.0f ? 1.0f / step : 0.0f;
+    uint32_t word = 0u;
+    if (in) {
+      Y y[8];
+      float stands[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float q = bad ? 0.0f : fminf(fmaxf(rintf((x[i] - base) * inverse), 0.0f), 15.0f);
+        word |= (uint32_t)q << (4 * i);
+        stands[i] = (float)(_Float16)__builtin_fmaf(step, q, base);
+      }
+      dbs_round(y, stands);
+      if (to.y) __builtin_memcpy((Y *)to.y + row * to.yt + head * to.yh + channel, y, sizeof y);
+    }
+    uint16_t bits[2];
+    __builtin_memcpy(&bits[0], &sc, 2);
+    __builtin_memcpy(&bits[1], &of, 2);
+    if (page && is_new && !side) {
+      // channels 32 k + 8 g .. + 7 are word g (d / 32) + k
+      ((uint32_t *)(page + (slot + e) * (padded / 2)))[(l & 3) * (padded / 32) + (l >> 2)] = word;
+      if (first) ((uint32_t *)(page + lay.key_records))[(slot + e) * lay.groups + channel / group] = bits[0] | (uint32_t)bits[1] << 16;
+    }
+    uint32_t (&words)[8][KV4_MAX_DIM / 8 + 1] = codes[(head - head0) & 1];
+    if (side) {
+      words[e][l] = word;
+      if (page && is_new && first) {
+        uint16_t *r = (uint16_t *)(page + lay.value_records) + ((slot >> 3) * lay.groups + channel / group) * 16 + kv4_place(e);
+        r[0] = bits[0];
+        r[8] = bits[1];
+      }
+    }
+    __syncthreads();  // one a head: the next head's words go to the other buffer
+    if (page) {
+      uint32_t *out = (uint32_t *)(page + lay.value_codes) + (slot >> 3) * padded;
+      for (int i = threadIdx.x; i < padded; i += blockDim.x) {
+        const int ch = 16 * (i % (padded / 16)) + i / (padded / 16);
+        uint32_t w = 0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w |= (words[k][ch >> 3] >> (4 * (ch & 7)) & 15u) << (4 * k);
+        out[i] = news == ~0u ? w : (out[i] & ~news) | (w & news);
+      }
+      page += lay.head_bytes;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) now[i] = next[i];
   }
 }
 
@@ -199,7 +208,8 @@ __global__ __launch_bounds__(1024) void k_kv4_combine(kv4_view c, int heads, int
   const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
   Y y[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) y[k] = dbs_value<Y>::of(v[k] * f);
+  for (int k = 0; k < 4; ++k) v[k] *= f;
+  dbs_round(y, v);
   __builtin_memcpy(out + t * ot + h * oh + 4 * lane, y, sizeof y);
 }
 
@@ -409,8 +419,10 @@ dbs_status dbs_kv4_store(const dbs_kv4_cache *a, int32_t tokens, const void *k, 
   const kv4_side ks = {k, kt, kh, k_out, kot, koh}, vs = {v, vt, vh, v_out, vot, voh};
   const auto run = x_dtype == DBS_F32 ? (out_dtype == DBS_F32 ? k_kv4_store<float, float> : k_kv4_store<float, bf16_bits>)
                                       : (out_dtype == DBS_F32 ? k_kv4_store<bf16_bits, float> : k_kv4_store<bf16_bits, bf16_bits>);
-  hipLaunchKernelGGL(run, dim3((unsigned)units, (unsigned)h), dim3(2 * padded), 0, (hipStream_t)stream, c, a->head_dim, padded, a->group,
-                     ks, vs);
+  int64_t per = units * h / 2048;  // heads of a workgroup, so that the card holds all workgroups at once
+  per = per < 1 ? 1 : per > h ? h : per;
+  hipLaunchKernelGGL(run, dim3((unsigned)units, (unsigned)((h + per - 1) / per)), dim3(2 * padded), 0, (hipStream_t)stream, c, (int)h, (int)per,
+                     a->head_dim, padded, a->group, ks, vs);
   return DBS_NOTE(hipGetLastError()) == hipSuccess ? DBS_OK : DBS_ERR_DEVICE;
 }
 

@@ -331,15 +331,14 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
     for (int r = 0; r < 4; ++r) {
       const int channel = 32 * n + 8 * r + 4 * h;
       if (channel >= a.dim) continue;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = o[n][4 * r + e] * f;
       if (a.out_bf16) {
-        bf16_bits v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = dbs_value<bf16_bits>::of(o[n][4 * r + e] * f);
-        __builtin_memcpy((bf16_bits *)a.out + at_token * a.ot + at_head * a.oh + channel, v, 8);
+        bf16_bits y[4];
+        dbs_round(y, v);
+        __builtin_memcpy((bf16_bits *)a.out + at_token * a.ot + at_head * a.oh + channel, y, 8);
       } else {
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = o[n][4 * r + e] * f;
         __builtin_memcpy((float *)a.out + at_token * a.ot + at_head * a.oh + channel, v, 16);
       }
     }

@@ -25,6 +25,22 @@ struct dbs_value<bf16_bits> {
   }
 };
 
+// Values rounded to the type, to nearest with ties to even, two bf16 to an instruction (dbs_value::of takes six for one).
+template <int W>
+DBS_DEV void dbs_round(float (&to)[W], const float (&v)[W]) {
+#pragma unroll
+  for (int e = 0; e < W; ++e) to[e] = v[e];
+}
+template <int W>
+DBS_DEV void dbs_round(bf16_bits (&to)[W], const float (&v)[W]) {
+  typedef float wide __attribute__((ext_vector_type(W)));
+  typedef __bf16 narrow __attribute__((ext_vector_type(W)));
+  wide w;
+  __builtin_memcpy(&w, v, sizeof v);
+  const narrow n = __builtin_convertvector(w, narrow);
+  __builtin_memcpy(to, &n, sizeof to);
+}
+
 inline bool dbs_is_vector_dtype(int dtype) { return dtype == DBS_F32 || dtype == DBS_BF16; }
 inline int64_t dbs_vector_size(int dtype) { return dtype == DBS_F32 ? 4 : 2; }
 
