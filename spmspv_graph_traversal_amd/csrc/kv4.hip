@@ -301,7 +301,7 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
   const int rep = heads / a->key_heads, d = kv4_padded(a->head_dim), nc = d / 32, gc = a->group / 32;
   const int64_t rows = (int64_t)tokens * rep, each = (rows + a->sequences - 1) / a->sequences;
   // two tiles a wave of larger heads leave no registers
-  p.tiles = each <= 16 ? 1 : each <= 64 && d <= 128 ? 2 : 4;
+  p.tiles = each <= 16 ? 1 : each <= 64 && d <= 128 ? 2 : each >= 512 && !wide && (d == 64 || d == 128) ? 8 : 4;
   int64_t slots = (int64_t)a->table_pages * a->page_tokens;
   if (max_len > 0 && max_len < slots) slots = max_len;
   const auto cut = [&](int per) {  // workgroups of `per` rows
@@ -316,7 +316,7 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
     }
     return blocks;
   };
-  const int waves = p.tiles == 4 ? 2 : kv4_waves(nc, gc, p.tiles, wide);
+  const int waves = p.tiles >= 4 ? 2 : kv4_waves(nc, gc, p.tiles, wide);
   p.splits = 1;
   if (p.tiles == 1 && waves > 1) {
     // All waves of a compute unit, or of half of one, for a key head's rows: where few blocks leave less to win by splits
@@ -328,14 +328,14 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
       return p;
     }
   }
-  const int per = p.tiles == 4 ? 128 : 64 * p.tiles;
+  const int per = p.tiles >= 4 ? 32 * p.tiles : 64 * p.tiles;
   cut(per);
   const int64_t blocks = blocks_of(per), groups = p.units * a->key_heads;
   int64_t splits = 1;
-  if (p.tiles == 4) {
+  if (p.tiles >= 4) {
     // Splits pay where they fill the card's last round better than the joining of their rows costs: rounds of workgroups in units
     // of a block's time, 1.3 us, in which joining moves 5 MB.
-    const int64_t at_once = units_of_card * (wide || d > 128 ? 1 : 2);
+    const int64_t at_once = units_of_card * (p.tiles == 8 || wide || d > 128 ? 1 : 2);
     double best = 0.0;
     for (int64_t s = 1; s <= 64 && s <= (blocks + 7) / 8; ++s) {
       const int64_t chunk = (blocks + s - 1) / s;

@@ -9,6 +9,9 @@ namespace kv4 {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// kinds of instructions, to __builtin_amdgcn_sched_group_barrier
+constexpr int kSchedVector = 0x2, kSchedMatrix = 0x8, kSchedRead = 0x100;
+
 /*
  * The mathematics of k_kv4_attention for the rows of a prompt, where the matrix cores and the exponentials bound it and not
  * the cache.  A workgroup takes 128 rows, 32 a wave, and goes through the tokens in tiles.  It turns the codes of a tile into halves
@@ -20,11 +23,12 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
  * operand is token (m with bits 2 and 3 exchanged), so that the lane which gets a row's scores of tokens 16 u + 8 h .. + 7 is the
  * one that gives them to the second product.
  */
-template <int NC, int GC, bool WIDE>
+template <int NC, int GC, bool WIDE, int W>
 struct prompt {
   static constexpr int NG = NC / GC, D = 32 * NC, PARTS = WIDE ? 2 : 1;
-  static constexpr int TOKENS = NC <= 4 ? 64 : 32, SB = TOKENS / 32, CUT = 64 / TOKENS, KW = NC / CUT;  // words a thread takes of K and of V
-  static constexpr int ROWS = 128;
+  static constexpr int TOKENS = NC <= 4 ? 64 : 32, SB = TOKENS / 32, CUT = W * 16 / TOKENS, KW = NC / CUT;  // words a thread takes of K and of V
+  static constexpr int ROWS = 32 * W;
+  static_assert(NC % CUT == 0, "whole words");
   static constexpr int kOperands = SB * 2 * NC * 64;  // of K or of V
   static constexpr int kFlags = NG * (TOKENS / 8);    // bytes
   static constexpr size_t kLds = 2 * (2 * kOperands * 16 + (kFlags + 15) / 16 * 16);
@@ -37,9 +41,9 @@ struct prompt {
   };
 };
 
-template <int NC, int GC, bool WIDE>
-__global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_attention_args a) {
-  typedef prompt<NC, GC, WIDE> T;
+template <int NC, int GC, bool WIDE, int W>
+__global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k_kv4_prompt(kv4_attention_args a) {
+  typedef prompt<NC, GC, WIDE, W> T;
   constexpr int NG = T::NG, D = T::D, PARTS = T::PARTS, TOKENS = T::TOKENS, SB = T::SB, KW = T::KW, ROWS = T::ROWS;
   extern __shared__ uint4 lds[];
   half8_t *const operands = (half8_t *)lds;
@@ -114,6 +118,13 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
   auto page_at = [&](int page) { return c.pool + ((unsigned)page < (unsigned)c.pages ? page : 0) * c.page_stride + head_offset; };
   auto group_of = [&](int e) { return T::kAligned ? e / (2 * GC) : (vj * KW + e) / (2 * GC) - vj * KW / (2 * GC); };
 
+  // where its words go among the operands
+  const int m = (kt & 0x13) | ((kt & 8) >> 1) | ((kt & 4) << 1);
+  const int k_to = ((kt >> 5) * 2 * NC + 2 * kp * KW + (kg >> 1)) * 64 + (kg & 1) * 32 + m;
+  auto v_to = [&](int n) {
+    return T::kOperands + (((vt >> 2) * NC + (n >> 1)) * 2 + ((vt >> 1) & 1)) * 64 + (vt & 1) * 32 + (n & 1) * 16 + vc;
+  };
+
   auto load = [&](int token, int k_page, int v_page, typename T::stage &s) {
     const uint8_t *k = page_at(k_page);
     const int at = (token + kt) & page_mask;
@@ -130,11 +141,10 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
       __builtin_memcpy(s.vr[n], __builtin_assume_aligned(v + lay.value_records + (block * NG + min(g + n, NG - 1)) * 32, 16), 32);
   };
   auto put = [&](int buffer, typename T::stage &s) {
-    half8_t *const k = operands + buffer * 2 * T::kOperands, *const v = k + T::kOperands;
-    const int m = (kt & 0x13) | ((kt & 8) >> 1) | ((kt & 4) << 1);
+    half8_t *const to = operands + buffer * 2 * T::kOperands;
 #pragma unroll
     for (int e = 0; e < KW; ++e)
-      k[((kt >> 5) * 2 * NC + 2 * (kp * KW + e) + (kg >> 1)) * 64 + (kg & 1) * 32 + m] = values_of(s.k[e], masks, s.kr[e]);
+      to[k_to + e * 128] = values_of(s.k[e], masks, s.kr[e]);
     // Nothing times a value that is not finite would be NaN: it becomes 0, and the rows that see it are told by the flags
     uint32_t some = 0u, bad[T::VG] = {};
 #pragma unroll
@@ -174,26 +184,37 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
         vs[p] = as_half2(x);
         vb[p] = as_half2(y);
       }
-      const int n = vj * KW + e;
-      v[(((vt >> 2) * NC + (n >> 1)) * 2 + ((vt >> 1) & 1)) * 64 + (vt & 1) * 32 + (n & 1) * 16 + vc] = values_of(s.v[e], masks, vs, vb);
+      to[KW % 2 ? v_to(vj * KW + e) : v_to(vj * KW) + v_to(e) - v_to(0)] = values_of(s.v[e], masks, vs, vb);
     }
   };
 
   auto attend = [&](int buffer, int j, uint64_t there, float scale) {
 #pragma clang fp contract(off)  // the largest score less the base is 6, exactly
     const half8_t *const k = operands + buffer * 2 * T::kOperands, *const v = k + T::kOperands;
+    const uint8_t *const f = flags + buffer * T::kFlags;
+    const int flagged = lane < T::kFlags ? f[lane] : 0;
     f32x16 s[SB];
 #pragma unroll
-    for (int n = 0; n < SB; ++n) {
+    for (int n = 0; n < SB; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[n][e] = 0.0f;
+    // Products of the tile's parts in turn, so that none waits for the one before it, and operands four products ahead: left alone, the
+    // compiler reads each operand when its product is due.
 #pragma unroll
-      for (int u = 0; u < 2 * NC; ++u) {
+    for (int u = 0; u < 2 * NC; ++u)
+#pragma unroll
+      for (int n = 0; n < SB; ++n) {
         const half8_t x = k[(n * 2 * NC + u) * 64 + lane];
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) s[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, q[p][u], s[n], 0, 0, 0);
       }
+    __builtin_amdgcn_sched_group_barrier(kSchedRead, 4, 0);
+#pragma unroll
+    for (int i = 0; i < SB * 2 * NC - 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMatrix, PARTS, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 4 * PARTS, 0);
     uint64_t see = ~0ull;
     const uint64_t all = TOKENS == 64 ? ~0ull : 0xFFFFFFFFull;
     const bool whole = there == all && j + TOKENS - 1 <= low && (!a.window || j > high - a.window || j + TOKENS <= a.sinks);
@@ -254,19 +275,27 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
         }
         __builtin_memcpy(&p[0][2 * n + u], high, 16);
         if (WIDE) __builtin_memcpy(&p[PARTS - 1][2 * n + u], low, 16);
-      }
 #pragma unroll
-    for (int n = 0; n < SB; ++n)
+        for (int ct = 0; ct < NC; ++ct) {
+          const half8_t y = v[((n * NC + ct) * 2 + u) * 64 + lane];
 #pragma unroll
-      for (int ct = 0; ct < NC; ++ct)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const half8_t x = v[((n * NC + ct) * 2 + u) * 64 + lane];
-#pragma unroll
-          for (int w = 0; w < PARTS; ++w) o[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, p[w][2 * n + u], o[ct], 0, 0, 0);
+          for (int w = 0; w < PARTS; ++w) o[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y, p[w][2 * n + u], o[ct], 0, 0, 0);
         }
-    const uint8_t *const f = flags + buffer * T::kFlags;
-    if (__builtin_expect(__any(lane < T::kFlags && f[lane < T::kFlags ? lane : 0]), 0)) {
+      }
+    // the next 16 tokens' exponentials and operands between these ones' products
+    constexpr int each = WIDE ? 44 : 24;  // vector instructions of 16 tokens' exponentials
+    __builtin_amdgcn_sched_group_barrier(kSchedRead, NC, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedVector, each, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * SB - 1; ++i)
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, PARTS, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedVector, (each + NC - 1) / NC, 0);
+      }
+    __builtin_amdgcn_sched_group_barrier(kSchedMatrix, NC * PARTS, 0);
+    if (__builtin_expect(__any(flagged), 0)) {
 #pragma unroll
       for (int ct = 0; ct < NC; ++ct) {
         uint64_t bad = 0;
@@ -300,9 +329,11 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
       }
       const bool none = !has_rows || token_now > high ||
                         (a.window && token_now + TOKENS - 1 <= low - a.window && token_now >= a.sinks);  // of its rows
+      // of two waves of a SIMD one dequantises while the other has the matrix cores
+      if (W == 8 && more && wave < 4) put(buffer ^ 1, s);
       if (!none) attend(buffer, token_now, there_now, scale);
       if (!more) break;
-      put(buffer ^ 1, s);
+      if (W != 8 || wave >= 4) put(buffer ^ 1, s);
       __syncthreads();
       ++next;
     }
@@ -344,10 +375,10 @@ __global__ __launch_bounds__(256, WIDE || NC > 4 ? 1 : 2) void k_kv4_prompt(kv4_
     }
 }
 
-template <int NC, int GC, bool WIDE>
+template <int NC, int GC, bool WIDE, int W>
 hipError_t launch_prompt(const kv4_attention_args &a, dim3 grid, hipStream_t s) {
-  typedef prompt<NC, GC, WIDE> T;
-  const auto kernel = k_kv4_prompt<NC, GC, WIDE>;
+  typedef prompt<NC, GC, WIDE, W> T;
+  const auto kernel = k_kv4_prompt<NC, GC, WIDE, W>;
   if (T::kLds > 65536) {  // more than a launch gets unasked; asked for once on each device
     static std::atomic<uint64_t> asked{0};
     const uint64_t bit = a.device < 64 ? 1ull << a.device : 0ull;
@@ -357,7 +388,7 @@ hipError_t launch_prompt(const kv4_attention_args &a, dim3 grid, hipStream_t s) 
       asked.fetch_or(bit, std::memory_order_release);
     }
   }
-  hipLaunchKernelGGL(kernel, grid, dim3(256), T::kLds, s, a);
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * W), T::kLds, s, a);
   return DBS_NOTE(hipGetLastError());
 }
 
@@ -376,7 +407,11 @@ hipError_t launch_few(const kv4_attention_args &a, int tiles, int share, dim3 gr
 template <int NC, int GC>
 hipError_t launch(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s) {
   if constexpr (NC % GC == 0) {
-    if (tiles == 4) return wide ? launch_prompt<NC, GC, true>(a, grid, s) : launch_prompt<NC, GC, false>(a, grid, s);
+    if (tiles >= 4) {
+      if constexpr (NC == 2 || NC == 4)
+        if (tiles == 8) return launch_prompt<NC, GC, false, 8>(a, grid, s);
+      return wide ? launch_prompt<NC, GC, true, 4>(a, grid, s) : launch_prompt<NC, GC, false, 4>(a, grid, s);
+    }
     return wide ? launch_few<NC, GC, true>(a, tiles, share, grid, s) : launch_few<NC, GC, false>(a, tiles, share, grid, s);
   }
   return hipErrorInvalidValue;
