@@ -146,12 +146,13 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
     for (int e = 0; e < KW; ++e)
       to[k_to + e * 128] = values_of(s.k[e], masks, s.kr[e]);
     // Nothing times a value that is not finite would be NaN: it becomes 0, and the rows that see it are told by the flags
-    uint32_t some = 0u, bad[T::VG] = {};
+    uint32_t bad[T::VG] = {};
+    half2_t some = {};
 #pragma unroll
     for (int n = 0; n < T::VG; ++n)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) some |= (s.vr[n][e] & 0x7C007C00u) + 0x04000400u;  // an exponent of ones carries into the sign
-    if (__builtin_expect(__any((some & 0x80008000u) != 0u), 0)) {
+      for (int e = 0; e < 8; ++e) some += as_half2(s.vr[n][e]) * half2_t{};  // NaN if a record is not finite, else nothing
+    if (__builtin_expect(__any(some.x != (_Float16)0.0f || some.y != (_Float16)0.0f), 0)) {
 #pragma unroll
       for (int n = 0; n < T::VG; ++n)
 #pragma unroll
@@ -329,11 +330,9 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
       }
       const bool none = !has_rows || token_now > high ||
                         (a.window && token_now + TOKENS - 1 <= low - a.window && token_now >= a.sinks);  // of its rows
-      // of two waves of a SIMD one dequantises while the other has the matrix cores
-      if (W == 8 && more && wave < 4) put(buffer ^ 1, s);
       if (!none) attend(buffer, token_now, there_now, scale);
       if (!more) break;
-      if (W != 8 || wave >= 4) put(buffer ^ 1, s);
+      put(buffer ^ 1, s);
       __syncthreads();
       ++next;
     }
@@ -408,7 +407,7 @@ template <int NC, int GC>
 hipError_t launch(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s) {
   if constexpr (NC % GC == 0) {
     if (tiles >= 4) {
-      if constexpr (NC == 2 || NC == 4)
+      if constexpr (NC == 4)
         if (tiles == 8) return launch_prompt<NC, GC, false, 8>(a, grid, s);
       return wide ? launch_prompt<NC, GC, true, 4>(a, grid, s) : launch_prompt<NC, GC, false, 4>(a, grid, s);
     }
