@@ -653,7 +653,7 @@ dbs_status dbs_kv4_page_bytes(int32_t key_heads, int32_t head_dim, int32_t group
  * now stands for, rounded to their type (also for what is stored nowhere), so
  * that a prompt's attention can be computed elsewhere from what later steps
  * will read; they may be k and v themselves (same type and strides), else they share no element with them.
- * No page that is written may belong to two sequences of the call.
+ * No page that is written may stand twice in the rows of the table.
  */
 dbs_status dbs_kv4_store(const dbs_kv4_cache *cache, int32_t tokens, const void *k, int64_t k_token_stride,
                          int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
@@ -670,12 +670,13 @@ dbs_status dbs_kv4_store(const dbs_kv4_cache *cache, int32_t tokens, const void 
  * where query head h reads key head h / (heads / key_heads) and the token at position i
  * sees j <= i and, if window > 0, of these j > i - window and j < sinks (a few
  * first tokens that stay visible).  A row that sees nothing is 0, rows of no sequence
- * (new_ptr[sequences] and behind) are left as they are.  What a row does not
- * see takes no part in it, whatever it holds.
+ * (before new_ptr[0], new_ptr[sequences] and behind) are left as they are.  What a row does not
+ * see takes no part in it, whatever it holds.  A row that sees a group of values of which a code would be no finite half
+ * has NaN, or what the formula gives, in that group's channels.
  *
  *   heads      a multiple of key_heads, tokens * heads <= DBS_KV4_MAX_ROWS
  *   q, out     device [tokens][heads][head_dim], free token and head strides, apart
- *   scale      > 0 and finite, usually 1/sqrt(head_dim)
+ *   scale      > 0, finite when multiplied by log2 e, usually 1/sqrt(head_dim)
  *   max_len    the host's bound of lens, or 0: the table's room.  It only tells how the work is cut:
  *              longer sequences are right, and slower
  *   workspace  device, 16-byte aligned, of dbs_kv4_attention_workspace bytes for these arguments; with

@@ -423,8 +423,10 @@ dbs_status dbs_kv4_store(const dbs_kv4_cache *a, int32_t tokens, const void *k, 
     if (dbs_rows_meet(in[1 - s], out[s])) return DBS_ERR_INVALID_ARG;
   }
   if (k_out && v_out && dbs_rows_meet(out[0], out[1])) return DBS_ERR_INVALID_ARG;
-  const dbs_rows lists = {(__int128)(uintptr_t)a->pool, 1, 0, 1, 0, (a->pages - 1) * a->page_stride + 1};
-  if (meets_lists(lists, a)) return DBS_ERR_INVALID_ARG;
+  int64_t bytes = 0;
+  (void)dbs_kv4_page_bytes(a->key_heads, a->head_dim, a->group, a->page_tokens, &bytes);
+  const dbs_rows pool = {(__int128)(uintptr_t)a->pool, 1, 0, 1, 0, (a->pages - 1) * a->page_stride + bytes};
+  if (meets_lists(pool, a)) return DBS_ERR_INVALID_ARG;
   const int padded = kv4_padded(a->head_dim);
   const int64_t units = a->new_ptr ? (int64_t)tokens / 8 + 2 * (int64_t)a->sequences + 1 : ((int64_t)c.each + 6) / 8 * a->sequences + a->sequences;
   const kv4_side ks = {k, kt, kh, k_out, kot, koh}, vs = {v, vt, vh, v_out, vot, voh};
@@ -459,7 +461,8 @@ dbs_status dbs_kv4_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t hea
   bool go;
   const dbs_status st = check_attention(a, tokens, heads, q_dtype, out_dtype, window, sinks, max_len, &c, &go);
   if (st != DBS_OK) return st;
-  if (!(scale > 0.0f) || !isfinite(scale) || workspace_bytes < 0) return DBS_ERR_INVALID_ARG;
+  const float scale2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.0f) || !isfinite(scale2) || workspace_bytes < 0) return DBS_ERR_INVALID_ARG;
   if (!go) return DBS_OK;
   if (!q || !out || (workspace_bytes > 0 && (!workspace || (uintptr_t)workspace % 16))) return DBS_ERR_INVALID_ARG;
   const dbs_rows in = rows_of(q, tokens, qt, heads, qh, a->head_dim, q_dtype), to = rows_of(out, tokens, ot, heads, oh, a->head_dim, out_dtype);
@@ -478,7 +481,8 @@ dbs_status dbs_kv4_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t hea
   int device = -1;
   if (DBS_NOTE(hipGetDevice(&device)) != hipSuccess) return DBS_ERR_DEVICE;
   kv4_attention_args k = {c, device, heads / a->key_heads, a->key_heads, a->head_dim, a->group, q, q_dtype == DBS_BF16, qt, qh, out,
-                          out_dtype == DBS_BF16, ot, oh, scale * 1.4426950408889634f, window, sinks, p.splits, p.chunk, (float *)workspace};
+                          out_dtype == DBS_BF16, ot, oh, scale2, window < DBS_KV4_MAX_CONTEXT ? window : DBS_KV4_MAX_CONTEXT,
+                          sinks < DBS_KV4_MAX_CONTEXT ? sinks : DBS_KV4_MAX_CONTEXT, p.splits, p.chunk, (float *)workspace};
   const int padded = kv4_padded(a->head_dim);
   const auto run = padded == 64 ? kv4_attention_64 : padded == 96 ? kv4_attention_96 : padded == 128 ? kv4_attention_128 :
                    padded == 192 ? kv4_attention_192 : kv4_attention_256;

@@ -55,6 +55,14 @@ DBS_DEV float sum_of(half2_t h, float sum) { return __builtin_amdgcn_fdot2(h, ha
 // Two halves of which either is infinite or NaN.
 DBS_DEV bool not_finite(uint32_t pair) { return (pair & 0x7C00u) == 0x7C00u || (pair & 0x7C000000u) == 0x7C000000u; }
 
+// What a pair of records makes of code 15: finite if and only if scale, offset and the values of all codes are.
+DBS_DEV half2_t last_value(uint32_t s, uint32_t b) {
+  return __builtin_elementwise_fma(as_half2(s), half2_t{(_Float16)15.0f, (_Float16)15.0f}, as_half2(b));
+}
+// x + 0 v: NaN from the first v that is not finite on
+DBS_DEV half2_t or_nan(half2_t x, half2_t v) { return __builtin_elementwise_fma(v, half2_t{}, x); }
+DBS_DEV bool is_nan(half2_t x) { return x.x != x.x || x.y != x.y; }
+
 /*
  * A lane's part of a query on its way: N runs of eight channels from `first` on, `step` apart.  All loads are issued together, from
  * addresses that are there (a run behind the head is the last one again), and nothing is waited for until halves() makes halves of
@@ -266,7 +274,7 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
   }
   const kv4_rows rows = kv4_rows_of(c, b);
   const int all_rows = rows.count * rep, row0 = tile * ROWS;  // DBS_KV4_MAX_ROWS keeps them within 31 bits
-  if (row0 >= all_rows) return;
+  if (tile < 0 || row0 >= all_rows) return;  // rows before the first sequence, or a unit with none
   const int have = min(all_rows - row0, ROWS);
   const int row_waves = have <= 16 * R ? 1 : have <= 32 * R ? 2 : 4;
   const int token_waves = W / row_waves, part = wave % token_waves;
@@ -389,7 +397,7 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
                        (!a.window || j > high - a.window || j + KV4_BLOCK <= a.sinks);
     uint32_t bad[NG], some = 0u;  // the same in all lanes
     if (!whole) {
-      uint32_t wrong = 0u;
+      half2_t wrong = {};
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const uint32_t see = seen(w.position[r], w.position[r]) >> (8 * g);
@@ -402,10 +410,10 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wrong |= (x.vr[n][e] & 0x7C007C00u) + 0x04000400u;  // an exponent of ones carries into the sign
+        for (int e = 0; e < 4; ++e) wrong = or_nan(wrong, last_value(x.vr[n][e], x.vr[n][4 + e]));
       // Nothing times a value that is not finite would be NaN: values that no row sees become 0, and one that is not finite and
       // that some rows see is added to those alone.
-      if (__builtin_expect(__any((wrong & 0x80008000u) != 0u), 0)) {
+      if (__builtin_expect(__any(is_nan(wrong)), 0)) {
         const uint32_t any = seen(high, low);
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
@@ -416,7 +424,7 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
             for (int h = 0; h < 2; ++h) {
               uint32_t &sc = x.vr[n][e], &of = x.vr[n][4 + e];
               const uint32_t bit = 1u << (8 * g + e + 4 * h), half = h ? 0xFFFF0000u : 0x0000FFFFu;
-              if (!not_finite(sc & half) && !not_finite(of & half)) continue;
+              if (!not_finite(as_bits(last_value(sc, of)) & half)) continue;
               mask |= any & bit;
               sc &= ~half;
               of &= ~half;

@@ -65,7 +65,7 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
   }
   const kv4_rows rows = kv4_rows_of(c, b);
   const int all_rows = rows.count * rep, row0 = tile * ROWS;
-  if (row0 >= all_rows) return;
+  if (tile < 0 || row0 >= all_rows) return;  // rows before the first sequence, or a unit with none
 
   const int wave_row = row0 + 32 * wave, row = wave_row + i;
   const bool real = row < all_rows;
@@ -151,8 +151,8 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
 #pragma unroll
     for (int n = 0; n < T::VG; ++n)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) some += as_half2(s.vr[n][e]) * half2_t{};  // NaN if a record is not finite, else nothing
-    if (__builtin_expect(__any(some.x != (_Float16)0.0f || some.y != (_Float16)0.0f), 0)) {
+      for (int e = 0; e < 4; ++e) some = or_nan(some, last_value(s.vr[n][e], s.vr[n][4 + e]));
+    if (__builtin_expect(__any(is_nan(some)), 0)) {
 #pragma unroll
       for (int n = 0; n < T::VG; ++n)
 #pragma unroll
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
 #pragma unroll
           for (int up = 0; up < 2; ++up) {
             const uint32_t part = up ? 0xFFFF0000u : 0x0000FFFFu;
-            if (not_finite(s.vr[n][e] & part) || not_finite(s.vr[n][4 + e] & part)) {
+            if (not_finite(as_bits(last_value(s.vr[n][e], s.vr[n][4 + e])) & part)) {
               s.vr[n][e] &= ~part;
               s.vr[n][4 + e] &= ~part;
               bad[n] |= 1u << (e + 4 * up);

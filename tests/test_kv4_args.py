@@ -62,7 +62,7 @@ BAD_CACHES = [
 
 @pytest.mark.parametrize("bad", BAD_CACHES + [
     dict(heads=3), dict(heads=-2), dict(qd=2), dict(od=-1), dict(q=None), dict(out=None), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf),
-    dict(scale=math.nan), dict(window=-1), dict(sinks=-1), dict(max_len=-1), dict(space_bytes=-1), dict(space_bytes=64), dict(space=P + 4, space_bytes=64),
+    dict(scale=math.nan), dict(scale=3e38), dict(window=-1), dict(sinks=-1), dict(max_len=-1), dict(space_bytes=-1), dict(space_bytes=64), dict(space=P + 4, space_bytes=64),
     dict(oh=63), dict(ot=255), dict(ot=0), dict(out=Q), dict(out=Q + 4 * 700), dict(out=POOL), dict(out=POOL + 4 * page_bytes()[1] - 16), dict(out=LENS),
     dict(out=TABLE + 48), dict(new_ptr=PTR, out=PTR - 4), dict(out=LENS - 4 * 767)])
 def test_attention_refusals(bad):
@@ -72,7 +72,7 @@ def test_attention_refusals(bad):
 @pytest.mark.parametrize("bad", BAD_CACHES + [
     dict(xd=2), dict(od=3), dict(k=None), dict(v=0), dict(k=POOL), dict(v=POOL + 64), dict(koh=63), dict(kot=64), dict(vot=-64), dict(ko=POOL), dict(vo=TABLE),
     dict(ko=LENS), dict(ko=Q, od=1), dict(ko=Q, kot=256), dict(ko=Q + (1 << 20)), dict(vo=OUT), dict(vo=OUT + 4 * 300), dict(lens=POOL + 16),
-    dict(table=POOL), dict(new_ptr=POOL + 4)])
+    dict(table=POOL), dict(new_ptr=POOL + 4), dict(lens=POOL + 4 * page_bytes()[1] - 8)])
 def test_store_refusals(bad):
     if bad.get("v") == 0:
         v = view()
