@@ -300,8 +300,9 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
   kv4_plan p = {};
   const int rep = heads / a->key_heads, d = kv4_padded(a->head_dim), nc = d / 32, gc = a->group / 32;
   const int64_t rows = (int64_t)tokens * rep, each = (rows + a->sequences - 1) / a->sequences;
-  // two tiles a wave of larger heads leave no registers
-  p.tiles = each <= 16 ? 1 : each <= 64 && d <= 128 ? 2 : 4;
+  // Two tiles a wave of larger heads leave no registers; of these, a workgroup takes 64 rows a tile to a wave: 16 x 32 rows of 3000 tokens of
+  // 256 channels 57 us, 98 with the kernel for many rows; 16 x 64 rows 101 and 96.
+  p.tiles = each <= 16 ? 1 : each > 64 ? 4 : d <= 128 ? 2 : 1;
   int64_t slots = (int64_t)a->table_pages * a->page_tokens;
   if (max_len > 0 && max_len < slots) slots = max_len;
   const auto cut = [&](int per) {  // workgroups of `per` rows
@@ -316,16 +317,18 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
     }
     return blocks;
   };
-  if (p.tiles == 4 && d == 128 && !wide) {
-    // Eight waves share a tile's values, four start and end a workgroup sooner, two of them to a compute unit.  Eight where the tokens
-    // are many, the workgroups fill the card, with tokens of like number or twice over, and no more rows are idle.  With 32 heads on 8
-    // of 128 channels, four and eight waves: 256 rows of 8000 tokens 68 and 62 us, 4096 of 4096 188 and 169; 2048 of 2048 63 and 73,
-    // 16 x 512 of 512 80 and 89, 16 x 96 of 2000 65 and 70.  At 64 channels, where three workgroups of four waves fit, 111 and 129.
+  if (p.tiles == 4 && (d == 128 || d == 192) && !wide) {
+    // Eight waves share a tile's values and are all that a compute unit holds; of workgroups of four it holds two at 128 channels, which start
+    // and end sooner, and one at 192.  Eight where they fill the card, as splits of a context that is long beside the rows too; at 128
+    // channels where they do so twice, tokens are many and no more rows are idle.  With 32 heads on 8, four and eight waves: of 128 channels
+    // 256 rows of 8000 tokens 68 and 62 us, 4096 of 4096 188 and 169, but 2048 of 2048 63 and 73, 16 x 512 of 512 80 and 89, 16 x 96 of
+    // 2000 65 and 70; of 192 channels 4096 of 4096 354 and 247, 16 x 512 of 512 170 and 133, but 1024 of 1024 49 and 62.  At 64 channels,
+    // where three workgroups of four fit, 111 and 129.
     cut(256);
     const int64_t eights = p.units * a->key_heads, seen = blocks_of(256);
     const int64_t idle = a->new_ptr ? 64 : (each + 255) / 256 * 256 - (each + 127) / 128 * 128;
-    if (seen >= 48 && idle * 16 <= each && (eights >= 2 * units_of_card || (slots * rep >= 4 * each && eights * (seen / 8) >= units_of_card)))
-      p.tiles = 8;
+    const bool fill = eights >= (d == 128 ? 2 : 1) * units_of_card || (slots * rep >= 4 * each && eights * (seen / 8) >= units_of_card);
+    if (fill && (d == 192 || (seen >= 48 && idle * 16 <= each))) p.tiles = 8;
   }
   const int waves = p.tiles >= 4 ? 2 : kv4_waves(nc, gc, p.tiles, wide);
   p.splits = 1;

@@ -26,7 +26,7 @@ constexpr int kSchedVector = 0x2, kSchedMatrix = 0x8, kSchedRead = 0x100;
 template <int NC, int GC, bool WIDE, int W>
 struct prompt {
   static constexpr int NG = NC / GC, D = 32 * NC, PARTS = WIDE ? 2 : 1;
-  static constexpr int TOKENS = NC <= 4 ? 64 : 32, SB = TOKENS / 32, CUT = W * 16 / TOKENS, KW = NC / CUT;  // words a thread takes of K and of V
+  static constexpr int TOKENS = NC <= 6 || !WIDE ? 64 : 32, SB = TOKENS / 32, CUT = W * 16 / TOKENS, KW = NC / CUT;  // words a thread takes of K and of V
   static constexpr int ROWS = 32 * W;
   static_assert(NC % CUT == 0, "whole words");
   static constexpr int kOperands = SB * 2 * NC * 64;  // of K or of V
@@ -407,7 +407,7 @@ template <int NC, int GC>
 hipError_t launch(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s) {
   if constexpr (NC % GC == 0) {
     if (tiles >= 4) {
-      if constexpr (NC == 4)
+      if constexpr (NC == 4 || NC == 6)
         if (tiles == 8) return launch_prompt<NC, GC, false, 8>(a, grid, s);
       return wide ? launch_prompt<NC, GC, true, 4>(a, grid, s) : launch_prompt<NC, GC, false, 4>(a, grid, s);
     }

@@ -99,15 +99,15 @@ def test_ways_of_cutting_the_work(dbs, dim, group, way):
     check(dbs, rng, lengths, new, heads, rep, dim, group, types=BOTH, many=3 if len(new) > 4 else 12)
 
 
-@pytest.mark.parametrize("group", [32, 64, 128])
-def test_prompts_of_eight_waves(dbs, group):
+@pytest.mark.parametrize("dim,group", [(128, 32), (128, 64), (128, 128), (192, 32), (192, 64), (104, 64), (136, 64)])
+def test_prompts_of_eight_waves(dbs, dim, group):
     """Rows enough for workgroups of 256 of them: beside a long context, cut along it or not, ragged, under a window, from the first token."""
     rng = np.random.default_rng(group)
-    check(dbs, rng, [8200], [512], 2, 4, 128, group, many=40)
-    check(dbs, rng, [3000, 1700, 2500], [1500, 1100, 1300], 2, 4, 128, group, many=20)
-    check(dbs, rng, [6000, 1100, 5001], [1100, 1000, 1201], 2, 4, 128, group, window=2000, sinks=70, many=20)
-    check(dbs, rng, [6000, 1100, 5001], [1100, 1000, 1201], 2, 4, 128, group, window=100, many=20)
-    check(dbs, rng, [1601], [1601], 16, 8, 128, group, many=3)
+    check(dbs, rng, [8200], [512], 2, 4, dim, group, many=40)
+    check(dbs, rng, [3000, 1700, 2500], [1500, 1100, 1300], 2, 4, dim, group, many=20)
+    check(dbs, rng, [6000, 1100, 5001], [1100, 1000, 1201], 2, 4, dim, group, window=2000, sinks=70, many=20)
+    check(dbs, rng, [6000, 1100, 5001], [1100, 1000, 1201], 2, 4, dim, group, window=100, many=20)
+    check(dbs, rng, [1601], [1601], 16, 8, dim, group, many=3)
 
 
 @pytest.mark.parametrize("rep", [17, 33, 64, 65, 80, 129, 200])
