@@ -125,10 +125,10 @@ DBS_DEV void kv4_partial_end(const kv4_attention_args &a, int64_t token, int hea
   ((float2 *)(a.partial + a.splits * rows * d))[blockIdx.y * rows + token * heads + head] = make_float2(base, sum);
 }
 
-// tiles: 16-row tiles of a wave, 4: the kernel for many rows (kv4_prompt.h); share: workgroups that share a compute unit, 0: as many
-// of four waves as fit; wide: q and p in two parts
-hipError_t kv4_attention_64(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
-hipError_t kv4_attention_96(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
-hipError_t kv4_attention_128(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
-hipError_t kv4_attention_192(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
-hipError_t kv4_attention_256(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s);
+// tiles: 16-row tiles of a wave, 4: the kernel for many rows (kv4_prompt.h); 8: that
+// with workgroups of eight waves; share: more than four waves for 16 rows; wide: q and p in two parts
+hipError_t kv4_attention_64(const kv4_attention_args &a, int tiles, bool share, bool wide, dim3 grid, hipStream_t s);
+hipError_t kv4_attention_96(const kv4_attention_args &a, int tiles, bool share, bool wide, dim3 grid, hipStream_t s);
+hipError_t kv4_attention_128(const kv4_attention_args &a, int tiles, bool share, bool wide, dim3 grid, hipStream_t s);
+hipError_t kv4_attention_192(const kv4_attention_args &a, int tiles, bool share, bool wide, dim3 grid, hipStream_t s);
+hipError_t kv4_attention_256(const kv4_attention_args &a, int tiles, bool share, bool wide, dim3 grid, hipStream_t s);

@@ -21,7 +21,11 @@ struct kv4_side {
  * A workgroup takes the new ones of eight tokens that share words of the value codes, one key head after the other: lanes along
  * the channels, eight to a lane, keys in the first half of the workgroup and values in the second; the next head's are on their
  * way meanwhile.  Words of tokens that were there before are read and kept.  Only this workgroup writes these words, so nothing is
- * atomic.  Few tokens have a workgroup for each head, many share the chain of list, length and page among `per` heads.
+ * atomic.  Few tokens have a workgroup for each head, many share the chain of list, length and page among `per` heads (some 8000
+ * tokens of 8 heads of 128 channels 24.6 us with a workgroup a head, 19.5 so).
+ *
+ * Bound by the launch and one chain for the tokens of a step (64 sequences 4.5 us), by memory and the barrier of each head for
+ * prompts: 65 MB in 19.5 us, 3.3 TB/s.
  */
 template <class X, class Y>
 __global__ __launch_bounds__(512) void k_kv4_store(kv4_view c, int heads, int per, int dim, int padded, int group, kv4_side key, kv4_side value) {
@@ -137,7 +141,8 @@ __global__ __launch_bounds__(512) void k_kv4_store(kv4_view c, int heads, int pe
 /*
  * Joins the splits of a row: o = sum_z 2^(m_z - m) o_z / sum_z 2^(m_z - m) l_z.  `lanes` lanes hold a row of four channels each, and
  * `parts` such groups of a workgroup take every parts-th split of it and meet in LDS, in a fixed order: all of a workgroup for one
- * row where rows are few and splits many, one group a row where rows are many.
+ * row where rows are few and splits many, one group a row where rows are many.  A launch and one chain of loads, 2 us, which
+ * an attention of no tokens takes longer with it than without (7 and 5.1 us).
  */
 template <class Y>
 __global__ __launch_bounds__(1024) void k_kv4_combine(kv4_view c, int heads, int dim, int padded, int splits, int lanes, int parts,
@@ -289,9 +294,11 @@ bool meets_pool(const dbs_rows &rows, const dbs_kv4_cache *a) {
   return written_over(rows, a->pool, (a->pages - 1) * a->page_stride + bytes);
 }
 
-// How a call is cut: tiles of 16 rows a wave takes, workgroups along the rows, waves of a workgroup, and splits of the tokens.
+// How a call is cut: tiles of 16 rows a wave takes (4 and 8: waves of 32 rows), workgroups along the rows, splits of the tokens, and whether
+// more than four waves share 16 rows.
 struct kv4_plan {
-  int tiles, share, splits, chunk;
+  int tiles, splits, chunk;
+  bool share;
   int64_t units;
 };
 
@@ -333,12 +340,16 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
   const int waves = p.tiles >= 4 ? 2 : kv4_waves(nc, gc, p.tiles, wide);
   p.splits = 1;
   if (p.tiles == 1 && waves > 1) {
-    // All waves of a compute unit, or of half of one, for a key head's rows: where few blocks leave less to win by splits
-    // than the launch costs that joins them (about three microseconds, of which a compute unit takes 25 blocks of 128 channels).
+    // More waves, for 16 rows of a key head, where four would be split and joined by a second launch: eight of four a SIMD, so that two
+    // workgroups fit, else all of a compute unit, for as many workgroups as the card holds.  With 8 key heads, four waves and more:
+    // of 64 channels 16 sequences of 300 tokens 5.6 and 5.3 us, of 800 9.1 and 7.0, 60 of 500 12.4 and 8.4, one of 1500 8.7 and 9.2; of
+    // 128 channels 32 of 500 11.5 and 8.8, of 1500 17.6 and 14.1, but one of 1500 9.4 and 13.1, 16 of 300 7.0 and 8.1, 60 of 500 10.6 and 16.
     cut(16);
-    const int64_t groups = p.units * a->key_heads;
-    if (groups <= 2 * units_of_card && blocks_of(16) * nc <= 100) {
-      p.share = groups <= units_of_card ? 1 : 2;
+    const int64_t groups = p.units * a->key_heads, blocks = blocks_of(16);
+    const bool half = waves == 4, many = groups * 2 >= units_of_card;
+    if (groups <= (half ? 2 : 1) * units_of_card && blocks >= (half && groups <= units_of_card ? 9 : 16) &&
+        blocks * nc <= (!half && many ? 200 : 100)) {
+      p.share = true;
       return p;
     }
   }

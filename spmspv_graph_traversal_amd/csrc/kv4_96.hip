@@ -1,6 +1,6 @@
 // Attention over the 4-bit cache, heads of up to 96.
 #include "kv4_prompt.h"
 
-hipError_t kv4_attention_96(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s) {
+hipError_t kv4_attention_96(const kv4_attention_args &a, int tiles, bool share, bool wide, dim3 grid, hipStream_t s) {
   return kv4::launch<3>(a, tiles, share, wide, grid, s);
 }

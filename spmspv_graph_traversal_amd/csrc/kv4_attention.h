@@ -152,8 +152,12 @@ struct block {
  * between lanes.  Sums of exponentials stay in each lane until the end.
  *
  * A workgroup's four waves split rows first (R tiles of 16 each) and, where the rows do not need them all, the tokens; further
- * splits of the tokens over workgroups are joined by k_kv4_combine.  Few rows over few tokens are one workgroup's of as many waves
- * as a compute unit holds, W, which all split the tokens.
+ * splits of the tokens over workgroups are joined by k_kv4_combine.  16 rows over few tokens are one workgroup's of W waves, more than four,
+ * which all split the tokens.
+ *
+ * What bounds it: memory where contexts are long, the launch and one chain of length, page, codes, two products and a reduction
+ * where they are short.  With 32 heads of 128 channels on 8: one token of 131072 33.0 us, 143 MB at 4.3 TB/s; 64 sequences of
+ * 1 to 8000 tokens 80.3 us, 374 MB at 4.7 TB/s (a large copy reaches 4.7); one token of 1500 9.6 us, of none 5.1.
  */
 template <int NC, int GC, int R, bool WIDE>
 struct wave_state {
@@ -525,7 +529,7 @@ __global__ __launch_bounds__(64 * W, kv4_waves(NC, GC, R, WIDE)) void k_kv4_atte
     return;
   }
   // the waves that split a row's tokens put theirs into LDS, and join and write a share of the channels each
-  constexpr int HALF = W <= 4 ? NV < 8 ? NV : 8 : W <= 12 ? NV < 4 ? NV : 4 : 2;
+  constexpr int HALF = W <= 4 ? NV < 8 ? NV : 8 : 4;
   __shared__ f32x4 shared[W][HALF][64];
   __shared__ float2 ends[W][64];
   const int first = wave - part;

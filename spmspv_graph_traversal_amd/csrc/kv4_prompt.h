@@ -14,10 +14,18 @@ constexpr int kSchedVector = 0x2, kSchedMatrix = 0x8, kSchedRead = 0x100;
 
 /*
  * The mathematics of k_kv4_attention for the rows of a prompt, where the matrix cores and the exponentials bound it and not
- * the cache.  A workgroup takes 128 rows, 32 a wave, and goes through the tokens in tiles.  It turns the codes of a tile into halves
+ * the cache.  A workgroup takes 32 rows a wave and goes through the tokens in tiles.  It turns the codes of a tile into halves
  * once for all its waves, in LDS, in the order in which the products take them: 16 bytes a lane, so that neither writes nor reads
  * meet in a bank.  The codes of the next tile are on their way meanwhile, in registers, and there are two tiles in LDS, so that a
  * tile costs one barrier.
+ *
+ * What bounds it: a product takes 16 cycles of a SIMD's issue and 32 of its matrix unit, another vector instruction 4 (an
+ * exponential 8).  Of 64 tokens of 128 channels a wave issues 32 products (512 cycles, 1024 of the matrix unit) and, of eight waves, 250
+ * others (1130): 1640 cycles, and takes about 2400, since waves wait for each other's pipe and at the barrier.  One sequence of 8192 tokens with 32 heads of
+ * 128 channels on 8 takes 592 us, 929 TFLOP/s (a large bf16 product reaches 1185 here); operands read four products ahead
+ * and exponentials dealt among the products are 2 to 6 % of it.  Tried and slower: the next tile's values between the score products, and
+ * its scores between this one's exponentials, both for want of registers; halves of the waves in opposite order (628); wave priorities
+ * changed nothing.
  *
  * Products are 32 x 32 x 16: scores K Q^T of 32 tokens by 32 rows, outputs V^T P^T of 32 channels by 32 rows.  Row m of a key
  * operand is token (m with bits 2 and 3 exchanged), so that the lane which gets a row's scores of tokens 16 u + 8 h .. + 7 is the
@@ -26,7 +34,8 @@ constexpr int kSchedVector = 0x2, kSchedMatrix = 0x8, kSchedRead = 0x100;
 template <int NC, int GC, bool WIDE, int W>
 struct prompt {
   static constexpr int NG = NC / GC, D = 32 * NC, PARTS = WIDE ? 2 : 1;
-  static constexpr int TOKENS = NC <= 6 || !WIDE ? 64 : 32, SB = TOKENS / 32, CUT = W * 16 / TOKENS, KW = NC / CUT;  // words a thread takes of K and of V
+  static constexpr int TOKENS = NC <= 6 || !WIDE ? 64 : 32,  // as registers allow; 64 against 32 at 192 channels 571 and 747 us
+                       SB = TOKENS / 32, CUT = W * 16 / TOKENS, KW = NC / CUT;  // words a thread takes of K and of V
   static constexpr int ROWS = 32 * W;
   static_assert(NC % CUT == 0, "whole words");
   static constexpr int kOperands = SB * 2 * NC * 64;  // of K or of V
@@ -200,7 +209,7 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[n][e] = 0.0f;
     // Products of the tile's parts in turn, so that none waits for the one before it, and operands four products ahead: left alone, the
-    // compiler reads each operand when its product is due.
+    // compiler reads each operand when its product is due (8192 tokens 616 -> 606 us, pieces of prompts 152 -> 143).
 #pragma unroll
     for (int u = 0; u < 2 * NC; ++u)
 #pragma unroll
@@ -392,19 +401,17 @@ hipError_t launch_prompt(const kv4_attention_args &a, dim3 grid, hipStream_t s) 
 }
 
 template <int NC, int GC, bool WIDE>
-hipError_t launch_few(const kv4_attention_args &a, int tiles, int share, dim3 grid, hipStream_t s) {
+hipError_t launch_few(const kv4_attention_args &a, int tiles, bool share, dim3 grid, hipStream_t s) {
   constexpr int waves = kv4_waves(NC, GC, 1, WIDE);
   if constexpr (NC <= 4)
     if (tiles == 2) return launch<NC, GC, 2, WIDE>(a, grid, s);
-  if constexpr (waves > 1) {
-    if (share == 1) return launch<NC, GC, 1, WIDE, 4 * waves>(a, grid, s);
-    if (share == 2 && waves > 2) return launch<NC, GC, 1, WIDE, 2 * waves>(a, grid, s);
-  }
+  if constexpr (waves > 1)
+    if (share) return launch<NC, GC, 1, WIDE, waves == 4 ? 8 : 4 * waves>(a, grid, s);
   return launch<NC, GC, 1, WIDE>(a, grid, s);
 }
 
 template <int NC, int GC>
-hipError_t launch(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s) {
+hipError_t launch(const kv4_attention_args &a, int tiles, bool share, bool wide, dim3 grid, hipStream_t s) {
   if constexpr (NC % GC == 0) {
     if (tiles >= 4) {
       if constexpr (NC == 4 || NC == 6)
@@ -417,7 +424,7 @@ hipError_t launch(const kv4_attention_args &a, int tiles, int share, bool wide, 
 }
 
 template <int NC>
-hipError_t launch(const kv4_attention_args &a, int tiles, int share, bool wide, dim3 grid, hipStream_t s) {
+hipError_t launch(const kv4_attention_args &a, int tiles, bool share, bool wide, dim3 grid, hipStream_t s) {
   if (a.group == 32) return launch<NC, 1>(a, tiles, share, wide, grid, s);
   if (a.group == 64) return launch<NC, 2>(a, tiles, share, wide, grid, s);
   return launch<NC, 4>(a, tiles, share, wide, grid, s);

@@ -81,6 +81,8 @@ BOTH = (("bf16", "bf16"), ("f32", "bf16"))
 WAYS = {
     "short": ([300, 1, 33], [1, 1, 1], 2, 3),
     "short of many": ([40, 7, 64, 15] * 75, [1] * 300, 1, 2),
+    "some": ([510, 20], [1, 1], 2, 3),
+    "some of many": ([500, 3, 130, 450] * 10, [1] * 40, 4, 2),
     "long": ([9000, 70], [1, 1], 1, 4),
     "drafts of a long one": ([6000, 90], [3, 3], 1, 4),
     "two tiles": ([1500, 70], [8, 3], 1, 7),
