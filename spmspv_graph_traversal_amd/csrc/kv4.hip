@@ -356,6 +356,7 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
   const int per = p.tiles >= 4 ? 32 * p.tiles : 64 * p.tiles;
   cut(per);
   const int64_t blocks = blocks_of(per), groups = p.units * a->key_heads;
+  int unit = 4;  // a split's blocks are a multiple of it
   int64_t splits = 1;
   if (p.tiles >= 4) {
     // Splits pay where they fill the card's last round better than the joining of their rows costs: rounds of workgroups in units
@@ -372,13 +373,18 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
     // as many workgroups as the card holds at once, of two blocks a wave at least; more of them where sequences may differ in length
     const int64_t once = units_of_card * waves, several = p.units > 1 ? 4 * once : 0;
     splits = once / groups < blocks / 8 ? once / groups : blocks / 8;
+    // down to four blocks while every workgroup has a compute unit to itself, of contexts that are split at all: seven sequences of
+    // 3001 tokens with 35 rows 17.5 us with eight, 15.3 so; but on shared ones seven of 1000 with 36 rows 16.2 and 20.4, and one of 300
+    // with four rows 6.7 in one piece, 8.8 in two
+    const int64_t fine = units_of_card / groups < blocks / 4 ? units_of_card / groups : blocks / 4;
+    if (blocks >= 16 && splits < fine) splits = fine, unit = each <= 16 * p.tiles ? 4 : 2;  // by the waves that split the tokens
     const int64_t more = several / groups < blocks / 40 ? several / groups : blocks / 40;
     if (splits < more) splits = more;
     if (splits > 1024) splits = 1024;
   }
   if (splits < 1) splits = 1;
   p.chunk = (int)((blocks + splits - 1) / splits);
-  p.chunk = (p.chunk + 3) / 4 * 4;
+  p.chunk = (p.chunk + unit - 1) / unit * unit;
   p.splits = blocks > p.chunk ? (int)((blocks + p.chunk - 1) / p.chunk) : 1;
   return p;
 }
