@@ -586,7 +586,10 @@ dbs_status dbs_norm_rope(int32_t tokens, int32_t head_dim, int32_t rot_dim, dbs_
                          dbs_dtype weight_dtype, void *stream);
 
 /* ------------------------------------------------------------------------
- * A paged cache of keys and values in 4 bits, and the attention over it.
+ * A paged cache of keys and values in 4 bits, and the attention over it.  As
+ * above, the calls allocate nothing, run on the current device, may be
+ * captured and give the same bits for the same arguments; what scratch the attention
+ * uses is the caller's workspace.
  *
  * A group (32, 64 or 128 channels of a head of a token; the last one may be
  * cut) is held as codes q, a scale s and an offset b, and stands for
@@ -674,7 +677,8 @@ dbs_status dbs_kv4_store(const dbs_kv4_cache *cache, int32_t tokens, const void 
  * see takes no part in it, whatever it holds.  A row that sees a group of values of which a code would be no finite half
  * has NaN, or what the formula gives, in that group's channels.
  *
- *   heads      a multiple of key_heads, tokens * heads <= DBS_KV4_MAX_ROWS
+ *   heads      a multiple of key_heads, tokens * heads <= DBS_KV4_MAX_ROWS; sequences * key_heads and what
+ *              tokens * heads / 64 adds stay within 2^23, else DBS_ERR_UNSUPPORTED
  *   q, out     device [tokens][heads][head_dim], free token and head strides, apart
  *   scale      > 0, finite when multiplied by log2 e, usually 1/sqrt(head_dim)
  *   max_len    the host's bound of lens, or 0: the table's room.  It only tells how the work is cut:

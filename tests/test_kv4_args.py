@@ -86,6 +86,8 @@ def test_limits_and_nothing_to_do():
     assert attend(sequences=b.DBS_KV4_MAX_SEQUENCES + 1, new_ptr=PTR) == UNSUPPORTED
     assert attend(tokens=3 << 20, heads=8) == UNSUPPORTED
     assert store(tokens=3 << 22, key_heads=2) == UNSUPPORTED
+    many = dict(sequences=1 << 20, tokens=1 << 20, key_heads=16, heads=16, qt=1024, ot=1024, out=16 << 30, table_pages=1, ldtable=1)
+    assert attend(**many) == UNSUPPORTED  # a workgroup a sequence and key head
     for none in (dict(tokens=0), dict(sequences=0, new_ptr=PTR), dict(sequences=0, tokens=0)):
         assert attend(pool=None, table=None, lens=None, q=None, out=None, **none) == OK
         assert store(pool=None, table=None, lens=None, k=None, ko=None, **none) == OK
