@@ -307,8 +307,8 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
   kv4_plan p = {};
   const int rep = heads / a->key_heads, d = kv4_padded(a->head_dim), nc = d / 32, gc = a->group / 32;
   const int64_t rows = (int64_t)tokens * rep, each = (rows + a->sequences - 1) / a->sequences;
-  // Two tiles a wave of larger heads leave no registers; of these, a workgroup takes 64 rows a tile to a wave: 16 x 32 rows of 3000 tokens of
-  // 256 channels 57 us, 98 with the kernel for many rows; 16 x 64 rows 101 and 96.
+  // Up to 64 rows two tiles a wave: 16 x 32 rows of 3000 tokens of 128 channels 24 us, 27 with one tile, 32 with the kernel for many
+  // rows.  Two tiles of larger heads leave no registers; one, and many, of 256 channels 57 and 98 us, of 16 x 64 rows 101 and 96.
   p.tiles = each <= 16 ? 1 : each > 64 ? 4 : d <= 128 ? 2 : 1;
   int64_t slots = (int64_t)a->table_pages * a->page_tokens;
   if (max_len > 0 && max_len < slots) slots = max_len;
