@@ -94,13 +94,14 @@ __global__ __launch_bounds__(512) void k_kv4_store(kv4_view c, int heads, int pe
     uint32_t word = 0u;
     if (in) {
       Y y[8];
-      float stands[8];
+      float stands[8], codes4[2] = {};  // four codes are exact in fp32
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = bad ? 0.0f : fminf(fmaxf(rintf((x[i] - base) * inverse), 0.0f), 15.0f);
-        word |= (uint32_t)q << (4 * i);
+      for (int i = 7; i >= 0; --i) {
+        const float q = __builtin_amdgcn_fmed3f(rintf((x[i] - base) * inverse), 0.0f, 15.0f);
+        codes4[i / 4] = __builtin_fmaf(codes4[i / 4], 16.0f, q);
         stands[i] = (float)(_Float16)__builtin_fmaf(step, q, base);
       }
+      if (!bad) word = (uint32_t)codes4[0] | (uint32_t)codes4[1] << 16;
       dbs_round(y, stands);
       if (to.y) __builtin_memcpy((Y *)to.y + row * to.yt + head * to.yh + channel, y, sizeof y);
     }
