@@ -13,6 +13,12 @@ struct kv4_side {
   int64_t yt, yh;
 };
 
+// another lane's value: by permutation of four lanes or from the other end of 8 or 16, an operand of the instruction that uses it
+template <int HOW>
+DBS_DEV float lane_swap(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), HOW, 0xF, 0xF, true));
+}
+
 /*
  * Mathematics: of a group's values x (32, 64 or 128 channels of a head of a token) b = half(min), s = half((max - b) / 15) and
  * codes rint((x - b) / s) within 0..15, each step in fp32 and with products by reciprocals, so that the codes are
@@ -81,11 +87,13 @@ __global__ __launch_bounds__(512) void k_kv4_store(kv4_view c, int heads, int pe
         bad |= !(fabsf(x[i]) <= DBS_KV4_MAX_VALUE);
       }
     }
-    for (int o = 1; o < group / 8; o <<= 1) {
-      low = fminf(low, __shfl_xor(low, o));
-      high = fmaxf(high, __shfl_xor(high, o));
-      bad |= __shfl_xor((int)bad, o) != 0;
-    }
+    if (bad) high = INFINITY;  // tells the group
+    // across the 4, 8 or 16 lanes of a group, each step leaving the lanes that it joined alike
+    low = fminf(low, lane_swap<0xB1>(low)), high = fmaxf(high, lane_swap<0xB1>(high));  // neighbours
+    low = fminf(low, lane_swap<0x4E>(low)), high = fmaxf(high, lane_swap<0x4E>(high));  // pairs
+    if (group > 32) low = fminf(low, lane_swap<0x141>(low)), high = fmaxf(high, lane_swap<0x141>(high));  // eight lanes backwards
+    if (group > 64) low = fminf(low, lane_swap<0x140>(low)), high = fmaxf(high, lane_swap<0x140>(high));  // sixteen
+    bad = high > DBS_KV4_MAX_VALUE;
     if (low > high) low = high = 0.0f;  // no channel of the head
     _Float16 of = (_Float16)low;
     _Float16 sc = (_Float16)fmaxf((high - (float)of) * (1.0f / 15.0f), 0.0f);
