@@ -83,7 +83,9 @@ struct query {
       for (int n = 0; n < N; ++n) __builtin_memcpy(raw[n], p + min(first + n * step, a.dim - 8), 32);
     }
   }
-  // the scores' scale
+  // The scores' scale.  A product's sum is below 2^39 (256 channels of 2^15 by 2^16), and two that differ do so by 2^-48 or more.  With a
+  // scale of 2^87 scores stay within fp32 and the largest has all the weight, as with any larger scale; with one of 2^-126 all are
+  // nothing beside 1, as with any smaller one, but minus infinity times it is not NaN.
   template <int LANES>
   DBS_DEV float halves(const kv4_attention_args &a, bool real, int first, int step, half8_t (&high)[N], half8_t (&low)[N]) {
     float x[N][8], most = 0.0f;
@@ -116,7 +118,7 @@ struct query {
         high[n][e] = (_Float16)v;
         if (WIDE) low[n][e] = (_Float16)(v - (float)high[n][e]);
       }
-    return ldexpf(a.scale, -up);
+    return __builtin_amdgcn_fmed3f(ldexpf(a.scale, -up), 0x1p-126f, 0x1p87f);
   }
 };
 

@@ -1,0 +1,85 @@
+"""The attention over the cache of 4-bit keys and values at the ends of what q and the scale can be, against 64-bit references, on
+the GPU: in the kernel for few rows and in the one for many, with tokens that some rows do not see in the same block."""
+import math
+
+import numpy as np
+import pytest
+
+import kv4_ref as ref
+from test_gpu_kv4 import cuda, dbs, empty, host, on_gpu, tables  # noqa: F401  (dbs: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+# rows of a sequence: the kernel for few rows with one tile a wave and two, the one for many rows
+ROWS = [5, 30, 130]
+
+
+def run(dbs, c, table, n, q, kind, out_kind, scale, **more):
+    out = empty(q.shape, out_kind)
+    dbs.dbs_kv4_attention(on_gpu(dbs, c), cuda(table), cuda(np.array([n], np.int32)), cuda(q, kind), out, scale=scale, **more)
+    return host(out).astype(np.float64)
+
+
+def one_sequence(seed, n, dim, group, page=64):
+    rng = np.random.default_rng(seed)
+    table, pages = tables(rng, [n], page)
+    c = ref.Cache(pages, 1, dim, group, page)
+    ref.random_bytes(rng, c)
+    return rng, table, c
+
+
+# (largest |q|, scale, head_dim, types): products down to where fp32 ends and behind it
+SMALL = [(2.0 ** -140, None, 128, ("f32", "f32")), (2.0 ** -140, None, 64, ("f32", "bf16")), (2.0 ** -149, None, 256, ("f32", "f32")),
+         (2.0 ** -133, None, 256, ("bf16", "bf16")), (1e-5, 1e-38, 64, ("bf16", "bf16")), (1e-5, 1e-38, 128, ("f32", "f32")),
+         (1.0, 2.0 ** -149, 128, ("bf16", "bf16")), (2.0 ** -126, 2.0 ** -126, 64, ("f32", "f32"))]
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("size,scale,dim,types", SMALL)
+def test_scores_that_are_next_to_nothing(dbs, size, scale, dim, types, rows):
+    """Each row is the mean of what it sees, to fp32: scale q k is below 2^-100 wherever it is."""
+    n = 150
+    rng, table, c = one_sequence(rows + dim, n, dim, 64)
+    q = ref.typed(size * rng.choice([-1.0, -0.5, 0.0, 0.5, 1.0], (rows, 1, dim)), types[0])
+    q[:, 0, 3] = size
+    assert q.max() > 0
+    scale = 1 / math.sqrt(dim) if scale is None else scale
+    got = run(dbs, c, table, n, q, *types, scale)
+    k, v = ref.sequence_values(c, table[0], n)
+    assert scale * size * np.abs(k).sum(-1).max() < 2.0 ** -100
+    for i in range(rows):
+        want, mass, score = ref.attention(q[i, 0].astype(np.float64), k[0], v[0], n - rows + i, scale)
+        tol = ref.attention_tolerance(want, mass, score, dim, n, types[1], "f32" in types)
+        assert (np.abs(got[i, 0] - want) <= tol).all(), f"token {i}"
+
+
+# scores (times log2 e) around 2^26 and above, where fp32 has steps of 8 and more, to where they leave its range
+LARGE = [(2.0 ** p, 1.0) for p in (19, 20, 21, 22, 23, 24, 30, 60, 118)] + [(2.0 ** 12, 2.0 ** 100), (2.0 ** 124, 2.0 ** 124), (1.0, 3e37)]
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("types", [("f32", "f32")])
+@pytest.mark.parametrize("size,scale", LARGE)
+def test_scores_of_any_size_single_out_the_largest(dbs, size, scale, types, rows):
+    """Scores that lie much further apart than they are off: each row is the value of the token with the largest one."""
+    n, dim = 200, 128
+    rng, table, c = one_sequence(rows, n, dim, 128)
+    q = ref.typed(size * rng.normal(0, 1, (rows, 1, dim)), types[0])
+    got = run(dbs, c, table, n, q, *types, scale)
+    k, v = ref.sequence_values(c, table[0], n)
+    sure = 0
+    for i in range(rows):
+        x = q[i, 0].astype(np.float64) * np.float64(np.float32(scale))
+        see = n - rows + i + 1
+        score, of = k[0, :see] @ x, np.abs(k[0, :see]) @ np.abs(x)
+        order = np.argsort(score)
+        # a score is off by dim + 8 roundings of its size, and the bf16 kinds hold q as halves of the row's scale (2^-25 of its largest
+        # element for those that are not exact): far less than the distance asked for, beyond which a weight is below 2^-90
+        apart = score[order[-1]] - score[order[-2]]
+        if apart < 4 * (dim + 8) * 2.0 ** -22 * of.max() + 64:
+            continue
+        sure += 1
+        want = v[0, order[-1]]
+        # one weight, which divides out: three roundings in fp32, and the output's
+        assert (np.abs(got[i, 0] - want) <= (ref.HALF_STEP[types[1]] + 2.0 ** -22) * np.abs(want)).all(), f"token {i}"
+    assert sure >= 0.8 * rows  # of the inputs
