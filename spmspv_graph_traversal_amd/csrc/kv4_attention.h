@@ -110,6 +110,7 @@ struct query {
     }
     for (int o = LANES; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o));
     const int up = most > 0.0f && most < INFINITY ? 14 - ilogbf(most) : 0;
+    if (most == INFINITY) x[0][0] = NAN;  // scores that are all minus infinity have no softmax, and would be those of a row that sees nothing
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll

@@ -83,3 +83,43 @@ def test_scores_of_any_size_single_out_the_largest(dbs, size, scale, types, rows
         # one weight, which divides out: three roundings in fp32, and the output's
         assert (np.abs(got[i, 0] - want) <= (ref.HALF_STEP[types[1]] + 2.0 ** -22) * np.abs(want)).all(), f"token {i}"
     assert sure >= 0.8 * rows  # of the inputs
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32")])
+def test_infinite_queries_make_their_rows_nan(dbs, types, rows):
+    """The difference of two infinite scores is no number.  A row that sees nothing is 0 all the same."""
+    n, dim, heads = 140, 64, 2
+    rng, table, c = one_sequence(rows, n, dim, 32)
+    q = rng.normal(0, 1, (rows, heads, dim)).astype(np.float32)
+    fine = run(dbs, c, table, n, q, *types, 0.125)
+    wrong = q.copy()
+    wrong[1, 0, 9], wrong[2, 1, 40] = np.inf, -np.inf
+    got = run(dbs, c, table, n, wrong, *types, 0.125)
+    assert np.isnan(got[1, 0]).all() and np.isnan(got[2, 1]).all()
+    got[1, 0], got[2, 1] = fine[1, 0], fine[2, 1]
+    np.testing.assert_array_equal(got, fine)
+    empty_table = np.full_like(table, -1)
+    assert (run(dbs, c, empty_table, n, wrong, *types, 0.125) == 0).all()
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_rows_whose_scores_are_all_minus_infinity(dbs, rows, sign):
+    """One infinite element of a bf16 query and keys of one sign in its channel, in one piece and in splits."""
+    n, dim, page = 140, 64, 64
+    rng = np.random.default_rng(rows)
+    table, pages = tables(rng, [n], page, extra=200)
+    c = ref.Cache(pages, 1, dim, 32, page)
+    k = rng.normal(0, 1, (n, 1, dim)).astype(np.float32)
+    k[..., 7] = sign * (1 + np.abs(k[..., 7]))
+    v = rng.normal(0, 1, (n, 1, dim)).astype(np.float32)
+    for t in range(n):
+        stands, _ = c.store(table[0, t // page], t % page, 0, k[t, 0], v[t, 0])
+        assert sign * stands[7] > 0
+    q = ref.typed(rng.normal(0, 1, (rows, 1, dim)), "bf16")
+    q[rows // 2, 0, 7] = -sign * np.inf
+    for max_len in (0, n):
+        got = run(dbs, c, table, n, q, "bf16", "bf16", 0.125, max_len=max_len)
+        assert np.isnan(got[rows // 2, 0]).all()
+        assert np.isfinite(np.delete(got, rows // 2, 0)).all()
