@@ -15,6 +15,7 @@ constexpr float kLow = -3.402823466e38f;  // a maximum before any score
 // Exponentials are 2^(score - base), the base being 6 below the largest score when it was last raised, which is when one is 12 above
 // it: up to 2^12, and 20 bits below the largest one before the half that holds them loses bits.
 constexpr float kBelow = 6.0f, kMost = 12.0f;
+constexpr float kFar = 0x1p24f;  // a base from which on fp32 has steps of 1 and more below it
 
 DBS_DEV half2_t as_half2(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
 DBS_DEV uint32_t as_bits(half2_t h) { return __builtin_bit_cast(uint32_t, h); }
@@ -188,7 +189,7 @@ struct wave_state {
 
   // Scores become exponentials.
   DBS_DEV void soften(f32x4 (&s)[2][R]) {
-#pragma clang fp contract(off)  // the largest score less the base is 6, exactly, where WIDE
+#pragma clang fp contract(off)  // one rounding of a score, for the base as for its exponential: no power passes 2^kMost, however large scores are
     bool raise = false;
     float most[R];
 #pragma unroll
@@ -199,7 +200,7 @@ struct wave_state {
 #pragma unroll
         for (int e = 0; e < 4; ++e) a = fmaxf(a, s[t][r][e]);
       most[r] = a * scale[r];
-      raise |= most[r] > top[r] + kMost;
+      raise |= most[r] - top[r] > kMost;  // exact where they are near; a sum would round
     }
     if (__builtin_expect(__any(raise), 0)) {
 #pragma unroll
@@ -219,10 +220,7 @@ struct wave_state {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = s[t][r][e];
-          s[t][r][e] = __builtin_amdgcn_exp2f(WIDE ? v * scale[r] - top[r] : __builtin_fmaf(v, scale[r], -top[r]));
-        }
+        for (int e = 0; e < 4; ++e) s[t][r][e] = __builtin_amdgcn_exp2f(s[t][r][e] * scale[r] - top[r]);
   }
 
   DBS_DEV void weigh(const block<NC, NG> &b, const code_masks &m, const f32x4 (&s)[2][R]) {

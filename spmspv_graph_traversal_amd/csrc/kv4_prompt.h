@@ -199,7 +199,7 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
   };
 
   auto attend = [&](int buffer, int j, uint64_t there, float scale) {
-#pragma clang fp contract(off)  // the largest score less the base is 6, exactly
+#pragma clang fp contract(off)  // as in soften()
     const half8_t *const k = operands + buffer * 2 * T::kOperands, *const v = k + T::kOperands;
     const uint8_t *const f = flags + buffer * T::kFlags;
     const int flagged = lane < T::kFlags ? f[lane] : 0;
@@ -253,14 +253,26 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
 #pragma unroll
       for (int e = 0; e < 16; ++e) most = fmaxf(most, s[n][e]);
     most *= scale;
-    if (__builtin_expect(__any(most > top + kMost), 0)) {
+    // Product and difference are rounded once, but for bases so far from 0 that a step of fp32 there is a power of two or more: then the product
+    // is rounded by itself, as the largest one's is, or a power would pass a half (all of them so: 8192 rows 621 us against 612, pieces of
+    // prompts 150 against 145).
+    float less = top;
+    if (__builtin_expect(__any(most - top > kMost || (!WIDE && fabsf(top) >= kFar)), 0)) {
       float x = fmaxf(most - kBelow, top);
       x = fmaxf(x, __shfl_xor(x, 32));
       const float f = __builtin_amdgcn_exp2f(top - x);
-      top = x;
+      less = top = x;
       sum *= f;
 #pragma unroll
       for (int n = 0; n < NC; ++n) o[n] *= f;
+      if (!WIDE && __any(fabsf(top) >= kFar)) {
+        const float back = 1.0f / scale;
+#pragma unroll
+        for (int n = 0; n < SB; ++n)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[n][e] = (s[n][e] * scale - top) * back;
+        less = 0.0f;
+      }
     }
     half8_t p[PARTS][2 * SB];
 #pragma unroll
@@ -271,7 +283,7 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float v = s[n][8 * u + e];
-          x[e] = __builtin_amdgcn_exp2f(WIDE ? v * scale - top : __builtin_fmaf(v, scale, -top));
+          x[e] = __builtin_amdgcn_exp2f(WIDE ? v * scale - top : __builtin_fmaf(v, scale, -less));
         }
         half2_t high[4], low[4];
 #pragma unroll

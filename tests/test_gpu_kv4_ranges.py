@@ -58,7 +58,7 @@ LARGE = [(2.0 ** p, 1.0) for p in (19, 20, 21, 22, 23, 24, 30, 60, 118)] + [(2.0
 
 
 @pytest.mark.parametrize("rows", ROWS)
-@pytest.mark.parametrize("types", [("f32", "f32")])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")])
 @pytest.mark.parametrize("size,scale", LARGE)
 def test_scores_of_any_size_single_out_the_largest(dbs, size, scale, types, rows):
     """Scores that lie much further apart than they are off: each row is the value of the token with the largest one."""
