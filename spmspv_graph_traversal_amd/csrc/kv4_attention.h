@@ -50,7 +50,8 @@ DBS_DEV half8_t values_of(uint32_t w, const code_masks &m, uint32_t record) {
   return values_of(w, m, ss, bb);
 }
 
-// sum + h.x + h.y in fp32.  Sums are of the halves that weigh the values, so that their rounding is no error of a row's total.
+// sum + h.x + h.y in fp32.  Sums are of the halves that weigh the values, so that their rounding is no error of a row's total; a
+// block's or tile's apart before they join the total, beside which a small one alone would lose its bits.
 DBS_DEV float sum_of(half2_t h, float sum) { return __builtin_amdgcn_fdot2(h, half2_t{(_Float16)1.0f, (_Float16)1.0f}, sum, false); }
 
 // Two halves of which either is infinite or NaN.
@@ -228,15 +229,17 @@ struct wave_state {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       half2_t h[4], l[4];
+      float of = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         h[e] = half2_t{(_Float16)s[0][r][e], (_Float16)s[1][r][e]};
-        sum[r] = sum_of(h[e], sum[r]);
+        of = sum_of(h[e], of);
         if (WIDE) {
           l[e] = half2_t{(_Float16)(s[0][r][e] - (float)h[e].x), (_Float16)(s[1][r][e] - (float)h[e].y)};
-          sum[r] = sum_of(l[e], sum[r]);
+          of = sum_of(l[e], of);
         }
       }
+      sum[r] += of;
       __builtin_memcpy(&p[0][r], h, 16);
       if (WIDE) __builtin_memcpy(&p[PARTS - 1][r], l, 16);
     }

@@ -275,6 +275,7 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
       }
     }
     half8_t p[PARTS][2 * SB];
+    float of = 0.0f;
 #pragma unroll
     for (int n = 0; n < SB; ++n)
 #pragma unroll
@@ -289,10 +290,10 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           high[e] = half2_t{(_Float16)x[e], (_Float16)x[4 + e]};
-          sum = sum_of(high[e], sum);
+          of = sum_of(high[e], of);
           if (WIDE) {
             low[e] = half2_t{(_Float16)(x[e] - (float)high[e].x), (_Float16)(x[4 + e] - (float)high[e].y)};
-            sum = sum_of(low[e], sum);
+            of = sum_of(low[e], of);
           }
         }
         __builtin_memcpy(&p[0][2 * n + u], high, 16);
@@ -304,6 +305,7 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
           for (int w = 0; w < PARTS; ++w) o[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y, p[w][2 * n + u], o[ct], 0, 0, 0);
         }
       }
+    sum += of;
     // the next 16 tokens' exponentials and operands between these ones' products
     constexpr int each = WIDE ? 44 : 24;  // vector instructions of 16 tokens' exponentials
     __builtin_amdgcn_sched_group_barrier(kSchedRead, NC, 0);

@@ -123,3 +123,41 @@ def test_rows_whose_scores_are_all_minus_infinity(dbs, rows, sign):
         got = run(dbs, c, table, n, q, "bf16", "bf16", 0.125, max_len=max_len)
         assert np.isnan(got[rows // 2, 0]).all()
         assert np.isfinite(np.delete(got, rows // 2, 0)).all()
+
+
+def strong_and_tail(dbs, below, rows, dim, group):
+    """Outputs in fp32 for sequences of one token whose weight is 2^`below` times that of each of some 16000 others, which carry all of the
+    values, in one piece: the channel of those values, got and wanted for each row, and what relative error the exponentials and the sums leave."""
+    import torch
+
+    n, page = 16001, 256
+    rng = np.random.default_rng(dim)
+    table, pages = tables(rng, [n], page)
+    cache = dbs.dbs_kv4_cache(pages, 1, dim, group, page)
+    k = np.zeros((n, 1, dim), np.float32)
+    k[..., 1::group] = 15.0  # every group holds 0 and 15: s = 1, b = 0, and all small integers are themselves
+    v = k.copy()
+    k[0, 0, 5] = 1.0
+    v[1:, 0, 4] = 8.0
+    lens = cuda(np.array([n], np.int32))
+    vo = empty(v.shape, "f32")
+    dbs.dbs_kv4_store(cache, cuda(table), lens, cuda(k), cuda(v), v_out=vo)
+    assert torch.equal(vo, cuda(v))
+    q = np.zeros((rows, 1, dim), np.float32)
+    q[..., 5] = np.float32(below * math.log(2.0))  # the only product that is not 0
+    out = empty(q.shape, "f32")
+    dbs.dbs_kv4_attention(cache, cuda(table), lens, cuda(q), out, scale=1.0, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    got = host(out).astype(np.float64)[:, 0, 4]
+    tail = (n - rows + np.arange(rows)) * math.exp(-float(q[0, 0, 5]))
+    # the exponent: q in two halves, the scale, their product, the difference; the power's own error; sums of two numbers, whose partial
+    # sums have tokens / 32 + 64 roundings on their way (of both signs: all of them one way is the bound)
+    return got, 8 * tail / (1 + tail), below * 4 * 2.0 ** -22 + 2.0 ** -21 + 2 * (n / 32 + 80) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("rows", [3, 100])
+def test_sums_of_many_small_weights_beside_a_large_one(dbs, rows, dim, group):
+    """Weights 1.5 2^-24 of the largest, which halves hold: a pair of them is one and a half steps of a sum that has the largest one in it,
+    and would be rounded to two each time."""
+    got, want, bound = strong_and_tail(dbs, 24 - math.log2(1.5), rows, dim, group)
+    assert (np.abs(got - want) <= bound * want).all(), (np.abs(got - want) / want).max()
