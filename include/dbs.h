@@ -689,7 +689,9 @@ dbs_status dbs_kv4_store(const dbs_kv4_cache *cache, int32_t tokens, const void 
  *
  * Keys and values enter the matrix cores as the halves that the cache stands for, q as a half
  * with its row's largest element below 2^15 and exponentials as halves, of which both are in
- * two parts where q or out is fp32.  Sums, maxima and the output are held in fp32.
+ * two parts where q or out is fp32.  Sums, maxima and the output are held in fp32.  What a weight loses
+ * as halves is at most 2^-11 of it (2^-23 in two parts), or 2^-35 of its row's largest: beside one that is far above
+ * all others, a weight below 2^-35 of it counts as 0.
  */
 dbs_status dbs_kv4_attention_workspace(const dbs_kv4_cache *cache, int32_t tokens, int32_t heads,
                                        dbs_dtype q_dtype, dbs_dtype out_dtype, int32_t window, int32_t sinks,

@@ -12,10 +12,17 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLow = -3.402823466e38f;  // a maximum before any score
-// Exponentials are 2^(score - base), the base being 6 below the largest score when it was last raised, which is when one is 12 above
-// it: up to 2^12, and 20 bits below the largest one before the half that holds them loses bits.
-constexpr float kBelow = 6.0f, kMost = 12.0f;
-constexpr float kFar = 0x1p24f;  // a base from which on fp32 has steps of 1 and more below it
+// Exponentials are 2^(score - base), the base being 10 below the largest score when it was last raised, which is when one is 15 above it: up to
+// 2^15, the largest being 2^10 or more.  Halves lose bits of those below 2^-14 and end at 2^-24: a weight of one half is off by 2^-11 of itself
+// or 2^-35 of the largest, one of two by 2^-23 or 2^-35.
+constexpr float kBelow = 10.0f, kMost = 15.0f;
+constexpr float kFar = 0x1p23f;  // a base from which on fp32 has steps of 1 and more
+
+// The base for a largest score, at least the one before.  Where fp32 has steps of 16, 10 below is 16 below.
+DBS_DEV float raised(float most, float top) {
+  const float below = most - kBelow;
+  return fmaxf(most - below > kMost ? most : below, top);
+}
 
 DBS_DEV half2_t as_half2(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
 DBS_DEV uint32_t as_bits(half2_t h) { return __builtin_bit_cast(uint32_t, h); }
@@ -206,7 +213,7 @@ struct wave_state {
     if (__builtin_expect(__any(raise), 0)) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float a = fmaxf(most[r] - kBelow, top[r]);
+        float a = raised(most[r], top[r]);
         a = fmaxf(a, __shfl_xor(a, 16));
         a = fmaxf(a, __shfl_xor(a, 32));
         const float f = __builtin_amdgcn_exp2f(top[r] - a);

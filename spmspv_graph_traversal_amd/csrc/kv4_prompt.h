@@ -258,7 +258,7 @@ __global__ __launch_bounds__(64 * W, W == 8 || !(WIDE || NC > 4) ? 2 : 1) void k
     // prompts 150 against 145).
     float less = top;
     if (__builtin_expect(__any(most - top > kMost || (!WIDE && fabsf(top) >= kFar)), 0)) {
-      float x = fmaxf(most - kBelow, top);
+      float x = raised(most, top);
       x = fmaxf(x, __shfl_xor(x, 32));
       const float f = __builtin_amdgcn_exp2f(top - x);
       less = top = x;

@@ -161,3 +161,13 @@ def test_sums_of_many_small_weights_beside_a_large_one(dbs, rows, dim, group):
     and would be rounded to two each time."""
     got, want, bound = strong_and_tail(dbs, 24 - math.log2(1.5), rows, dim, group)
     assert (np.abs(got - want) <= bound * want).all(), (np.abs(got - want) / want).max()
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("rows", [3, 100])
+@pytest.mark.parametrize("below", [17.3, 19.3, 21.6])
+def test_a_long_tail_beside_one_strong_token(dbs, below, rows, dim, group):
+    """In fp32 calls a weight is off by 2^-35 of the row's largest at most (half a step of the smaller half's 2^-24, the largest being 2^10 or
+    more), and all of these err alike: 2^(below - 35) of the output."""
+    got, want, bound = strong_and_tail(dbs, below, rows, dim, group)
+    assert (np.abs(got - want) <= (bound + 2.0 ** (below - 35)) * want).all(), (np.abs(got - want) / want).max()
