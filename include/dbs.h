@@ -628,6 +628,8 @@ dbs_status dbs_norm_rope(int32_t tokens, int32_t head_dim, int32_t rot_dim, dbs_
 #define DBS_KV4_MAX_CONTEXT 1073741824
 #define DBS_KV4_MAX_SEQUENCES 1048576
 #define DBS_KV4_MAX_ROWS 16777216
+/* bytes of the attention's workspace at most */
+#define DBS_KV4_MAX_WORKSPACE 536870912
 
 typedef struct {
   void *pool;              /* device, 16-byte aligned */
@@ -683,7 +685,7 @@ dbs_status dbs_kv4_store(const dbs_kv4_cache *cache, int32_t tokens, const void 
  *   scale      > 0, finite when multiplied by log2 e, usually 1/sqrt(head_dim)
  *   max_len    the host's bound of lens, or 0: the table's room.  It only tells how the work is cut:
  *              longer sequences are right, and slower
- *   workspace  device, 16-byte aligned, of dbs_kv4_attention_workspace bytes for these arguments; with
+ *   workspace  device, 16-byte aligned, of dbs_kv4_attention_workspace bytes for these arguments (DBS_KV4_MAX_WORKSPACE at most); with
  *              fewer (NULL and 0 among them) the work is not cut along the tokens, which is slower for long ones and few
  *              rows.  Calls that may overlap in time need workspaces of their own.
  *

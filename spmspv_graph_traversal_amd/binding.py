@@ -36,7 +36,7 @@ DBS_ROPE_PLAIN, DBS_ROPE_LINEAR, DBS_ROPE_BASE, DBS_ROPE_BANDS, DBS_ROPE_RAMP = 
 DBS_Q4_MAX_TOKENS, DBS_Q4_MAX_ROWS, DBS_Q4_MAX_COLUMNS = 524288, 2147483520, 1 << 28
 DBS_LOGITS_MAX_ROWS, DBS_ROPE_MAX_DIM, DBS_ROPE_MAX_ELEMENTS = 65535, 1024, 1 << 30
 DBS_KV4_MAX_VALUE, DBS_KV4_MAX_DIM, DBS_KV4_MAX_CONTEXT = 65024.0, 256, 1 << 30
-DBS_KV4_MAX_SEQUENCES, DBS_KV4_MAX_ROWS = 1 << 20, 1 << 24
+DBS_KV4_MAX_SEQUENCES, DBS_KV4_MAX_ROWS, DBS_KV4_MAX_WORKSPACE = 1 << 20, 1 << 24, 1 << 29
 # exported arrays
 (DBS_ARR_RB_PTR, DBS_ARR_T_CB, DBS_ARR_T_META, DBS_ARR_CB_PTR, DBS_ARR_CSC_RB, DBS_ARR_CSC2CSR,
  DBS_ARR_PAYLOAD, DBS_ARR_SEGMENTS, DBS_ARR_XMASK, DBS_ARR_ACTIVE, DBS_ARR_CSC_CM, DBS_ARR_PAT_SEGS,

@@ -311,6 +311,10 @@ struct kv4_plan {
   int64_t units;
 };
 
+int64_t partial_bytes(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, int splits) {
+  return splits > 1 ? (int64_t)splits * tokens * heads * (kv4_padded(a->head_dim) + 2) * 4 : 0;
+}
+
 kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wide, int32_t window, int32_t sinks, int32_t max_len) {
   constexpr int units_of_card = 256;
   kv4_plan p = {};
@@ -367,12 +371,14 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
   const int64_t blocks = blocks_of(per), groups = p.units * a->key_heads;
   int unit = 4;  // a split's blocks are a multiple of it
   int64_t splits = 1;
+  const int64_t most = DBS_KV4_MAX_WORKSPACE / (partial_bytes(a, tokens, heads, 2) / 2);  // splits that the workspace has room for
   if (p.tiles >= 4) {
     // Splits pay where they fill the card's last round better than the joining of their rows costs: rounds of workgroups in units
-    // of a block's time, 1.3 us, in which joining moves 5 MB.
+    // of a block's time, 1.3 us, in which joining moves 5 MB.  The room is not what sequences have: without a bound on the workspace
+    // tables of a million tokens would ask for gigabytes of it.
     const int64_t at_once = units_of_card * (p.tiles == 8 || wide || d > 128 ? 1 : 2);
     double best = 0.0;
-    for (int64_t s = 1; s <= 64 && s <= (blocks + 7) / 8; ++s) {
+    for (int64_t s = 1; s <= 64 && s <= most && s <= (blocks + 7) / 8; ++s) {
       const int64_t chunk = (blocks + s - 1) / s;
       const double cost = (double)((groups * s + at_once - 1) / at_once) * (chunk + 4) +
                           (s > 1 ? 4.0 + (double)s * tokens * heads * d * 8 / 5e6 : 0.0);
@@ -390,16 +396,13 @@ kv4_plan plan_of(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, bool wid
     const int64_t more = several / groups < blocks / 40 ? several / groups : blocks / 40;
     if (splits < more) splits = more;
     if (splits > 1024) splits = 1024;
+    if (splits > most) splits = most;
   }
   if (splits < 1) splits = 1;
   p.chunk = (int)((blocks + splits - 1) / splits);
   p.chunk = (p.chunk + unit - 1) / unit * unit;
   p.splits = blocks > p.chunk ? (int)((blocks + p.chunk - 1) / p.chunk) : 1;
   return p;
-}
-
-int64_t partial_bytes(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, int splits) {
-  return splits > 1 ? (int64_t)splits * tokens * heads * (kv4_padded(a->head_dim) + 2) * 4 : 0;
 }
 
 dbs_status check_attention(const dbs_kv4_cache *a, int32_t tokens, int32_t heads, int32_t q_dtype, int32_t out_dtype, int32_t window,
