@@ -53,7 +53,7 @@ struct kv4_view {
 };
 
 struct kv4_rows {
-  int sequence, first, count;  // rows [first, first + count)
+  int first, count;  // rows [first, first + count)
   int position;                // of the first one, negative where the cache holds fewer tokens than are new
 };
 
@@ -65,7 +65,6 @@ DBS_DEV int kv4_new_ptr(const kv4_view &c, int b) { return min(max(kv4_list(c.ne
 
 DBS_DEV kv4_rows kv4_rows_of(const kv4_view &c, int b) {
   kv4_rows r;
-  r.sequence = b;
   r.first = c.new_ptr ? kv4_new_ptr(c, b) : b * c.each;
   r.count = c.new_ptr ? max(kv4_new_ptr(c, b + 1) - r.first, 0) : c.each;
   const int most = c.width << c.page_shift;
