@@ -568,7 +568,8 @@ def dbs_kv4_attention(cache: KV4Cache, table, lens, q, out, new_ptr=None, window
     """Attention of the new tokens, stored before, over their sequences: q and out [tokens, heads, head_dim].  A token at
     position i sees tokens j <= i and, with a window, of these j > i - window and j < sinks.  scale: 1/sqrt(head_dim)
     unless given.  max_len bounds lens (0: the table's room); it and the workspace (uint8, allocated for the call
-    unless given) only tell how the work is cut."""
+    unless given) only tell how the work is cut: give the bound where it is far below the room.  Where the allocation
+    fails the call raises torch.OutOfMemoryError; an empty workspace asks for none, and the work is not cut."""
     st = _calls.kv4_attention(cache.pool, cache.key_heads, cache.head_dim, cache.group, cache.page_tokens, table, lens, q, out,
                               new_ptr, window, sinks, scale, max_len, workspace, stream)
     if st:

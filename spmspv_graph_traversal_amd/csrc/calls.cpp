@@ -162,6 +162,11 @@ PyObject *status(F f) {
   try {
     return PyLong_FromLongLong(f());
   } catch (const failed &) {
+  } catch (const c10::OutOfMemoryError &e) {
+    PyObject *const torch = PyImport_ImportModule("torch"), *const type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }
