@@ -572,7 +572,10 @@ typedef struct {
  *   y = w * x / sqrt(mean(x^2) + eps),  then y as dbs_rope's x
  *
  * in fp32 with one rounding to the output's type; the mean is over the
- * head's head_dim elements.  A weight that is held as its distance from 1 is
+ * head's head_dim elements.  A sum of squares past fp32 (elements around 2^63
+ * and above) makes the head's finite elements 0; with eps = 0 the mean has to be
+ * one that fp32 holds (elements around 2^-63 and above), or results are
+ * infinite, and those of zeros NaN.  A weight that is held as its distance from 1 is
  * given as 1 + w.  head_dim <= DBS_ROPE_MAX_DIM, eps >= 0 and finite; a
  * negative position leaves the token's rows as they are.  A part's out may
  * be its x itself; otherwise, and between the parts, outputs share nothing
@@ -684,7 +687,8 @@ dbs_status dbs_kv4_store(const dbs_kv4_cache *cache, int32_t tokens, const void 
  *   q, out     device [tokens][heads][head_dim], free token and head strides, apart
  *   scale      > 0, finite when multiplied by log2 e, usually 1/sqrt(head_dim)
  *   max_len    the host's bound of lens, or 0: the table's room.  It only tells how the work is cut:
- *              longer sequences are right, and slower
+ *              longer sequences are right, and slower, and so are those that are far shorter (one
+ *              token of 1500 in a table of 131072: 19 us, 9.4 with a bound of 1500)
  *   workspace  device, 16-byte aligned, of dbs_kv4_attention_workspace bytes for these arguments (DBS_KV4_MAX_WORKSPACE at most); with
  *              fewer (NULL and 0 among them) the work is not cut along the tokens, which is slower for long ones and few
  *              rows.  Calls that may overlap in time need workspaces of their own.
