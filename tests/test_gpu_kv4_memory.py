@@ -25,12 +25,17 @@ def test_a_workspace_that_cannot_be_allocated(dbs):
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
     limit = torch.cuda.memory_reserved() + size // 2
+    held = []
     try:
         torch.cuda.set_per_process_memory_fraction(limit / torch.cuda.get_device_properties(0).total_memory)
+        with pytest.raises(torch.OutOfMemoryError):  # what is free in segments that cannot be returned
+            while True:
+                held.append(torch.empty(size, dtype=torch.uint8, device="cuda"))
         with pytest.raises(torch.OutOfMemoryError):
             dbs.dbs_kv4_attention(cache, table, lens, q, outs[1])
         dbs.dbs_kv4_attention(cache, table, lens, q, outs[1], workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     finally:
+        del held
         torch.cuda.set_per_process_memory_fraction(1.0)
     dbs.dbs_kv4_attention(cache, table, lens, q, outs[2])
     assert torch.equal(outs[2], outs[0])
