@@ -168,8 +168,9 @@ struct block {
  * which all split the tokens.
  *
  * What bounds it: memory where contexts are long, the launch and one chain of length, page, codes, two products and a reduction
- * where they are short.  With 32 heads of 128 channels on 8: one token of 131072 33.5 us, 143 MB at 4.3 TB/s; 64 sequences of
- * 2000 to 8000 tokens 81 us, 374 MB at 4.6 TB/s (a large copy reaches 4.7); one token of 1500 9.4 us, of none 7 with the joining launch.
+ * where they are short.  With 32 heads of 128 channels on 8: one token of 131072 33.3 us, 143 MB at 4.3 TB/s; 64 sequences of
+ * 2000 to 8000 tokens 81 us, 374 MB at 4.6 TB/s (a large copy reaches 4.7); one token of 1500 9.4 us, of none 7.3 with the joining launch
+ * and 3.3 without.  In fp32, twice the products and conversions: 131072 tokens 41 us, the 64 sequences 91.
  */
 template <int NC, int GC, int R, bool WIDE>
 struct wave_state {

@@ -20,9 +20,9 @@ constexpr int kSchedVector = 0x2, kSchedMatrix = 0x8, kSchedRead = 0x100;
  * tile costs one barrier.
  *
  * What bounds it: a product takes 16 cycles of a SIMD's issue and 32 of its matrix unit, another vector instruction 4 (an
- * exponential 8).  Of 64 tokens of 128 channels a wave issues 32 products (512 cycles, 1024 of the matrix unit) and, of eight waves, 250
- * others (1130): 1640 cycles, and takes about 2400, since waves wait for each other's pipe and at the barrier.  One sequence of
- * 8192 tokens with 32 heads of 128 channels on 8 takes 592 to 613 us, some 900 TFLOP/s (a large bf16 product reaches 1185 here).
+ * exponential 8).  Of 64 tokens of 128 channels a wave issues 32 products (512 cycles, 1024 of the matrix unit) and, of eight waves, 260
+ * others (1180): 1690 cycles, and takes about 2400, since waves wait for each other's pipe and at the barrier.  One sequence of
+ * 8192 tokens with 32 heads of 128 channels on 8 takes 607 to 632 us, 870 to 906 TFLOP/s (a large bf16 product reaches 1185 here).
  * Operands read four products ahead and exponentials dealt among the products are 2 to 6 % of it.  Slower: the next tile's values
  * between the score products (708 us, 649 then), halves of the waves in opposite order (628, 604 then).  The next tile's scores between
  * this one's exponentials spill, and wave priorities change nothing.
